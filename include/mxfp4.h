@@ -123,6 +123,38 @@ MXFP4_API size_t mxfp4_gemm_workspace_size(int64_t M, int64_t K, int64_t N, mxfp
  * least 2^62, or the mode is unknown.  No counterpart in the pages: the launch policy of the GEMMs above. */
 MXFP4_API int32_t mxfp4_token_tile_rows(int64_t rows, int64_t groups, mxfp4_mode mode);
 
+/* ---------------------------------------------------------------- linear layer
+ * y [M, n_out] bf16 = act( x [M, K] bf16 . dequant(W)^T + bias ) + residual, W = MXFP4
+ * codes [N, K/2] + scales [N, K/32] (W4A16); the sum, bias, activation and residual are
+ * taken in fp32 and rounded once, to y.
+ *   act     z -> NONE z, RELU max(z, 0), SILU z / (1 + e^-z), GELU z (1 + erf(z / sqrt 2)) / 2,
+ *           GELU_TANH z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2;
+ *           SWIGLU SiLU(z_g) * z_u with W rows [0, N/2) gate and [N/2, N) up (N even);
+ *   n_out   N, or N / 2 with SWIGLU;
+ *   bias    [N] in bf16 or fp32 per `bias_dt`, or NULL;
+ *   residual bf16 [M, n_out], or NULL; it may be y itself (the sum in place).
+ * Inf and NaN in x, in a block scale (0xFF), bias or residual spread as in the formula.
+ * A weight is its code times 2^(S-127); where that is past bf16's range (S > 252) it may
+ * enter the product as Inf or as the exact value.
+ * Requires K % 32 == 0, K <= 2^20, M < 2^31, N < 2^31 and M * n_out < 2^46; any M >= 1, N >= 1.  ws:
+ * mxfp4_linear_workspace_size() bytes (none for small M).
+ * Source: agentlenshq.com, "Transformers 4.40 performance upgrades for OpenAI GPT-OSS ...",
+ * section "MXFP4 4-Bit Quantization" (MXFP4 weights multiplied without a bf16 copy of the
+ * model); the epilogue is this library's. */
+typedef enum {
+    MXFP4_ACT_NONE = 0,
+    MXFP4_ACT_RELU = 1,
+    MXFP4_ACT_SILU = 2,
+    MXFP4_ACT_GELU = 3,
+    MXFP4_ACT_GELU_TANH = 4,
+    MXFP4_ACT_SWIGLU = 5
+} mxfp4_act;
+MXFP4_API mxfp4_status mxfp4_linear(const void* x_bf16, int64_t M, int64_t K, const uint8_t* w_codes,
+                                    const uint8_t* w_scales, int64_t N, const void* bias,
+                                    mxfp4_in_dtype bias_dt, mxfp4_act act, const void* residual_bf16,
+                                    void* y_bf16, void* ws, size_t ws_bytes, void* stream);
+MXFP4_API size_t mxfp4_linear_workspace_size(int64_t M, int64_t K, int64_t N, mxfp4_act act);
+
 /* ---------------------------------------------------------------- routing
  * Per token t of router logits [T, E] fp32: the top_k experts ordered by
  * (logit descending, expert id ascending) -> ids int32 [T, top_k]; softmax over
@@ -162,6 +194,38 @@ MXFP4_API mxfp4_status moe_mxfp4_route_project(const void* x_bf16, int64_t T, in
                                                void* stream);
 /* Scratch bytes moe_mxfp4_route needs in `ws` (per-chunk counts and ranks). */
 MXFP4_API size_t moe_mxfp4_route_workspace_size(int64_t T, int64_t E, int32_t top_k);
+
+/* ---------------------------------------------------------------- routing with scores
+ * The routing of models that score experts otherwise than moe_mxfp4_route does.  Per
+ * token of router logits l [E] (fp32 or bf16 per `dt`):
+ *   score    SIGMOID s_e = 1 / (1 + e^-l_e); SOFTMAX s_e = e^l_e / sum over all E of e^l;
+ *   choice   c_e = s_e + bias_e (bias fp32 [E] or NULL), compared as in 64-bit arithmetic; without
+ *            bias and sums of scores the order of the logits themselves;
+ *   groups   n_groups groups of E / n_groups consecutive experts; a group's value is its
+ *            largest c (group_top = 1) or the sum of its two largest (2; those at -inf are
+ *            left out); the top_groups groups by (value desc, index asc) are kept;
+ *   ids      the top_k experts of the kept groups by (c desc, id asc);
+ *   weights  s of the chosen experts (without bias); renorm != 0: divided by their sum;
+ *            times `scale`.
+ * A logit of -inf masks its expert: s = 0, c = -inf, and it is chosen only where the kept
+ * groups have nothing better; a score below the smallest 64-bit number is 0, and a token
+ * whose chosen scores are all 0 gets weights 0.  A NaN
+ * logit takes no part in the softmax of the others, and its c (like a NaN bias's) ranks below -inf;
+ * a token that has to choose a NaN logit gets NaN there (with renorm in all its slots).
+ * ids, counts, offsets, perm, inv as moe_mxfp4_route (pairs p = t * top_k + j).
+ * Requires 1 <= top_k <= 8, E <= 256, n_groups <= 32, E % n_groups == 0, group_top 1 or 2
+ * and at most E / n_groups, 1 <= top_groups <= n_groups, top_k <= top_groups * E /
+ * n_groups, a finite scale, T * top_k < 2^31.  ws: moe_mxfp4_route_scored_workspace_size() bytes.
+ * Source: as moe_mxfp4_route; the scores, bias and groups are readings of routers that
+ * the pages do not print. */
+typedef enum { MXFP4_SCORE_SOFTMAX = 0, MXFP4_SCORE_SIGMOID = 1 } mxfp4_score;
+MXFP4_API mxfp4_status moe_mxfp4_route_scored(const void* router_logits, mxfp4_in_dtype dt, int64_t T, int64_t E,
+                                              int32_t top_k, mxfp4_score score, const float* bias,
+                                              int32_t n_groups, int32_t top_groups, int32_t group_top,
+                                              int32_t renorm, float scale, int32_t* ids, float* weights,
+                                              int32_t* counts, int32_t* offsets, int32_t* perm, int32_t* inv,
+                                              void* ws, size_t ws_bytes, void* stream);
+MXFP4_API size_t moe_mxfp4_route_scored_workspace_size(int64_t T, int64_t E, int32_t top_k);
 
 /* ---------------------------------------------------------------- MoE expert MLP
  * gpt-oss-style MoE expert MLP with MXFP4 expert weights, one layer:

@@ -19,7 +19,8 @@ import ctypes
 import torch
 
 from . import _lib
-from ._lib import (Mxfp4Error, Mxfp4LibraryMissing, SCALE_CEIL, SCALE_FLOOR, W4A4, W4A16)
+from ._lib import (ACT_GELU, ACT_GELU_TANH, ACT_NONE, ACT_RELU, ACT_SILU, ACT_SWIGLU, Mxfp4Error,
+                   Mxfp4LibraryMissing, SCALE_CEIL, SCALE_FLOOR, SCORE_SIGMOID, SCORE_SOFTMAX, W4A4, W4A16)
 
 __all__ = [
     "mxfp4_quantize", "mxfp4_dequantize", "mxfp4_gemm", "mxfp4_gemm_workspace_size",
@@ -29,6 +30,9 @@ __all__ = [
     "mxfp4_selftest_wait_timeout", "mxfp4_selftest_mma_rate", "mxfp4_set_trace_events",
     "moe_mxfp4_route_project", "mxfp4_gather_rows", "moe_mxfp4_experts",
     "moe_mxfp4_experts_workspace_size", "moe_mxfp4_combine", "moe_bf16_mlp", "moe_bf16_workspace_size",
+    "mxfp4_linear", "mxfp4_linear_workspace_size", "moe_mxfp4_route_scored",
+    "moe_mxfp4_route_scored_workspace_size", "SCORE_SOFTMAX", "SCORE_SIGMOID",
+    "ACT_NONE", "ACT_RELU", "ACT_SILU", "ACT_GELU", "ACT_GELU_TANH", "ACT_SWIGLU",
     "Mxfp4Error", "Mxfp4LibraryMissing",
     "SCALE_FLOOR", "SCALE_CEIL", "W4A16", "W4A4", "library_path",
 ]
@@ -161,6 +165,62 @@ def mxfp4_gemm(x: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Tensor, m
     return out
 
 
+def _used_on(stream, *tensors):
+    """Tell the allocator that `stream`, if the caller gave one, uses these tensors: those
+    allocated here belong to the current stream's pool and must not be reused before."""
+    if stream is not None and stream != torch.cuda.current_stream():
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+
+
+def mxfp4_linear_workspace_size(M, K, N, act=ACT_NONE) -> int:
+    return int(_lib.load().mxfp4_linear_workspace_size(M, K, N, int(act)))
+
+
+def mxfp4_linear(x: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Tensor, bias=None, act: int = ACT_NONE,
+                 residual=None, out=None, ws=None, stream=None):
+    """y bf16 [M, n_out] = act(x bf16 [M, K] . dequant(W)^T + bias) + residual (W4A16), W codes
+    [N, K/2] + scales [N, K/32]; bias bf16 or fp32 [N]; n_out = N, or N / 2 with ACT_SWIGLU
+    (W rows [0, N/2) gate, [N/2, N) up); residual bf16 [M, n_out], which may be `out`."""
+    _need_dims(x, "x", 2)
+    _need_dims(w_codes, "w_codes", 2)
+    M, K = x.shape
+    N = w_codes.shape[0]
+    act = int(act)
+    if act == ACT_SWIGLU and N % 2:
+        raise ValueError(f"w_codes: the gated activation needs an even number of rows, got {N}")
+    n_out = N // 2 if act == ACT_SWIGLU else N
+    _need(x, "x", torch.bfloat16)
+    _need(w_codes, "w_codes", torch.uint8, (N, K // 2))
+    _need(w_scales, "w_scales", torch.uint8, (N, K // 32))
+    if bias is not None:
+        _need(bias, "bias", None, (N,))
+        if bias.dtype not in (torch.bfloat16, torch.float32):
+            raise ValueError(f"bias: expected dtype bf16 or fp32, got {bias.dtype}")
+    if residual is not None:
+        _need(residual, "residual", torch.bfloat16, (M, n_out))
+    if out is not None:
+        _need(out, "out", torch.bfloat16, (M, n_out))
+    if ws is not None:
+        _need(ws, "ws")
+    _on_current_device(x=x, w_codes=w_codes, w_scales=w_scales, bias=bias, residual=residual, out=out, ws=ws)
+    lib = _lib.load()
+    new_out = new_ws = None
+    if out is None:
+        out = new_out = _empty((M, n_out), torch.bfloat16, x)
+    if ws is None:
+        need = int(lib.mxfp4_linear_workspace_size(M, K, N, act))
+        if need:
+            ws = new_ws = _empty((need,), torch.uint8, x)
+    nbytes = 0 if ws is None else ws.numel() * ws.element_size()
+    bias_dt = _lib.IN_F32 if bias is not None and bias.dtype == torch.float32 else _lib.IN_BF16
+    _lib.check("mxfp4_linear", lib.mxfp4_linear(_p(x), M, K, _p(w_codes), _p(w_scales), N, _p(bias), bias_dt, act,
+                                                _p(residual), _p(out), _p(ws), nbytes, _stream(stream)))
+    _used_on(stream, new_out, new_ws)
+    return out
+
+
 def moe_mxfp4_route_workspace_size(T, E, top_k) -> int:
     return int(_lib.load().moe_mxfp4_route_workspace_size(T, E, top_k))
 
@@ -223,6 +283,54 @@ def moe_mxfp4_route_project(x: torch.Tensor, w_router: torch.Tensor, top_k: int,
         _p(x), T, H, _p(w_router), E, top_k, _p(out["ids"]), _p(out["weights"]), _p(out["counts"]),
         _p(out["offsets"]), _p(out["perm"]), _p(out["inv"]), _p(out["logits"]) if logits_out else None,
         _p(ws), ws.numel() * ws.element_size(), _stream(stream)))
+    return out
+
+
+def moe_mxfp4_route_scored_workspace_size(T, E, top_k) -> int:
+    return int(_lib.load().moe_mxfp4_route_scored_workspace_size(T, E, top_k))
+
+
+def moe_mxfp4_route_scored(logits: torch.Tensor, top_k: int, score: int = SCORE_SOFTMAX, bias=None,
+                           n_groups: int = 1, top_groups: int = 1, group_top: int = 1, renorm: bool = True,
+                           scale: float = 1.0, ws=None, stream=None):
+    """Routing with softmax-over-all or sigmoid scores (see include/mxfp4.h): logits fp32 or
+    bf16 [T, E]; bias fp32 [E] is added to the scores for the choice only; of n_groups groups
+    the top_groups by their group_top largest choice values are kept; weights are the chosen
+    experts' scores, renormalised to their sum if `renorm`, times `scale`.  Returns the dict
+    of ``moe_mxfp4_route``."""
+    _need_dims(logits, "logits", 2)
+    dt = {torch.bfloat16: _lib.IN_BF16, torch.float32: _lib.IN_F32}.get(logits.dtype)
+    if dt is None:
+        raise ValueError(f"logits: expected dtype bf16 or fp32, got {logits.dtype}")
+    _need(logits, "logits")
+    T, E = logits.shape
+    if bias is not None:
+        _need(bias, "bias", torch.float32, (E,))
+    if ws is not None:
+        _need(ws, "ws")
+    _on_current_device(logits=logits, bias=bias, ws=ws)
+    lib = _lib.load()
+    top_k = int(top_k)
+    if top_k < 1:
+        raise ValueError(f"top_k: expected at least 1, got {top_k}")
+    P = T * top_k
+    out = dict(ids=_empty((T, top_k), torch.int32, logits),
+               weights=_empty((T, top_k), torch.float32, logits),
+               counts=_empty((E,), torch.int32, logits),
+               offsets=_empty((E + 1,), torch.int32, logits),
+               perm=_empty((P,), torch.int32, logits),
+               inv=_empty((P,), torch.int32, logits))
+    new_ws = None
+    if ws is None:
+        need = int(lib.moe_mxfp4_route_scored_workspace_size(T, E, top_k))
+        if need:
+            ws = new_ws = _empty((need,), torch.uint8, logits)
+    nbytes = 0 if ws is None else ws.numel() * ws.element_size()
+    _lib.check("moe_mxfp4_route_scored", lib.moe_mxfp4_route_scored(
+        _p(logits), dt, T, E, top_k, int(score), _p(bias), int(n_groups), int(top_groups), int(group_top),
+        int(bool(renorm)), float(scale), _p(out["ids"]), _p(out["weights"]), _p(out["counts"]), _p(out["offsets"]),
+        _p(out["perm"]), _p(out["inv"]), _p(ws), nbytes, _stream(stream)))
+    _used_on(stream, new_ws, *out.values())
     return out
 
 

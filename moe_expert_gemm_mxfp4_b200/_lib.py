@@ -29,6 +29,8 @@ IN_BF16, IN_F32 = 0, 1
 NOALLOC_SCRATCH_BYTES = 16 << 20   # MXFP4_NOALLOC_SCRATCH_BYTES in include/mxfp4.h
 SCALE_FLOOR, SCALE_CEIL = 0, 1
 W4A16, W4A4 = 0, 1
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
+ACT_NONE, ACT_RELU, ACT_SILU, ACT_GELU, ACT_GELU_TANH, ACT_SWIGLU = range(6)
 
 
 class Mxfp4LibraryMissing(RuntimeError):
@@ -46,6 +48,7 @@ class Mxfp4Error(RuntimeError):
 _LIB = None
 
 _i64, _i32, _sz, _vp = ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t, ctypes.c_void_p
+_f32 = ctypes.c_float
 _SIGS = {
     "mxfp4_quantize": (ctypes.c_int, [_vp, ctypes.c_int, _i64, _i64, _vp, _vp, ctypes.c_int, _vp]),
     "mxfp4_dequantize": (ctypes.c_int, [_vp, _vp, _i64, _i64, _vp, _vp]),
@@ -56,6 +59,12 @@ _SIGS = {
     "moe_mxfp4_route_workspace_size": (_sz, [_i64, _i64, _i32]),
     "moe_mxfp4_route_project": (ctypes.c_int, [_vp, _i64, _i64, _vp, _i64, _i32, _vp, _vp, _vp, _vp, _vp, _vp,
                                                _vp, _vp, _sz, _vp]),
+    "mxfp4_linear": (ctypes.c_int, [_vp, _i64, _i64, _vp, _vp, _i64, _vp, ctypes.c_int, ctypes.c_int, _vp, _vp,
+                                    _vp, _sz, _vp]),
+    "mxfp4_linear_workspace_size": (_sz, [_i64, _i64, _i64, ctypes.c_int]),
+    "moe_mxfp4_route_scored": (ctypes.c_int, [_vp, ctypes.c_int, _i64, _i64, _i32, ctypes.c_int, _vp, _i32, _i32,
+                                              _i32, _i32, _f32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "moe_mxfp4_route_scored_workspace_size": (_sz, [_i64, _i64, _i32]),
     "moe_mxfp4_mlp": (ctypes.c_int, [_vp, _i64, _i64, _vp, _i64, _i32, _vp, _vp, _i64, _vp, _vp, _vp,
                                      ctypes.c_int, _vp, _sz, _vp]),
     "moe_mxfp4_workspace_size": (_sz, [_i64, _i64, _i64, _i64, _i32, ctypes.c_int]),

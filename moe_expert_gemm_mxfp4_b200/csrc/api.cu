@@ -504,6 +504,51 @@ mxfp4_status mxfp4_gemm(const void* x_bf16, int64_t M, int64_t K, const uint8_t*
     return e == cudaSuccess ? MXFP4_OK : cuda_fail(e);
 }
 
+size_t mxfp4_linear_workspace_size(int64_t M, int64_t K, int64_t N, mxfp4_act act) {
+    (void)M, (void)K, (void)N, (void)act;
+    return 0;
+}
+
+mxfp4_status mxfp4_linear(const void* x_bf16, int64_t M, int64_t K, const uint8_t* w_codes,
+                          const uint8_t* w_scales, int64_t N, const void* bias, mxfp4_in_dtype bias_dt,
+                          mxfp4_act act, const void* residual_bf16, void* y_bf16, void* ws, size_t ws_bytes,
+                          void* stream) {
+    if (!x_bf16 || !w_codes || !w_scales || !y_bf16) return MXFP4_ERR_INVALID_ARG;
+    if (M <= 0 || K <= 0 || N <= 0) return MXFP4_ERR_INVALID_ARG;
+    if (bias && bias_dt != MXFP4_IN_BF16 && bias_dt != MXFP4_IN_F32) return MXFP4_ERR_INVALID_ARG;
+    if (act < MXFP4_ACT_NONE || act > MXFP4_ACT_SWIGLU) return MXFP4_ERR_INVALID_ARG;
+    const int64_t lim = int64_t{1} << 31;
+    if (K % 32 != 0 || K > (1 << 20) || M >= lim || N >= lim) return MXFP4_ERR_UNSUPPORTED_SHAPE;
+    if (act == MXFP4_ACT_SWIGLU && N % 2 != 0) return MXFP4_ERR_UNSUPPORTED_SHAPE;
+    const int64_t n_out = act == MXFP4_ACT_SWIGLU ? N / 2 : N;
+    if (M > (int64_t{1} << 46) / n_out) return MXFP4_ERR_UNSUPPORTED_SHAPE;
+    if (!aligned16(x_bf16) || !aligned16(w_codes) || !aligned16(w_scales) || !aligned16(y_bf16) ||
+        (bias && !aligned16(bias)) || (residual_bf16 && !aligned16(residual_bf16)))
+        return MXFP4_ERR_MISALIGNED;
+    const size_t need = mxfp4_linear_workspace_size(M, K, N, act);
+    if (need > 0 && (!ws || ws_bytes < need)) return MXFP4_ERR_WORKSPACE;
+    if (ws && !aligned16(ws)) return MXFP4_ERR_MISALIGNED;
+    DeviceInfo* d = nullptr;
+    mxfp4_status st = device_info(&d);
+    if (st != MXFP4_OK) return st;
+    mx::LinearArgs a{};
+    a.x = x_bf16;
+    a.codes = w_codes;
+    a.scales = w_scales;
+    a.bias = bias;
+    a.residual = residual_bf16;
+    a.y = y_bf16;
+    a.M = M;
+    a.K = K;
+    a.N = N;
+    a.n_out = n_out;
+    a.bias_f32 = bias_dt == MXFP4_IN_F32;
+    a.act = static_cast<int>(act);
+    a.status = d->status;
+    cudaError_t e = mx::launch_linear(a, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? MXFP4_OK : cuda_fail(e);
+}
+
 static mxfp4_status check_route_args(const float* logits, int64_t T, int64_t E, int32_t top_k) {
     if (!logits) return MXFP4_ERR_INVALID_ARG;
     if (T <= 0 || E <= 0 || top_k <= 0) return MXFP4_ERR_INVALID_ARG;
@@ -571,6 +616,59 @@ mxfp4_status moe_mxfp4_route_project(const void* x_bf16, int64_t T, int64_t H, c
     if (e != cudaSuccess) return cuda_fail(e);
     e = mx::launch_route_finish(T, E, top_k, ids, weights, counts, offsets, perm, inv, nullptr, nullptr,
                                 ws, nullptr, 0, nullptr, nullptr, 0, nullptr, d->sm_count, s);
+    return e == cudaSuccess ? MXFP4_OK : cuda_fail(e);
+}
+
+size_t moe_mxfp4_route_scored_workspace_size(int64_t T, int64_t E, int32_t top_k) {
+    if (T <= 0 || E <= 0 || top_k <= 0) return 0;
+    return align_up(mx::route_scored_ws_bytes(T, E), 256);
+}
+
+mxfp4_status moe_mxfp4_route_scored(const void* router_logits, mxfp4_in_dtype dt, int64_t T, int64_t E,
+                                    int32_t top_k, mxfp4_score score, const float* bias, int32_t n_groups,
+                                    int32_t top_groups, int32_t group_top, int32_t renorm, float scale,
+                                    int32_t* ids, float* weights, int32_t* counts, int32_t* offsets,
+                                    int32_t* perm, int32_t* inv, void* ws, size_t ws_bytes, void* stream) {
+    if (!router_logits || !ids || !weights || !counts || !offsets || !perm || !inv) return MXFP4_ERR_INVALID_ARG;
+    if (T <= 0 || E <= 0 || top_k <= 0 || n_groups <= 0 || top_groups <= 0) return MXFP4_ERR_INVALID_ARG;
+    if (dt != MXFP4_IN_BF16 && dt != MXFP4_IN_F32) return MXFP4_ERR_INVALID_ARG;
+    if (score != MXFP4_SCORE_SOFTMAX && score != MXFP4_SCORE_SIGMOID) return MXFP4_ERR_INVALID_ARG;
+    if (group_top != 1 && group_top != 2) return MXFP4_ERR_INVALID_ARG;
+    if (!(scale - scale == 0.f)) return MXFP4_ERR_INVALID_ARG;   // Inf or NaN
+    if (E > 256 || top_k > 8 || top_k > E || n_groups > 32 || E % n_groups != 0 || top_groups > n_groups ||
+        group_top > E / n_groups || top_k > top_groups * (E / n_groups))
+        return MXFP4_ERR_UNSUPPORTED_SHAPE;
+    if (T >= (int64_t{1} << 31) || T * top_k >= (int64_t{1} << 31)) return MXFP4_ERR_UNSUPPORTED_SHAPE;
+    if (!aligned16(router_logits) || (bias && !aligned16(bias)) || !aligned16(ids) || !aligned16(weights) ||
+        !aligned16(counts) || !aligned16(offsets) || !aligned16(perm) || !aligned16(inv))
+        return MXFP4_ERR_MISALIGNED;
+    const size_t need = moe_mxfp4_route_scored_workspace_size(T, E, top_k);
+    if (need > 0 && (!ws || ws_bytes < need)) return MXFP4_ERR_WORKSPACE;
+    if (ws && !aligned16(ws)) return MXFP4_ERR_MISALIGNED;
+    DeviceInfo* d = nullptr;
+    mxfp4_status st = device_info(&d);
+    if (st != MXFP4_OK) return st;
+    mx::RouteScoredArgs a{};
+    a.logits = router_logits;
+    a.bias = bias;
+    a.ids = ids;
+    a.weights = weights;
+    a.counts = counts;
+    a.offsets = offsets;
+    a.perm = perm;
+    a.inv = inv;
+    a.chunk_counts = static_cast<int32_t*>(ws);
+    a.T = T;
+    a.E = static_cast<int>(E);
+    a.top_k = top_k;
+    a.score = static_cast<int>(score);
+    a.n_groups = n_groups;
+    a.top_groups = top_groups;
+    a.group_top = group_top;
+    a.renorm = renorm != 0;
+    a.by_logit = !bias && (n_groups == 1 || group_top == 1);
+    a.scale = scale;
+    cudaError_t e = mx::launch_route_scored(a, dt == MXFP4_IN_BF16, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? MXFP4_OK : cuda_fail(e);
 }
 

@@ -30,6 +30,38 @@ struct GemmArgs {
     int act_stages;
 };
 
+// Arguments of the routing with scores (see route_scored.cu).
+struct RouteScoredArgs {
+    const void* logits;        // [T, E] fp32 or bf16
+    const float* bias;         // [E] or nullptr
+    int32_t* ids;              // [T, top_k]
+    float* weights;            // [T, top_k]
+    int32_t* counts;           // [E]
+    int32_t* offsets;          // [E + 1]
+    int32_t* perm;             // [T * top_k]
+    int32_t* inv;              // [T * top_k]
+    int32_t* chunk_counts;     // scratch [chunks, E]
+    int64_t T;
+    int E, top_k, score, n_groups, top_groups, group_top, renorm;
+    int by_logit;              // the choice goes by the logits (no bias, no sums of scores)
+    float scale;
+};
+
+// Arguments of the linear layer (see linear.cu).
+struct LinearArgs {
+    const void* x;             // bf16 [M, K]
+    const uint8_t* codes;      // [N, K/2]
+    const uint8_t* scales;     // [N, K/32]
+    const void* bias;          // [N] bf16 or fp32, or nullptr
+    const void* residual;      // bf16 [M, n_out], or nullptr
+    void* y;                   // bf16 [M, n_out]
+    int64_t M, K, N;
+    int64_t n_out;             // N, or N / 2 with the gated activation
+    int bias_f32;
+    int act;
+    unsigned* status;
+};
+
 // Token tiling of the grouped GEMM: NT token rows per MMA, TT token tiles per
 // dequantized weight tile.
 struct TokenTiling {
@@ -69,6 +101,9 @@ cudaError_t launch_gather_rows(const void* src, int64_t n_src, int64_t row_bytes
                                cudaStream_t stream);
 cudaError_t launch_combine(const void* y_sorted, const int32_t* inv, int64_t T, int top_k,
                            int64_t H, void* out, int sm_count, cudaStream_t stream);
+size_t route_scored_ws_bytes(int64_t T, int64_t E);
+cudaError_t launch_route_scored(const RouteScoredArgs& a, bool bf16, cudaStream_t stream);
+cudaError_t launch_linear(const LinearArgs& a, cudaStream_t stream);
 TokenTiling pick_token_tiling(int64_t rows, int64_t groups);
 int64_t max_gemm_k();   // largest contraction length the grouped GEMM accepts
 

@@ -41,6 +41,7 @@ __all__ = [
     "E2M1_GRID", "FLOOR", "CEIL", "e2m1_magnitude", "bf16_to_f64", "f64_to_bf16",
     "quantize", "dequantize_bf16", "dequantize_f64", "route", "gemm_w4a16",
     "gemm_w4a4", "moe_mlp", "moe_down", "silu", "router_logits", "moe_mlp_dense",
+    "route_scored", "linear",
 ]
 
 FLOOR = 0
@@ -215,6 +216,59 @@ def route(logits: np.ndarray, top_k: int):
     return dict(ids=ids, w=w, counts=counts, offsets=offsets, perm=perm, inv=inv)
 
 
+def route_scored(logits, top_k: int, score: str = "softmax", bias=None, n_groups: int = 1, top_groups: int = 1,
+                 group_top: int = 1, renorm: bool = True, scale: float = 1.0):
+    """Routing with softmax-over-all or sigmoid scores, a bias for the choice, groups and
+    renormalised weights, token by token in fp64 (readings, as ``route``):
+      * s_e = exp(l_e - m) / sum exp(l - m) over the numbers of the row (an infinite
+        maximum is shared by its experts), or 1 / (1 + exp(-l_e)); l_e = -inf: s_e = 0;
+      * c_e = s_e + bias_e, -inf where l_e = -inf; without bias and group_top = 2 the
+        logits stand for c (the same order);
+      * a group's value: its largest c, or the sum of its two largest above -inf; NaN
+        takes no part; kept groups by (value desc, index asc);
+      * ids by (c desc, id asc) in the kept groups, NaN below -inf;
+      * w_j = s_{id_j}, over their sum if renorm (0 where the sum is 0), times scale.
+    Returns the dict of ``route``."""
+    logits = np.asarray(logits, dtype=np.float64)
+    T, E = logits.shape
+    gs = E // n_groups
+    by_logit = bias is None and (n_groups == 1 or group_top == 1)
+    ids = np.zeros((T, top_k), dtype=np.int32)
+    w = np.zeros((T, top_k))
+    for t in range(T):
+        l = logits[t]
+        num = l[~np.isnan(l)]
+        with np.errstate(over="ignore", invalid="ignore"):
+            if score == "sigmoid":
+                s = np.where(l >= 0, 1.0 / (1.0 + np.exp(-l)), np.exp(l) / (1.0 + np.exp(l)))
+            else:
+                m = num.max() if num.size else -np.inf
+                z = np.where(l == m, 1.0, np.exp(l - m))
+                z = np.where(l == -np.inf, 0.0, z)
+                s = z / np.nansum(z)
+        s = np.where(l == -np.inf, 0.0, s)
+        c = l.copy() if by_logit else s + (0.0 if bias is None else np.asarray(bias, dtype=np.float64))
+        c = np.where(l == -np.inf, -np.inf, c)
+        values = []
+        for g in range(n_groups):
+            best = sorted((v for v in c[g * gs:(g + 1) * gs] if v > -np.inf), reverse=True)[:group_top]
+            values.append(sum(best) if best else -np.inf)
+        kept = sorted(range(n_groups), key=lambda g: (-values[g], g))[:top_groups]
+        cand = [e for g in kept for e in range(g * gs, (g + 1) * gs)]
+        cand.sort(key=lambda e: (bool(np.isnan(c[e])), 0.0 if np.isnan(c[e]) else -c[e], e))
+        ids[t] = cand[:top_k]
+        v = s[ids[t]]
+        if renorm:
+            v = v / v.sum() if v.sum() != 0 else np.zeros(top_k)
+        w[t] = v * scale
+    flat = ids.reshape(-1).astype(np.int64)
+    counts = np.bincount(flat, minlength=E).astype(np.int64)
+    perm = np.argsort(flat, kind="stable").astype(np.int64)
+    inv = np.empty_like(perm)
+    inv[perm] = np.arange(perm.size)
+    return dict(ids=ids, w=w, counts=counts, offsets=np.concatenate([[0], np.cumsum(counts)]), perm=perm, inv=inv)
+
+
 # --------------------------------------------------------------------------- GEMM
 
 def _as_bf16_bits(x) -> np.ndarray:
@@ -300,6 +354,35 @@ def moe_mlp(x_bits, logits, top_k, w13_codes, w13_scales, w2_codes, w2_scales,
     if return_h:
         return out, h_all
     return out
+
+
+def activation(name: str, z: np.ndarray) -> np.ndarray:
+    """none, relu, silu, gelu (erf), gelu_tanh elementwise; swiglu on columns [gate | up]."""
+    from math import erfc, pi, sqrt
+    if name == "relu":
+        return np.where(z < 0, 0.0, z)
+    if name == "silu":
+        return silu(z)
+    if name == "gelu":
+        return 0.5 * z * np.vectorize(erfc)(-z / sqrt(2.0))
+    if name == "gelu_tanh":
+        return 0.5 * z * (1.0 + np.tanh(sqrt(2.0 / pi) * (z + 0.044715 * z ** 3)))
+    if name == "swiglu":
+        half = z.shape[1] // 2
+        return silu(z[:, :half]) * z[:, half:]
+    if name != "none":
+        raise ValueError(name)
+    return z
+
+
+def linear(x_bits, w_codes, w_scales, bias=None, act: str = "none", residual=None) -> np.ndarray:
+    """act(x . dequant(W)^T + bias) + residual in fp64, unrounded: bf16 x [M, K], MXFP4 W
+    [N, K] (exact values, not rounded to bf16), bias [N] and residual [M, n_out] as fp64 values."""
+    z = bf16_to_f64(_as_bf16_bits(x_bits)) @ dequantize_f64(w_codes, w_scales).T
+    if bias is not None:
+        z = z + bias
+    a = activation(act, z)
+    return a if residual is None else a + residual
 
 
 def moe_down(h_bits, logits, top_k, w2_codes, w2_scales, mode: str = "w4a16", tokens=None):
