@@ -504,9 +504,13 @@ mxfp4_status mxfp4_gemm(const void* x_bf16, int64_t M, int64_t K, const uint8_t*
     return e == cudaSuccess ? MXFP4_OK : cuda_fail(e);
 }
 
+// Whether a linear layer takes the many-token engine (weights dequantized once).
+static bool linear_many(int64_t M) { return M >= 256; }
+
 size_t mxfp4_linear_workspace_size(int64_t M, int64_t K, int64_t N, mxfp4_act act) {
-    (void)M, (void)K, (void)N, (void)act;
-    return 0;
+    (void)act;
+    if (M <= 0 || K <= 0 || N <= 0 || !linear_many(M)) return 0;
+    return align_up(static_cast<size_t>(N) * K * 2, 256);   // W in bf16
 }
 
 mxfp4_status mxfp4_linear(const void* x_bf16, int64_t M, int64_t K, const uint8_t* w_codes,
@@ -517,11 +521,11 @@ mxfp4_status mxfp4_linear(const void* x_bf16, int64_t M, int64_t K, const uint8_
     if (M <= 0 || K <= 0 || N <= 0) return MXFP4_ERR_INVALID_ARG;
     if (bias && bias_dt != MXFP4_IN_BF16 && bias_dt != MXFP4_IN_F32) return MXFP4_ERR_INVALID_ARG;
     if (act < MXFP4_ACT_NONE || act > MXFP4_ACT_SWIGLU) return MXFP4_ERR_INVALID_ARG;
-    const int64_t lim = int64_t{1} << 31;
-    if (K % 32 != 0 || K > (1 << 20) || M >= lim || N >= lim) return MXFP4_ERR_UNSUPPORTED_SHAPE;
+    const int64_t lim = int64_t{1} << 30;
+    if (K % 32 != 0 || K > (1 << 20) || M > lim || N > lim) return MXFP4_ERR_UNSUPPORTED_SHAPE;
     if (act == MXFP4_ACT_SWIGLU && N % 2 != 0) return MXFP4_ERR_UNSUPPORTED_SHAPE;
     const int64_t n_out = act == MXFP4_ACT_SWIGLU ? N / 2 : N;
-    if (M > (int64_t{1} << 46) / n_out) return MXFP4_ERR_UNSUPPORTED_SHAPE;
+    if (M > (int64_t{1} << 46) / n_out || N > (int64_t{1} << 40) / K) return MXFP4_ERR_UNSUPPORTED_SHAPE;
     if (!aligned16(x_bf16) || !aligned16(w_codes) || !aligned16(w_scales) || !aligned16(y_bf16) ||
         (bias && !aligned16(bias)) || (residual_bf16 && !aligned16(residual_bf16)))
         return MXFP4_ERR_MISALIGNED;
@@ -545,7 +549,19 @@ mxfp4_status mxfp4_linear(const void* x_bf16, int64_t M, int64_t K, const uint8_
     a.bias_f32 = bias_dt == MXFP4_IN_F32;
     a.act = static_cast<int>(act);
     a.status = d->status;
-    cudaError_t e = mx::launch_linear(a, static_cast<cudaStream_t>(stream));
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    cudaError_t e;
+    if (linear_many(M)) {
+        const int nt = mx::linear_many_cols(M, n_out, act == MXFP4_ACT_SWIGLU, d->sm_count);
+        CUtensorMap tx, tw;
+        if ((st = encode_act_map(&tx, x_bf16, K, M, 128)) != MXFP4_OK) return st;
+        if ((st = encode_act_map(&tw, ws, K, N, nt / 2)) != MXFP4_OK) return st;
+        if ((e = mx::launch_dequantize(w_codes, w_scales, N, K, ws, d->sm_count, d->status, s)) != cudaSuccess)
+            return cuda_fail(e);
+        e = mx::launch_linear_many(a, tx, tw, nt, d->sm_count, s);
+    } else {
+        e = mx::launch_linear(a, s);
+    }
     return e == cudaSuccess ? MXFP4_OK : cuda_fail(e);
 }
 

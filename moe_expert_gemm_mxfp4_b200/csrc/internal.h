@@ -104,6 +104,9 @@ cudaError_t launch_combine(const void* y_sorted, const int32_t* inv, int64_t T, 
 size_t route_scored_ws_bytes(int64_t T, int64_t E);
 cudaError_t launch_route_scored(const RouteScoredArgs& a, bool bf16, cudaStream_t stream);
 cudaError_t launch_linear(const LinearArgs& a, cudaStream_t stream);
+int linear_many_cols(int64_t M, int64_t n_out, bool gated, int sm_count);   // columns of a work tile
+cudaError_t launch_linear_many(const LinearArgs& a, const CUtensorMap& tmap_x, const CUtensorMap& tmap_w, int nt,
+                               int sm_count, cudaStream_t stream);
 TokenTiling pick_token_tiling(int64_t rows, int64_t groups);
 int64_t max_gemm_k();   // largest contraction length the grouped GEMM accepts
 

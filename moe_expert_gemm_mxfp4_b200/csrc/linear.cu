@@ -1,26 +1,14 @@
 // Linear layer on MXFP4 weights with a fused epilogue:
 //   y = bf16( act(x . dequant(W)^T + bias) + residual ).
-#include "common.cuh"
-#include "internal.h"
+#include "linear_epilogue.cuh"
 
 namespace mx {
 
 namespace {
 
-constexpr int kTM = 64, kTN = 64;   // tokens and output features per CTA
+using namespace linear;
 
-// The activation of one output in fp32 (u: the gated activation's second factor).
-__device__ __forceinline__ float activate(int act, float z, float u) {
-    switch (act) {
-        case MXFP4_ACT_RELU: return z < 0.f ? 0.f : z;   // keeps NaN
-        case MXFP4_ACT_SILU: return z / (1.f + expf(-z));
-        case MXFP4_ACT_GELU: return 0.5f * z * erfcf(-0.70710678118654752f * z);
-        case MXFP4_ACT_GELU_TANH:   // 0.5 (1 + tanh(v)) = 1 / (1 + exp(-2 v))
-            return z / (1.f + expf(-1.5957691216057308f * (z + 0.044715f * z * z * z)));
-        case MXFP4_ACT_SWIGLU: return z / (1.f + expf(-z)) * u;
-        default: return z;
-    }
-}
+constexpr int kTM = 64, kTN = 64;   // tokens and output features per CTA
 
 // One 64 x 64 tile of outputs per CTA, a 32-element weight block of K at a time.
 template <bool kGated>
@@ -62,11 +50,6 @@ __global__ void __launch_bounds__(256) linear_kernel(const LinearArgs a) {
         }
         __syncthreads();
     }
-    auto bias_at = [&](int64_t n) {
-        if (!a.bias) return 0.f;
-        return a.bias_f32 ? static_cast<const float*>(a.bias)[n]
-                          : __bfloat162float(static_cast<const __nv_bfloat16*>(a.bias)[n]);
-    };
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int64_t m = m0 + tm * 4 + i;
@@ -74,8 +57,8 @@ __global__ void __launch_bounds__(256) linear_kernel(const LinearArgs a) {
         for (int j = 0; j < 4; ++j) {
             const int64_t n = n0 + tn + 16 * j;
             if (m < a.M && n < a.n_out) {
-                float v = activate(a.act, acc[0][i][j] + bias_at(n),
-                                   kGated ? acc[NW - 1][i][j] + bias_at(n + a.n_out) : 0.f);
+                float v = activate(a.act, acc[0][i][j] + bias_at(a, n),
+                                   kGated ? acc[NW - 1][i][j] + bias_at(a, n + a.n_out) : 0.f);
                 const int64_t at = m * a.n_out + n;
                 if (a.residual) v += __bfloat162float(static_cast<const __nv_bfloat16*>(a.residual)[at]);
                 static_cast<__nv_bfloat16*>(a.y)[at] = __float2bfloat16_rn(v);
