@@ -504,13 +504,15 @@ mxfp4_status mxfp4_gemm(const void* x_bf16, int64_t M, int64_t K, const uint8_t*
     return e == cudaSuccess ? MXFP4_OK : cuda_fail(e);
 }
 
-// Whether a linear layer takes the many-token engine (weights dequantized once).
-static bool linear_many(int64_t M) { return M >= 256; }
+// Whether a linear layer takes the many-token engine (weights dequantized once).  The other
+// keeps 128 rows of block scales in shared memory, which bounds K.
+static bool linear_many(int64_t M, int64_t K) { return M > 512 || K > 8192; }
 
 size_t mxfp4_linear_workspace_size(int64_t M, int64_t K, int64_t N, mxfp4_act act) {
-    (void)act;
-    if (M <= 0 || K <= 0 || N <= 0 || !linear_many(M)) return 0;
-    return align_up(static_cast<size_t>(N) * K * 2, 256);   // W in bf16
+    if (M <= 0 || K <= 0 || N <= 0) return 0;
+    if (linear_many(M, K)) return align_up(static_cast<size_t>(N) * K * 2, 256);   // W in bf16
+    const bool gated = act == MXFP4_ACT_SWIGLU;
+    return align_up(mx::linear_few_ws_bytes(M, K, gated ? N / 2 : N, gated), 256);
 }
 
 mxfp4_status mxfp4_linear(const void* x_bf16, int64_t M, int64_t K, const uint8_t* w_codes,
@@ -551,7 +553,7 @@ mxfp4_status mxfp4_linear(const void* x_bf16, int64_t M, int64_t K, const uint8_
     a.status = d->status;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e;
-    if (linear_many(M)) {
+    if (linear_many(M, K)) {
         const int nt = mx::linear_many_cols(M, n_out, act == MXFP4_ACT_SWIGLU, d->sm_count);
         CUtensorMap tx, tw;
         if ((st = encode_act_map(&tx, x_bf16, K, M, 128)) != MXFP4_OK) return st;
@@ -560,7 +562,7 @@ mxfp4_status mxfp4_linear(const void* x_bf16, int64_t M, int64_t K, const uint8_
             return cuda_fail(e);
         e = mx::launch_linear_many(a, tx, tw, nt, d->sm_count, s);
     } else {
-        e = mx::launch_linear(a, s);
+        e = mx::launch_linear_few(a, ws, d->sm_count, s);
     }
     return e == cudaSuccess ? MXFP4_OK : cuda_fail(e);
 }

@@ -1,0 +1,590 @@
+// Linear layer for few tokens: y = bf16( act(x . W^T + bias) + residual ) with the MXFP4
+// weights fed to the tensor core as they are (tcgen05 kind::mxf8f6f4, block scales).
+//
+// With few tokens the weights' bytes bound the call, and turning codes into bf16 costs more
+// than reading them.  So the weights stay E2M1 with their E8M0 scales (the MMA's A side),
+// and the bf16 activations become two E4M3 parts with block scales (the B side):
+//   x = 2^s (hi + 2^-5 lo),   2^7 <= max |x| / 2^s < 2^8 over a 32-block,
+//   hi = e4m3(x / 2^s),       lo = e4m3(2^5 (x / 2^s - hi)).
+// bf16 has 8 significant bits, hi takes 4, and what is left of an element fits the 4 of lo: the
+// sum is exact for every element within 2^14 of its block's largest, and off by at most
+// 2^-22 of that largest for the others, about what one addition in fp32 rounds.  Products with
+// E2M1 are exact, sums are fp32.  A block that holds Inf or NaN gets the scale NaN; an output
+// that comes out NaN is computed again from x and W in fp32, so that infinities act as in
+// the formula.
+//
+// Two launches, the second overlapping the first (programmatic dependent launch):
+//   linear_few_prepare  x -> hi and lo tiles in the tensor core's shared-memory image, their
+//                       scales and the weights' scales in its scale-factor layout;
+//   linear_few          one CTA per (128 weight rows, K range, token tile).
+// Roles (8 warps): warps 0-3 bring the codes with 8-byte cp.async straight into the 16-element
+// containers that the tensor core takes (8 bytes of codes, 8 of padding); warp 4 bulk-copies
+// the prepared tiles; warp 5 issues scale copies and MMAs.  The CTAs of a cluster split K and sum
+// their partial results through distributed shared memory in rank order (the same on every
+// run); each finishes a share of the tokens.
+//
+// hi and lo rows lie next to each other in one MMA of N = 2 Mp columns while that fits the 128
+// rows of a scale atom (an MMA of N <= 64 costs the same whatever its N), else they are
+// two MMAs of N = Mp into the same accumulator.
+#include "linear_epilogue.cuh"
+
+namespace mx {
+
+namespace {
+
+using namespace linear;
+
+constexpr int kThreads = 256;
+constexpr int kBM = 128;             // weight rows per tile
+constexpr int kBK = 128;             // K per stage: 128 one-byte containers per row
+constexpr int kABytes = kBM * kBK;
+constexpr int kAtom = 512;           // scale atom: 128 rows x 4 scales
+constexpr int kMaxMp = 128;          // tokens per tile
+constexpr int kMaxStages = 8;
+constexpr int kSmemSm = 228 * 1024;  // per SM, 1 KB of it taken by each resident CTA
+constexpr int kMaxCluster = 8;
+constexpr uint32_t kTmemCols = 256, kSfCol = 128;   // D [0, 128), scale sets of 16 columns behind it
+
+__device__ __forceinline__ uint32_t ctarank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync_all() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t in_rank(uint32_t saddr, uint32_t rank) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ float2 ld_cluster_f32x2(uint32_t addr) {
+    float2 v;
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr));
+    return v;
+}
+__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global.L2::128B [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void fence_async_proxy() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+// r[0..7] <- 8 consecutive 32-bit TMEM columns of this thread's lane.
+__device__ __forceinline__ void tmem_ld_x8(uint32_t taddr, uint32_t* r) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr)
+                 : "memory");
+}
+// D[tmem] (+)= (A . 2^SFA) (B . 2^SFB)^T, one scale per 32 elements of K, K = 32.
+__device__ __forceinline__ void mma_mxf8f6f4(uint32_t d, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                             uint32_t sfa, uint32_t sfb, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(d),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(acc), "r"(sfa), "r"(sfb)
+        : "memory");
+}
+// Instruction descriptor of kind::mxf8f6f4: B scale id (bits 4-5), A format E2M1 = 5 (bits 7-9),
+// B format E4M3 = 0 (bits 10-12), N >> 3 (bits 17-22), scales E8M0 (bit 23), M >> 7 (bits
+// 27-28), A scale id (bits 29-30).
+__device__ __forceinline__ uint32_t idesc_mxf8(int N, uint32_t sf_id) {
+    return (sf_id << 4) | (5u << 7) | (static_cast<uint32_t>(N >> 3) << 17) | (1u << 23) | (1u << 27) | (sf_id << 29);
+}
+
+// hi and lo of two scaled values: packed E4M3 bytes (low byte first).
+__device__ __forceinline__ void split2(float a, float b, float up, uint32_t& hi, uint32_t& lo) {
+    uint16_t h, l;
+    uint32_t back;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(h) : "f"(b), "f"(a));
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(back) : "h"(h));
+    float ha, hb;
+    asm("{\n\t.reg .b16 x, y;\n\tmov.b32 {x, y}, %2;\n\tcvt.f32.f16 %0, x;\n\tcvt.f32.f16 %1, y;\n\t}"
+        : "=f"(ha), "=f"(hb) : "r"(back));
+    const float ra = (a - ha) * up, rb = (b - hb) * up;   // exact: the difference has at most 5 bits
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(l) : "f"(rb), "f"(ra));
+    hi = h;
+    lo = l;
+}
+
+struct Plan {
+    int mp;            // token rows of a tile (padded to 8 or a multiple of 16)
+    int t_tiles;       // token tiles of mp rows
+    int stacked;       // hi and lo rows in one MMA of N = 2 mp
+    int w_tiles;       // tiles of 128 weight rows
+    int split;         // CTAs of a cluster along K
+    int nk;            // K stages
+    int stages;        // ring depth
+    int b_bytes;       // prepared bytes per token tile and stage: hi and lo rows, scale atoms
+    int stage_bytes;
+};
+
+// First weight row of a tile's row r, or -1 past the end.  Gated tiles hold 64 gate rows and
+// the 64 up rows of the same features.
+template <bool kGated>
+__device__ __forceinline__ int64_t weight_row(const LinearArgs& a, int64_t f, int r) {
+    if (!kGated) {
+        const int64_t n = f * kBM + r;
+        return n < a.N ? n : -1;
+    }
+    const int64_t n = f * 64 + (r & 63);
+    return n < a.n_out ? n + (r >= 64 ? a.n_out : 0) : -1;
+}
+
+// ---------------------------------------------------------------- prepare
+// The first w_tiles CTAs lay the weights' scales out: per tile and stage an atom of 512
+// bytes, scale j of row r at byte 16 (r % 32) + 4 (r / 32) + j.  The others take (token, stage)
+// items, one per warp: 4 elements per lane, 8 lanes to a block.
+template <bool kGated>
+__global__ void __launch_bounds__(kThreads)
+linear_few_prepare_kernel(const LinearArgs a, const Plan p, uint8_t* __restrict__ ws_b, uint8_t* __restrict__ ws_sfa) {
+    grid_launch_dependents();
+    extern __shared__ __align__(16) uint8_t s_rows[];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int kb = static_cast<int>(a.K / 32);
+    if (static_cast<int>(blockIdx.x) < p.w_tiles) {
+        const int64_t f = blockIdx.x;
+        // the tile's scales: one run of rows (gated: one of gate, one of up rows)
+        constexpr int kSeg = kGated ? 64 : kBM;
+        int shift[2] = {0, 0};
+#pragma unroll
+        for (int h = 0; h < (kGated ? 2 : 1); ++h) {
+            const int64_t row0 = f * kSeg + (h ? a.n_out : 0);
+            const int64_t left = (kGated ? a.n_out : a.N) - f * kSeg;
+            const int len = static_cast<int>((left < kSeg ? left : kSeg) * kb);
+            const uint8_t* src = a.scales + row0 * kb;
+            shift[h] = static_cast<int>(reinterpret_cast<uintptr_t>(src) & 15);
+            uint8_t* dst = s_rows + h * (64 * kb + 32) / 16 * 16 + shift[h];
+            const int head = min(len, (16 - shift[h]) & 15), body = (len - head) / 16;
+            for (int i = tid; i < body; i += kThreads)
+                reinterpret_cast<uint4*>(dst + head)[i] = __ldg(reinterpret_cast<const uint4*>(src + head) + i);
+            for (int i = tid; i < head; i += kThreads) dst[i] = src[i];
+            for (int i = head + 16 * body + tid; i < len; i += kThreads) dst[i] = src[i];
+        }
+        __syncthreads();
+        for (int j = warp; j < p.nk; j += kThreads / 32) {
+            uint32_t w[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int r = lane + 32 * q;
+                w[q] = 0x7F7F7F7Fu;
+                if (weight_row<kGated>(a, f, r) >= 0) {
+                    const int h = kGated && r >= 64;
+                    const uint8_t* row = s_rows + h * (64 * kb + 32) / 16 * 16 + shift[h] + (kGated ? r & 63 : r) * kb;
+                    w[q] = 0;
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) {
+                        const uint32_t s = 4 * j + b < kb ? row[4 * j + b] : 0x7Fu;
+                        w[q] |= s << (8 * b);
+                    }
+                }
+            }
+            reinterpret_cast<uint4*>(ws_sfa + (f * p.nk + j) * kAtom)[lane] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        return;
+    }
+    const int64_t items = a.M * p.nk;
+    const int64_t step = static_cast<int64_t>(gridDim.x - p.w_tiles) * (kThreads / 32);
+    for (int64_t it = static_cast<int64_t>(blockIdx.x - p.w_tiles) * (kThreads / 32) + warp; it < items; it += step) {
+        const int64_t t = it / p.nk;
+        const int j = static_cast<int>(it - t * p.nk);
+        const int64_t tt = t / p.mp;
+        const int r = static_cast<int>(t - tt * p.mp);
+        const int64_t k = static_cast<int64_t>(j) * kBK + 4 * lane;
+        uint2 v = make_uint2(0u, 0u);
+        if (k < a.K) v = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.x) + t * a.K + k));
+        // bf16 magnitudes order as integers, infinities and NaN last
+        uint32_t amax = max(max(v.x & 0x7FFFu, (v.x >> 16) & 0x7FFFu), max(v.y & 0x7FFFu, (v.y >> 16) & 0x7FFFu));
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1) amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
+        const bool odd = amax >= 0x7F80u;
+        const int e = static_cast<int>(amax >> 7);          // biased exponent of the largest
+        const int s_hi = e > 7 ? e - 7 : 0, s_lo = s_hi > 5 ? s_hi - 5 : 0;
+        const float down = __uint_as_float(static_cast<uint32_t>(254 - s_hi) << 23);   // 2^(127 - s_hi)
+        const float up = __uint_as_float(static_cast<uint32_t>(127 + s_hi - s_lo) << 23);
+        uint32_t h0, h1, l0, l1;
+        split2(bf16_lo(v.x) * down, bf16_hi(v.x) * down, up, h0, l0);
+        split2(bf16_lo(v.y) * down, bf16_hi(v.y) * down, up, h1, l1);
+        const uint32_t hi = odd ? 0x7F7F7F7Fu : h0 | h1 << 16, lo = odd ? 0u : l0 | l1 << 16;
+        uint8_t* blk = ws_b + (tt * p.nk + j) * p.b_bytes;
+        const int r_lo = p.mp + r;
+        auto at = [&](int row) { return row * kBK + (((lane >> 2) ^ (row & 7)) << 4) + 4 * (lane & 3); };
+        *reinterpret_cast<uint32_t*>(blk + at(r)) = hi;
+        *reinterpret_cast<uint32_t*>(blk + at(r_lo)) = lo;
+        if ((lane & 7) == 0) {
+            uint8_t* atom = blk + 2 * p.mp * kBK;
+            auto sf = [&](int row) { return 16 * (row & 31) + 4 * (row >> 5) + (lane >> 3); };
+            atom[sf(r)] = static_cast<uint8_t>(odd ? 255 : s_hi);
+            atom[p.stacked ? sf(r_lo) : kAtom + sf(r)] = static_cast<uint8_t>(odd ? 255 : s_lo);
+        }
+    }
+}
+
+// One output's sum in fp32 from x and W themselves.
+__device__ __noinline__ float dot_direct(const LinearArgs& a, int64_t m, int64_t row) {
+    const uint16_t* x = static_cast<const uint16_t*>(a.x) + m * a.K;
+    const uint8_t* c = a.codes + row * (a.K / 2);
+    float acc = 0.f;
+    for (int64_t k = 0; k < a.K; k += 2) {
+        const float s = e8m0_f32(a.scales[row * (a.K / 32) + k / 32]);
+        const uint32_t byte = c[k / 2];
+        acc += __uint_as_float(static_cast<uint32_t>(x[k]) << 16) * (e2m1_f32(byte & 15u) * s);
+        acc += __uint_as_float(static_cast<uint32_t>(x[k + 1]) << 16) * (e2m1_f32(byte >> 4) * s);
+    }
+    return acc;
+}
+
+// ---------------------------------------------------------------- product
+// D: cp.async groups in flight per producer thread (ring depth D + 1 at least).
+template <bool kGated, int D>
+__global__ void __launch_bounds__(kThreads)
+linear_few_kernel(const LinearArgs a, const Plan p, const uint8_t* __restrict__ ws_b, const uint8_t* __restrict__ ws_sfa) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                               ~static_cast<uintptr_t>(1023));
+    __shared__ uint64_t full_a[kMaxStages], full_b[kMaxStages], empty[kMaxStages], done[1];
+    __shared__ uint32_t s_tmem;
+    __shared__ volatile int s_abort, s_never;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int NS = p.stages;
+    const uint32_t rank = ctarank();
+    const int64_t f = blockIdx.x / p.split;
+    const int64_t tt = blockIdx.y;
+    // this CTA's K stages [j0, j0 + n); the launch keeps split <= nk, so n >= 1
+    const int j0 = static_cast<int>(rank) * p.nk / p.split;
+    const int n = (static_cast<int>(rank) + 1) * p.nk / p.split - j0;
+    if (tid == 0) {
+        for (int s = 0; s < NS; ++s) {
+            mbar_init(&full_a[s], 4);   // one arrival per producer warp
+            mbar_init(&full_b[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        mbar_init(done, 1);
+        s_abort = 0;
+        s_never = 0;
+        fence_mbar_init();
+    }
+    if (warp == 6) {
+        tmem_alloc(&s_tmem, kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = s_tmem;
+
+    if (warp < 4) {
+        // ---------------- codes: warp w brings rows 32 w .. 32 w + 31; a warp's copy is 4 rows x 64
+        // bytes; 16 elements (8 bytes) per container, swizzled in 16-byte chunks
+        const int c = lane & 7;                       // container of the row
+        const uint8_t* src[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int64_t row = weight_row<kGated>(a, f, 32 * warp + 4 * i + (lane >> 3));
+            src[i] = row < 0 ? nullptr : a.codes + row * (a.K / 2) + 8 * c;
+        }
+        bool ok = true;
+        auto finish = [&](int i) {   // stage i has landed for this thread
+            fence_async_proxy();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&full_a[i % NS]);
+        };
+        int i = 0;
+        for (; i < n; ++i) {
+            const int s = i % NS;
+            if (!__all_sync(0xFFFFFFFFu, mbar_wait(&empty[s], ((i / NS) & 1) ^ 1, &s_abort))) { ok = false; break; }
+            const uint32_t dst = smem_u32(smem + s * p.stage_bytes);
+            const int64_t k = static_cast<int64_t>(j0 + i) * kBK;
+            if (k + 16 * c < a.K) {
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    const int r = 32 * warp + 4 * q + (lane >> 3);
+                    if (src[q]) cp_async8(dst + r * kBK + ((c ^ (r & 7)) << 4), src[q] + k / 2);
+                }
+            }
+            cp_async_commit();
+            if (i >= D) {
+                cp_async_wait<D>();
+                finish(i - D);
+            }
+        }
+        cp_async_wait<0>();
+        if (ok) {
+            for (int d = n > D ? n - D : 0; d < n; ++d) finish(d);
+        } else {
+            s_abort = 1;
+            record_status(a.status, MXFP4_ERR_TIMEOUT);
+        }
+    } else if (warp == 4) {
+        // ---------------- prepared activations and scales
+        if (lane == 0) {
+            grid_wait();   // the prepare kernel's writes are complete
+            int issued = 0;
+            bool ok = true;
+            for (int i = 0; i < n; ++i, ++issued) {
+                const int s = i % NS;
+                if (!mbar_wait(&empty[s], ((i / NS) & 1) ^ 1, &s_abort)) { ok = false; break; }
+                uint8_t* dst = smem + s * p.stage_bytes + kABytes;
+                mbar_arrive_expect_tx(&full_b[s], static_cast<uint32_t>(p.b_bytes + kAtom));
+                bulk_load(dst, ws_b + (tt * p.nk + j0 + i) * p.b_bytes, static_cast<uint32_t>(p.b_bytes), &full_b[s]);
+                bulk_load(dst + p.b_bytes, ws_sfa + (f * p.nk + j0 + i) * kAtom, kAtom, &full_b[s]);
+            }
+            if (!ok) {
+                s_abort = 1;
+                record_status(a.status, MXFP4_ERR_TIMEOUT);
+                for (int i = issued > NS ? issued - NS : 0; i < issued; ++i)
+                    mbar_wait(&full_b[i % NS], (i / NS) & 1, &s_never);
+            }
+        }
+    } else if (warp == 5) {
+        // ---------------- MMA issuer
+        if (lane == 0) {
+            bool ok = true;
+            const int nn = p.stacked ? 2 * p.mp : p.mp;
+            for (int i = 0; i < n; ++i) {
+                const int s = i % NS;
+                if (!mbar_wait(&full_a[s], (i / NS) & 1, &s_abort) || !mbar_wait(&full_b[s], (i / NS) & 1, &s_abort)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                fence_async_proxy();
+                const uint32_t wa = smem_u32(smem + s * p.stage_bytes), xb = wa + kABytes;
+                const uint32_t sf = xb + 2 * p.mp * kBK;      // hi (and lo) scale atoms, then the weights'
+                const uint32_t set = tmem + kSfCol + 16 * (i & 1);
+                tmem_cp_32x128b_x4(set, rows16_desc(xb + p.b_bytes));
+                tmem_cp_32x128b_x4(set + 4, rows16_desc(sf));
+                if (!p.stacked) tmem_cp_32x128b_x4(set + 8, rows16_desc(sf + kAtom));
+                const int64_t k0 = static_cast<int64_t>(j0 + i) * kBK;
+                const int steps = static_cast<int>(min(static_cast<int64_t>(4), (a.K - k0) / 32));
+                for (int q = 0; q < steps; ++q) {
+                    const uint32_t id = static_cast<uint32_t>(q);
+                    const uint32_t idesc = idesc_mxf8(nn, id);
+                    const uint64_t da = sw128_desc(wa + 32 * q);
+                    mma_mxf8f6f4(tmem, da, sw128_desc(xb + 32 * q), idesc, set | (id << 30), (set + 4) | (id << 30),
+                                 (i | q) != 0 ? 1u : 0u);
+                    if (!p.stacked)
+                        mma_mxf8f6f4(tmem, da, sw128_desc(xb + p.mp * kBK + 32 * q), idesc, set | (id << 30),
+                                     (set + 8) | (id << 30), 1u);
+                }
+                tc_commit(&empty[s]);
+            }
+            if (!ok) {
+                s_abort = 1;
+                record_status(a.status, MXFP4_ERR_TIMEOUT);
+            }
+            tc_commit(done);   // also drains every MMA issued before TMEM is released
+        }
+    }
+    __syncwarp();
+
+    // ---------------- partial sums -> shared memory [token][128 rows] (the idle ring)
+    const bool got = mbar_wait(done, 0, &s_never);
+    if (!__all_sync(0xFFFFFFFFu, got)) {
+        s_abort = 1;
+        record_status(a.status, MXFP4_ERR_TIMEOUT);
+    }
+    tc_fence_after();
+    __syncthreads();   // no copy into the ring is in flight: its last stage has been multiplied
+    float* part = reinterpret_cast<float*>(smem);
+    const int64_t t0 = tt * p.mp;
+    const int mt = static_cast<int>(min(static_cast<int64_t>(p.mp), a.M - t0));
+    {
+        const int q = warp & 3;
+        const uint32_t base = tmem + (static_cast<uint32_t>(q * 32) << 16);
+        const int row = 32 * q + lane;
+        for (int c = 8 * (warp >> 2); c < mt; c += 16) {
+            uint32_t v[8], w[8];
+            tmem_ld_x8(base + c, v);
+            if (p.stacked) tmem_ld_x8(base + p.mp + c, w);
+            tmem_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                float z = __uint_as_float(v[j]);
+                if (p.stacked) z += __uint_as_float(w[j]);
+                part[(c + j) * kBM + row] = z;
+            }
+        }
+    }
+    __syncwarp();
+    if (p.split > 1) cluster_sync_all(); else __syncthreads();
+
+    // ---------------- each CTA finishes its share of the tokens, two features per thread
+    {
+        constexpr int kPairs = kGated ? 32 : 64;
+        const int c0 = static_cast<int>(rank) * mt / p.split, c1 = (static_cast<int>(rank) + 1) * mt / p.split;
+        const int pr = tid % kPairs;
+        const int64_t n0 = f * (2 * kPairs) + 2 * pr;
+        const uint32_t mine = smem_u32(part);
+        const bool even = a.n_out % 2 == 0;
+        float bz[2] = {0.f, 0.f}, bu[2] = {0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            if (n0 + j < a.n_out) {
+                bz[j] = bias_at(a, n0 + j);
+                if (kGated) bu[j] = bias_at(a, n0 + j + a.n_out);
+            }
+        }
+        const uint16_t* res = static_cast<const uint16_t*>(a.residual);
+        uint16_t* y = static_cast<uint16_t*>(a.y);
+        for (int c = c0 + tid / kPairs; c < c1; c += kThreads / kPairs) {
+            if (n0 >= a.n_out) break;
+            float z[2] = {0.f, 0.f}, u[2] = {0.f, 0.f};
+            const uint32_t off = mine + (c * kBM + 2 * pr) * 4;
+            float2 v[kMaxCluster], w[kMaxCluster];
+#pragma unroll
+            for (int q = 0; q < kMaxCluster; ++q) {
+                if (q < p.split) {
+                    v[q] = ld_cluster_f32x2(in_rank(off, q));
+                    if (kGated) w[q] = ld_cluster_f32x2(in_rank(off + 64 * 4, q));
+                }
+            }
+#pragma unroll
+            for (int q = 0; q < kMaxCluster; ++q) {
+                if (q < p.split) {
+                    z[0] += v[q].x;
+                    z[1] += v[q].y;
+                    if (kGated) {
+                        u[0] += w[q].x;
+                        u[1] += w[q].y;
+                    }
+                }
+            }
+            const int64_t m = t0 + c;
+            float out[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                if (n0 + j < a.n_out) {
+                    if (z[j] != z[j]) z[j] = dot_direct(a, m, n0 + j);
+                    if (kGated && u[j] != u[j]) u[j] = dot_direct(a, m, n0 + j + a.n_out);
+                }
+                out[j] = activate(kGated ? static_cast<int>(MXFP4_ACT_SWIGLU) : a.act, z[j] + bz[j], u[j] + bu[j]);
+            }
+            const int64_t at = m * a.n_out + n0;
+            if (even) {
+                if (res) {
+                    const uint32_t r = *reinterpret_cast<const uint32_t*>(res + at);
+                    out[0] += bf16_lo(r);
+                    out[1] += bf16_hi(r);
+                }
+                *reinterpret_cast<uint32_t*>(y + at) = pack_bf16(out[0], out[1]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    if (n0 + j < a.n_out) {
+                        if (res) out[j] += __uint_as_float(static_cast<uint32_t>(res[at + j]) << 16);
+                        y[at + j] = static_cast<uint16_t>(pack_bf16(out[j], out[j]));
+                    }
+                }
+            }
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    if (p.split > 1) cluster_sync_all();   // the partials are read: their CTAs may end
+    __syncthreads();
+    if (warp == 6) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+// The launch geometry.  Independent of the device, so that the workspace query and the call agree.
+Plan make_plan(int64_t M, int64_t K, int64_t n_out, bool gated) {
+    Plan p{};
+    p.t_tiles = static_cast<int>((M + kMaxMp - 1) / kMaxMp);
+    const int per = static_cast<int>((M + p.t_tiles - 1) / p.t_tiles);
+    p.mp = per <= 8 ? 8 : (per + 15) / 16 * 16;
+    p.t_tiles = static_cast<int>((M + p.mp - 1) / p.mp);
+    p.stacked = 2 * p.mp <= 128;
+    const int f = gated ? 64 : kBM;
+    p.w_tiles = static_cast<int>((n_out + f - 1) / f);
+    p.nk = static_cast<int>((K + kBK - 1) / kBK);
+    p.b_bytes = 2 * p.mp * kBK + (p.stacked ? 1 : 2) * kAtom;
+    p.stage_bytes = (kABytes + p.b_bytes + kAtom + 1023) / 1024 * 1024;
+    return p;
+}
+
+}  // namespace
+
+size_t linear_few_ws_bytes(int64_t M, int64_t K, int64_t n_out, bool gated) {
+    const Plan p = make_plan(M, K, n_out, gated);
+    return static_cast<size_t>(p.t_tiles) * p.nk * p.b_bytes + static_cast<size_t>(p.w_tiles) * p.nk * kAtom;
+}
+
+namespace {
+
+template <bool kGated, int D>
+cudaError_t launch_product(const LinearArgs& a, const Plan& p, const uint8_t* ws_b, const uint8_t* ws_sfa,
+                           cudaStream_t stream) {
+    auto kern = linear_few_kernel<kGated, D>;
+    const int part = p.mp * kBM * 4;
+    int smem = p.stages * p.stage_bytes;
+    smem = (smem > part ? smem : part) + 1024;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(p.w_tiles * p.split), static_cast<unsigned>(p.t_tiles), 1);
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(p.split);
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kern, a, p, ws_b, ws_sfa);
+}
+
+template <bool kGated>
+cudaError_t launch_few(const LinearArgs& a, Plan p, void* ws, int sm_count, cudaStream_t stream) {
+    // ring depth and resident CTAs per SM: two where at least four stages then fit each
+    const int fixed = 1024 + 1024 + 512;   // alignment slack, the system's share, static shared memory
+    int occ = 2;
+    p.stages = (kSmemSm / 2 - fixed) / p.stage_bytes;
+    if (p.stages < 4) {
+        occ = 1;
+        p.stages = (kSmemSm - fixed) / p.stage_bytes;
+    }
+    if (p.stages > 6) p.stages = 6;
+    if (p.stages < 4) return cudaErrorInvalidConfiguration;
+    // K split over a cluster while the CTAs fit the SMs at once
+    p.split = 1;
+    while (p.split < kMaxCluster && 2 * p.split <= p.nk &&
+           2LL * p.split * p.w_tiles * p.t_tiles <= static_cast<int64_t>(occ) * sm_count)
+        p.split *= 2;
+    uint8_t* ws_b = static_cast<uint8_t*>(ws);
+    uint8_t* ws_sfa = ws_b + static_cast<size_t>(p.t_tiles) * p.nk * p.b_bytes;
+    const int kb = static_cast<int>(a.K / 32);
+    const int rows_smem = kBM * kb + 2 * 48;
+    cudaError_t e = cudaFuncSetAttribute(linear_few_prepare_kernel<kGated>, cudaFuncAttributeMaxDynamicSharedMemorySize, rows_smem);
+    if (e != cudaSuccess) return e;
+    const int64_t items = a.M * p.nk;
+    int64_t xg = (items + kThreads / 32 - 1) / (kThreads / 32);
+    if (xg > 4LL * sm_count) xg = 4LL * sm_count;
+    linear_few_prepare_kernel<kGated><<<static_cast<unsigned>(p.w_tiles + xg), kThreads, rows_smem, stream>>>(a, p, ws_b, ws_sfa);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    return p.stages >= 5 ? launch_product<kGated, 4>(a, p, ws_b, ws_sfa, stream)
+                         : launch_product<kGated, 3>(a, p, ws_b, ws_sfa, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_linear_few(const LinearArgs& a, void* ws, int sm_count, cudaStream_t stream) {
+    const bool gated = a.act == MXFP4_ACT_SWIGLU;
+    const Plan p = make_plan(a.M, a.K, a.n_out, gated);
+    return gated ? launch_few<true>(a, p, ws, sm_count, stream) : launch_few<false>(a, p, ws, sm_count, stream);
+}
+
+}  // namespace mx
