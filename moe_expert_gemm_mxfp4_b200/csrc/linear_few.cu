@@ -58,10 +58,18 @@ __device__ __forceinline__ uint32_t in_rank(uint32_t saddr, uint32_t rank) {
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
     return r;
 }
-__device__ __forceinline__ float2 ld_cluster_f32x2(uint32_t addr) {
-    float2 v;
-    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr));
+__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr));
     return v;
+}
+// One lane of the (converged) warp; what it issues keeps its operands in uniform registers.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, e;\n\t}" : "=r"(p));
+    return p != 0;
 }
 __device__ __forceinline__ void cp_async8(uint32_t dst, const void* src) {
     asm volatile("cp.async.ca.shared.global.L2::128B [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
@@ -242,8 +250,9 @@ __device__ __noinline__ float dot_direct(const LinearArgs& a, int64_t m, int64_t
 }
 
 // ---------------------------------------------------------------- product
-// D: cp.async groups in flight per producer thread (ring depth D + 1 at least).
-template <bool kGated, int D>
+// D: cp.async groups in flight per producer thread (the ring holds D + 1 stages at least);
+// SPLIT: CTAs of a cluster along K.
+template <bool kGated, int D, int SPLIT>
 __global__ void __launch_bounds__(kThreads)
 linear_few_kernel(const LinearArgs a, const Plan p, const uint8_t* __restrict__ ws_b, const uint8_t* __restrict__ ws_sfa) {
     extern __shared__ uint8_t smem_raw[];
@@ -252,15 +261,40 @@ linear_few_kernel(const LinearArgs a, const Plan p, const uint8_t* __restrict__ 
     __shared__ uint64_t full_a[kMaxStages], full_b[kMaxStages], empty[kMaxStages], done[1];
     __shared__ uint32_t s_tmem;
     __shared__ volatile int s_abort, s_never;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0), lane = tid & 31;
     const int NS = p.stages;
-    const uint32_t rank = ctarank();
-    const int64_t f = blockIdx.x / p.split;
+    const int rank = SPLIT > 1 ? static_cast<int>(ctarank()) : 0;
+    const int64_t f = blockIdx.x / SPLIT;
     const int64_t tt = blockIdx.y;
-    // this CTA's K stages [j0, j0 + n); the launch keeps split <= nk, so n >= 1
-    const int j0 = static_cast<int>(rank) * p.nk / p.split;
-    const int n = (static_cast<int>(rank) + 1) * p.nk / p.split - j0;
-    if (tid == 0) {
+    // this CTA's K stages [j0, j0 + n); the launch keeps SPLIT <= nk, so n >= 1
+    const int j0 = rank * p.nk / SPLIT;
+    const int n = (rank + 1) * p.nk / SPLIT - j0;
+    constexpr int kFeat = kGated ? 64 : kBM;     // output features of the tile
+
+    // Codes: producer warp w brings rows 32 w .. 32 w + 31 of the tile; one copy of the warp
+    // is 4 rows x 64 bytes, 8 bytes (16 elements) into the low half of a 16-byte container;
+    // containers are swizzled within the row's 128 bytes.
+    const int c8 = lane & 7, r8 = lane >> 3;
+    const int64_t row0 = f * kFeat + (kGated ? 32 * (warp & 1) : 32 * warp) + r8;
+    const int64_t left = (kGated ? a.n_out : a.N) - row0;   // rows from row0 on
+    const uint8_t* src = a.codes + (row0 + (kGated && warp >= 2 ? a.n_out : 0)) * (a.K / 2) + 64LL * j0 + 8 * c8;
+    const int rows = left <= 0 ? 0 : left > 28 ? 8 : static_cast<int>(left + 3) / 4;   // copies 4 rows apart
+    const int k_left = static_cast<int>(a.K - static_cast<int64_t>(j0) * kBK) - 16 * c8;
+    const uint32_t to = smem_u32(smem) + (32 * warp + r8) * kBK + ((c8 ^ r8) << 4);
+    auto bring = [&](int i) {
+        const uint32_t dst = to + (i % NS) * p.stage_bytes;
+        if (i * kBK < k_left) {
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+                if (q < rows) cp_async8((dst + 512 * q) ^ (q & 1 ? 64u : 0u), src + q * 2 * a.K + 64 * i);
+        }
+        cp_async_commit();
+    };
+    // the first stages need no barrier: their copies start before anything else
+    if (warp < 4) {
+        for (int i = 0; i < min(n, D); ++i) bring(i);
+    }
+    if (tid == 128) {
         for (int s = 0; s < NS; ++s) {
             mbar_init(&full_a[s], 4);   // one arrival per producer warp
             mbar_init(&full_b[s], 1);
@@ -281,47 +315,36 @@ linear_few_kernel(const LinearArgs a, const Plan p, const uint8_t* __restrict__ 
     const uint32_t tmem = s_tmem;
 
     if (warp < 4) {
-        // ---------------- codes: warp w brings rows 32 w .. 32 w + 31; a warp's copy is 4 rows x 64
-        // bytes; 16 elements (8 bytes) per container, swizzled in 16-byte chunks
-        const int c = lane & 7;                       // container of the row
-        const uint8_t* src[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int64_t row = weight_row<kGated>(a, f, 32 * warp + 4 * i + (lane >> 3));
-            src[i] = row < 0 ? nullptr : a.codes + row * (a.K / 2) + 8 * c;
-        }
+        // ---------------- codes
         bool ok = true;
         auto finish = [&](int i) {   // stage i has landed for this thread
             fence_async_proxy();
             __syncwarp();
             if (lane == 0) mbar_arrive(&full_a[i % NS]);
         };
-        int i = 0;
-        for (; i < n; ++i) {
-            const int s = i % NS;
-            if (!__all_sync(0xFFFFFFFFu, mbar_wait(&empty[s], ((i / NS) & 1) ^ 1, &s_abort))) { ok = false; break; }
-            const uint32_t dst = smem_u32(smem + s * p.stage_bytes);
-            const int64_t k = static_cast<int64_t>(j0 + i) * kBK;
-            if (k + 16 * c < a.K) {
-#pragma unroll
-                for (int q = 0; q < 8; ++q) {
-                    const int r = 32 * warp + 4 * q + (lane >> 3);
-                    if (src[q]) cp_async8(dst + r * kBK + ((c ^ (r & 7)) << 4), src[q] + k / 2);
-                }
+        for (int i = D; i < n; ++i) {
+            if (i >= NS && !__all_sync(0xFFFFFFFFu, mbar_wait_spin(&empty[i % NS], ((i / NS) & 1) ^ 1, &s_abort))) {
+                ok = false;
+                break;
             }
-            cp_async_commit();
-            if (i >= D) {
-                cp_async_wait<D>();
-                finish(i - D);
-            }
+            bring(i);
+            cp_async_wait<D>();
+            finish(i - D);
         }
-        cp_async_wait<0>();
         if (ok) {
-            for (int d = n > D ? n - D : 0; d < n; ++d) finish(d);
+            for (int d = n > D ? n - D : 0; d < n; ++d) {
+                // the n - 1 - d youngest groups may still be in flight
+                if (n - 1 - d >= 3) cp_async_wait<3>();
+                else if (n - 1 - d == 2) cp_async_wait<2>();
+                else if (n - 1 - d == 1) cp_async_wait<1>();
+                else cp_async_wait<0>();
+                finish(d);
+            }
         } else {
             s_abort = 1;
             record_status(a.status, MXFP4_ERR_TIMEOUT);
         }
+        cp_async_wait<0>();
     } else if (warp == 4) {
         // ---------------- prepared activations and scales
         if (lane == 0) {
@@ -330,7 +353,7 @@ linear_few_kernel(const LinearArgs a, const Plan p, const uint8_t* __restrict__ 
             bool ok = true;
             for (int i = 0; i < n; ++i, ++issued) {
                 const int s = i % NS;
-                if (!mbar_wait(&empty[s], ((i / NS) & 1) ^ 1, &s_abort)) { ok = false; break; }
+                if (!mbar_wait_spin(&empty[s], ((i / NS) & 1) ^ 1, &s_abort)) { ok = false; break; }
                 uint8_t* dst = smem + s * p.stage_bytes + kABytes;
                 mbar_arrive_expect_tx(&full_b[s], static_cast<uint32_t>(p.b_bytes + kAtom));
                 bulk_load(dst, ws_b + (tt * p.nk + j0 + i) * p.b_bytes, static_cast<uint32_t>(p.b_bytes), &full_b[s]);
@@ -344,38 +367,45 @@ linear_few_kernel(const LinearArgs a, const Plan p, const uint8_t* __restrict__ 
             }
         }
     } else if (warp == 5) {
-        // ---------------- MMA issuer
-        if (lane == 0) {
-            bool ok = true;
-            const int nn = p.stacked ? 2 * p.mp : p.mp;
-            for (int i = 0; i < n; ++i) {
-                const int s = i % NS;
-                if (!mbar_wait(&full_a[s], (i / NS) & 1, &s_abort) || !mbar_wait(&full_b[s], (i / NS) & 1, &s_abort)) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
-                fence_async_proxy();
-                const uint32_t wa = smem_u32(smem + s * p.stage_bytes), xb = wa + kABytes;
-                const uint32_t sf = xb + 2 * p.mp * kBK;      // hi (and lo) scale atoms, then the weights'
-                const uint32_t set = tmem + kSfCol + 16 * (i & 1);
-                tmem_cp_32x128b_x4(set, rows16_desc(xb + p.b_bytes));
-                tmem_cp_32x128b_x4(set + 4, rows16_desc(sf));
-                if (!p.stacked) tmem_cp_32x128b_x4(set + 8, rows16_desc(sf + kAtom));
-                const int64_t k0 = static_cast<int64_t>(j0 + i) * kBK;
-                const int steps = static_cast<int>(min(static_cast<int64_t>(4), (a.K - k0) / 32));
-                for (int q = 0; q < steps; ++q) {
-                    const uint32_t id = static_cast<uint32_t>(q);
-                    const uint32_t idesc = idesc_mxf8(nn, id);
-                    const uint64_t da = sw128_desc(wa + 32 * q);
-                    mma_mxf8f6f4(tmem, da, sw128_desc(xb + 32 * q), idesc, set | (id << 30), (set + 4) | (id << 30),
-                                 (i | q) != 0 ? 1u : 0u);
-                    if (!p.stacked)
-                        mma_mxf8f6f4(tmem, da, sw128_desc(xb + p.mp * kBK + 32 * q), idesc, set | (id << 30),
-                                     (set + 8) | (id << 30), 1u);
+        // ---------------- MMA issuer (the whole warp walks the loop, one lane issues)
+        bool ok = true;
+        const bool lead = elect_one();
+        const uint32_t idesc = idesc_mxf8(p.stacked ? 2 * p.mp : p.mp, 0);
+        constexpr uint32_t kNextId = (1u << 4) | (1u << 29);
+        const int k_all = static_cast<int>(a.K - static_cast<int64_t>(j0) * kBK);
+        const uint32_t b_lo = static_cast<uint32_t>(p.mp * kBK) >> 4;          // lo rows behind the hi rows
+        const uint32_t sf_at = kABytes + 2 * p.mp * kBK, sfa_at = kABytes + p.b_bytes;
+        for (int i = 0; i < n; ++i) {
+            const int s = i % NS;
+            const uint32_t ph = (i / NS) & 1;
+            if (!__all_sync(0xFFFFFFFFu, mbar_wait_spin(&full_b[s], ph, &s_abort) && mbar_wait_spin(&full_a[s], ph, &s_abort))) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            const uint32_t st = smem_u32(smem) + s * p.stage_bytes;
+            const uint32_t set = tmem + kSfCol + 16 * (i & 1);
+            const uint64_t da = sw128_desc(st), db = sw128_desc(st + kABytes);
+            const int steps = (k_all - i * kBK) / 32;
+            if (lead) {
+                tmem_cp_32x128b_x4(set, rows16_desc(st + sfa_at));
+                tmem_cp_32x128b_x4(set + 4, rows16_desc(st + sf_at));
+                if (!p.stacked) tmem_cp_32x128b_x4(set + 8, rows16_desc(st + sf_at + kAtom));
+#pragma unroll
+                for (uint32_t q = 0; q < 4; ++q) {   // 32 elements of K per MMA, scale q of the stage
+                    if (static_cast<int>(q) < steps) {
+                        mma_mxf8f6f4(tmem, da + 2 * q, db + 2 * q, idesc + q * kNextId, set | (q << 30),
+                                     (set + 4) | (q << 30), q == 0 && i == 0 ? 0u : 1u);
+                        if (!p.stacked)
+                            mma_mxf8f6f4(tmem, da + 2 * q, db + b_lo + 2 * q, idesc + q * kNextId, set | (q << 30),
+                                         (set + 8) | (q << 30), 1u);
+                    }
                 }
                 tc_commit(&empty[s]);
             }
+            __syncwarp();
+        }
+        if (lead) {
             if (!ok) {
                 s_abort = 1;
                 record_status(a.status, MXFP4_ERR_TIMEOUT);
@@ -386,7 +416,7 @@ linear_few_kernel(const LinearArgs a, const Plan p, const uint8_t* __restrict__ 
     __syncwarp();
 
     // ---------------- partial sums -> shared memory [token][128 rows] (the idle ring)
-    const bool got = mbar_wait(done, 0, &s_never);
+    const bool got = mbar_wait(done, 0, &s_never);   // suspends: a spinning warp slows the issuer
     if (!__all_sync(0xFFFFFFFFu, got)) {
         s_abort = 1;
         record_status(a.status, MXFP4_ERR_TIMEOUT);
@@ -399,7 +429,7 @@ linear_few_kernel(const LinearArgs a, const Plan p, const uint8_t* __restrict__ 
     {
         const int q = warp & 3;
         const uint32_t base = tmem + (static_cast<uint32_t>(q * 32) << 16);
-        const int row = 32 * q + lane;
+        float* to_row = part + 32 * q + lane;
         for (int c = 8 * (warp >> 2); c < mt; c += 16) {
             uint32_t v[8], w[8];
             tmem_ld_x8(base + c, v);
@@ -409,78 +439,92 @@ linear_few_kernel(const LinearArgs a, const Plan p, const uint8_t* __restrict__ 
             for (int j = 0; j < 8; ++j) {
                 float z = __uint_as_float(v[j]);
                 if (p.stacked) z += __uint_as_float(w[j]);
-                part[(c + j) * kBM + row] = z;
+                to_row[(c + j) * kBM] = z;
             }
         }
     }
     __syncwarp();
-    if (p.split > 1) cluster_sync_all(); else __syncthreads();
+    if (SPLIT > 1) cluster_sync_all(); else __syncthreads();
 
-    // ---------------- each CTA finishes its share of the tokens, two features per thread
+    // ---------------- each CTA finishes its share of the tokens, four features per thread;
+    // the loads of kBatch tokens from every CTA of the cluster are in flight together
     {
-        constexpr int kPairs = kGated ? 32 : 64;
-        const int c0 = static_cast<int>(rank) * mt / p.split, c1 = (static_cast<int>(rank) + 1) * mt / p.split;
-        const int pr = tid % kPairs;
-        const int64_t n0 = f * (2 * kPairs) + 2 * pr;
-        const uint32_t mine = smem_u32(part);
-        const bool even = a.n_out % 2 == 0;
-        float bz[2] = {0.f, 0.f}, bu[2] = {0.f, 0.f};
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            if (n0 + j < a.n_out) {
-                bz[j] = bias_at(a, n0 + j);
-                if (kGated) bu[j] = bias_at(a, n0 + j + a.n_out);
-            }
-        }
+        constexpr int kQuads = kFeat / 4, kStep = kThreads / kQuads;
+        constexpr int kBatch = SPLIT >= 4 ? 1 : 4 / SPLIT;
+        const int c0 = rank * mt / SPLIT, c1 = (rank + 1) * mt / SPLIT;
+        const int qd = tid % kQuads;
+        const int64_t n0 = f * kFeat + 4 * qd;
+        const uint32_t mine = smem_u32(part) + 16 * qd;
+        const bool vec = a.n_out % 4 == 0;
         const uint16_t* res = static_cast<const uint16_t*>(a.residual);
         uint16_t* y = static_cast<uint16_t*>(a.y);
-        for (int c = c0 + tid / kPairs; c < c1; c += kThreads / kPairs) {
-            if (n0 >= a.n_out) break;
-            float z[2] = {0.f, 0.f}, u[2] = {0.f, 0.f};
-            const uint32_t off = mine + (c * kBM + 2 * pr) * 4;
-            float2 v[kMaxCluster], w[kMaxCluster];
+        float bz[4], bu[4];
 #pragma unroll
-            for (int q = 0; q < kMaxCluster; ++q) {
-                if (q < p.split) {
-                    v[q] = ld_cluster_f32x2(in_rank(off, q));
-                    if (kGated) w[q] = ld_cluster_f32x2(in_rank(off + 64 * 4, q));
-                }
-            }
+        for (int j = 0; j < 4; ++j) {
+            const bool in = n0 + j < a.n_out;
+            bz[j] = in ? bias_at(a, n0 + j) : 0.f;
+            bu[j] = kGated && in ? bias_at(a, n0 + j + a.n_out) : 0.f;
+        }
+        if (n0 < a.n_out) {
+            for (int c = c0 + tid / kQuads; c < c1; c += kBatch * kStep) {
+                float4 v[kBatch][SPLIT], w[kBatch][SPLIT];
+                uint2 r[kBatch];
 #pragma unroll
-            for (int q = 0; q < kMaxCluster; ++q) {
-                if (q < p.split) {
-                    z[0] += v[q].x;
-                    z[1] += v[q].y;
-                    if (kGated) {
-                        u[0] += w[q].x;
-                        u[1] += w[q].y;
+                for (int b = 0; b < kBatch; ++b) {
+                    const int cc = c + b * kStep;
+                    if (cc < c1) {
+#pragma unroll
+                        for (int q = 0; q < SPLIT; ++q) {
+                            const uint32_t at = mine + cc * (kBM * 4);
+                            const uint32_t from = SPLIT > 1 ? in_rank(at, q) : at;
+                            v[b][q] = ld_cluster_f32x4(from);
+                            if (kGated) w[b][q] = ld_cluster_f32x4(from + 64 * 4);
+                        }
+                        if (res && vec) r[b] = *reinterpret_cast<const uint2*>(res + (t0 + cc) * a.n_out + n0);
                     }
                 }
-            }
-            const int64_t m = t0 + c;
-            float out[2];
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                if (n0 + j < a.n_out) {
-                    if (z[j] != z[j]) z[j] = dot_direct(a, m, n0 + j);
-                    if (kGated && u[j] != u[j]) u[j] = dot_direct(a, m, n0 + j + a.n_out);
-                }
-                out[j] = activate(kGated ? static_cast<int>(MXFP4_ACT_SWIGLU) : a.act, z[j] + bz[j], u[j] + bu[j]);
-            }
-            const int64_t at = m * a.n_out + n0;
-            if (even) {
-                if (res) {
-                    const uint32_t r = *reinterpret_cast<const uint32_t*>(res + at);
-                    out[0] += bf16_lo(r);
-                    out[1] += bf16_hi(r);
-                }
-                *reinterpret_cast<uint32_t*>(y + at) = pack_bf16(out[0], out[1]);
-            } else {
+                for (int b = 0; b < kBatch; ++b) {
+                    const int cc = c + b * kStep;
+                    if (cc >= c1) break;
+                    const int64_t m = t0 + cc, at = m * a.n_out + n0;
+                    float z[4] = {v[b][0].x, v[b][0].y, v[b][0].z, v[b][0].w};
+                    float u[4] = {0.f, 0.f, 0.f, 0.f};
+                    if (kGated) u[0] = w[b][0].x, u[1] = w[b][0].y, u[2] = w[b][0].z, u[3] = w[b][0].w;
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    if (n0 + j < a.n_out) {
-                        if (res) out[j] += __uint_as_float(static_cast<uint32_t>(res[at + j]) << 16);
-                        y[at + j] = static_cast<uint16_t>(pack_bf16(out[j], out[j]));
+                    for (int q = 1; q < SPLIT; ++q) {
+                        z[0] += v[b][q].x, z[1] += v[b][q].y, z[2] += v[b][q].z, z[3] += v[b][q].w;
+                        if (kGated) u[0] += w[b][q].x, u[1] += w[b][q].y, u[2] += w[b][q].z, u[3] += w[b][q].w;
+                    }
+                    bool nan = false;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) nan |= z[j] != z[j] || u[j] != u[j];
+                    if (nan) {
+                        for (int j = 0; j < 4; ++j) {
+                            if (n0 + j < a.n_out) {
+                                z[j] = dot_direct(a, m, n0 + j);
+                                if (kGated) u[j] = dot_direct(a, m, n0 + j + a.n_out);
+                            }
+                        }
+                    }
+                    float o[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        o[j] = activate(kGated ? static_cast<int>(MXFP4_ACT_SWIGLU) : a.act, z[j] + bz[j], u[j] + bu[j]);
+                    if (vec) {
+                        if (res) {
+                            o[0] += bf16_lo(r[b].x), o[1] += bf16_hi(r[b].x);
+                            o[2] += bf16_lo(r[b].y), o[3] += bf16_hi(r[b].y);
+                        }
+                        *reinterpret_cast<uint2*>(y + at) = make_uint2(pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]));
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            if (n0 + j < a.n_out) {
+                                if (res) o[j] += __uint_as_float(static_cast<uint32_t>(res[at + j]) << 16);
+                                y[at + j] = static_cast<uint16_t>(pack_bf16(o[j], o[j]));
+                            }
+                        }
                     }
                 }
             }
@@ -488,7 +532,7 @@ linear_few_kernel(const LinearArgs a, const Plan p, const uint8_t* __restrict__ 
     }
     __syncwarp();
     tc_fence_before();
-    if (p.split > 1) cluster_sync_all();   // the partials are read: their CTAs may end
+    if (SPLIT > 1) cluster_sync_all();   // the partials are read: their CTAs may end
     __syncthreads();
     if (warp == 6) {
         tc_fence_after();
@@ -521,10 +565,10 @@ size_t linear_few_ws_bytes(int64_t M, int64_t K, int64_t n_out, bool gated) {
 
 namespace {
 
-template <bool kGated, int D>
+template <bool kGated, int D, int SPLIT>
 cudaError_t launch_product(const LinearArgs& a, const Plan& p, const uint8_t* ws_b, const uint8_t* ws_sfa,
                            cudaStream_t stream) {
-    auto kern = linear_few_kernel<kGated, D>;
+    auto kern = linear_few_kernel<kGated, D, SPLIT>;
     const int part = p.mp * kBM * 4;
     int smem = p.stages * p.stage_bytes;
     smem = (smem > part ? smem : part) + 1024;
@@ -545,6 +589,17 @@ cudaError_t launch_product(const LinearArgs& a, const Plan& p, const uint8_t* ws
     cfg.attrs = attr;
     cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, kern, a, p, ws_b, ws_sfa);
+}
+
+template <bool kGated, int D>
+cudaError_t launch_product(const LinearArgs& a, const Plan& p, const uint8_t* ws_b, const uint8_t* ws_sfa,
+                           cudaStream_t stream) {
+    switch (p.split) {
+        case 1: return launch_product<kGated, D, 1>(a, p, ws_b, ws_sfa, stream);
+        case 2: return launch_product<kGated, D, 2>(a, p, ws_b, ws_sfa, stream);
+        case 4: return launch_product<kGated, D, 4>(a, p, ws_b, ws_sfa, stream);
+        default: return launch_product<kGated, D, 8>(a, p, ws_b, ws_sfa, stream);
+    }
 }
 
 template <bool kGated>
