@@ -153,6 +153,20 @@ mxfp4_status encode_w16_map(CUtensorMap* m, const void* w, int64_t K, int64_t ro
     return r == CUDA_SUCCESS ? MXFP4_OK : cuda_fail(cudaErrorInvalidValue);
 }
 
+// Packed codes {K/2 bytes, rows} as they lie; box {128, box_rows}, not swizzled.
+mxfp4_status encode_rows_map(CUtensorMap* m, const uint8_t* codes, int64_t K, int64_t rows, int box_rows) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return cuda_fail(cudaErrorNotSupported);
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(K / 2), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(K / 2)};
+    const cuuint32_t box[2] = {128, static_cast<cuuint32_t>(box_rows)};
+    const cuuint32_t estr[2] = {1, 1};
+    CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(codes), dims, strides,
+                    box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? MXFP4_OK : cuda_fail(cudaErrorInvalidValue);
+}
+
 size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
 // Workspace of moe_mxfp4_mlp, carved in this order (256-byte aligned pieces).
@@ -562,7 +576,9 @@ mxfp4_status mxfp4_linear(const void* x_bf16, int64_t M, int64_t K, const uint8_
             return cuda_fail(e);
         e = mx::launch_linear_many(a, tx, tw, nt, d->sm_count, s);
     } else {
-        e = mx::launch_linear_few(a, ws, d->sm_count, s);
+        CUtensorMap tc;
+        if ((st = encode_rows_map(&tc, w_codes, K, N, act == MXFP4_ACT_SWIGLU ? 64 : 128)) != MXFP4_OK) return st;
+        e = mx::launch_linear_few(a, tc, ws, d->sm_count, s);
     }
     return e == cudaSuccess ? MXFP4_OK : cuda_fail(e);
 }

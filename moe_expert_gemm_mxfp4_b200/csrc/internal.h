@@ -104,7 +104,8 @@ cudaError_t launch_combine(const void* y_sorted, const int32_t* inv, int64_t T, 
 size_t route_scored_ws_bytes(int64_t T, int64_t E);
 cudaError_t launch_route_scored(const RouteScoredArgs& a, bool bf16, cudaStream_t stream);
 size_t linear_few_ws_bytes(int64_t M, int64_t K, int64_t n_out, bool gated);
-cudaError_t launch_linear_few(const LinearArgs& a, void* ws, int sm_count, cudaStream_t stream);
+cudaError_t launch_linear_few(const LinearArgs& a, const CUtensorMap& tmap_codes, void* ws, int sm_count,
+                              cudaStream_t stream);
 int linear_many_cols(int64_t M, int64_t n_out, bool gated, int sm_count);   // columns of a work tile
 cudaError_t launch_linear_many(const LinearArgs& a, const CUtensorMap& tmap_x, const CUtensorMap& tmap_w, int nt,
                                int sm_count, cudaStream_t stream);

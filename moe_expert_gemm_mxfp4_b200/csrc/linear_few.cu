@@ -17,8 +17,9 @@
 //   linear_few_prepare  x -> hi and lo tiles in the tensor core's shared-memory image, their
 //                       scales and the weights' scales in its scale-factor layout;
 //   linear_few          one CTA per (128 weight rows, K range, token tile).
-// Roles (8 warps): warps 0-3 bring the codes with 8-byte cp.async straight into the 16-element
-// containers that the tensor core takes (8 bytes of codes, 8 of padding); warp 4 bulk-copies
+// Roles (8 warps): warp 7 streams packed codes (TMA, 128 bytes per row) into a ring of their own;
+// warps 0-3 spread them over the 16-element containers that the tensor core takes (8
+// bytes of codes, 8 of padding), three instructions per 16 bytes; warp 4 bulk-copies
 // the prepared tiles; warp 5 issues scale copies and MMAs.  The CTAs of a cluster split K and sum
 // their partial results through distributed shared memory in rank order (the same on every
 // run); each finishes a share of the tokens.
@@ -40,7 +41,9 @@ constexpr int kBK = 128;             // K per stage: 128 one-byte containers per
 constexpr int kABytes = kBM * kBK;
 constexpr int kAtom = 512;           // scale atom: 128 rows x 4 scales
 constexpr int kMaxMp = 128;          // tokens per tile
-constexpr int kMaxStages = 8;
+constexpr int kMaxStages = 4;
+constexpr int kCodeBytes = kBM * 128;   // a code slot: 128 bytes (two stages) of each row
+constexpr int kMaxSlots = 4;
 constexpr int kSmemSm = 228 * 1024;  // per SM, 1 KB of it taken by each resident CTA
 constexpr int kMaxCluster = 8;
 constexpr uint32_t kTmemCols = 256, kSfCol = 128;   // D [0, 128), scale sets of 16 columns behind it
@@ -58,6 +61,14 @@ __device__ __forceinline__ uint32_t in_rank(uint32_t saddr, uint32_t rank) {
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
     return r;
 }
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+    return v;
+}
+__device__ __forceinline__ void sts64(uint32_t addr, uint32_t x, uint32_t y) {
+    asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(x), "r"(y) : "memory");
+}
 __device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
     float4 v;
     asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
@@ -70,14 +81,6 @@ __device__ __forceinline__ bool elect_one() {
     uint32_t p;
     asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, e;\n\t}" : "=r"(p));
     return p != 0;
-}
-__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src) {
-    asm volatile("cp.async.ca.shared.global.L2::128B [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 __device__ __forceinline__ void fence_async_proxy() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
@@ -129,7 +132,8 @@ struct Plan {
     int w_tiles;       // tiles of 128 weight rows
     int split;         // CTAs of a cluster along K
     int nk;            // K stages
-    int stages;        // ring depth
+    int stages;        // ring of stages (containers, activations, scales)
+    int slots;         // ring of packed codes
     int b_bytes;       // prepared bytes per token tile and stage: hi and lo rows, scale atoms
     int stage_bytes;
 };
@@ -250,19 +254,20 @@ __device__ __noinline__ float dot_direct(const LinearArgs& a, int64_t m, int64_t
 }
 
 // ---------------------------------------------------------------- product
-// D: cp.async groups in flight per producer thread (the ring holds D + 1 stages at least);
 // SPLIT: CTAs of a cluster along K.
-template <bool kGated, int D, int SPLIT>
+template <bool kGated, int SPLIT>
 __global__ void __launch_bounds__(kThreads)
-linear_few_kernel(const LinearArgs a, const Plan p, const uint8_t* __restrict__ ws_b, const uint8_t* __restrict__ ws_sfa) {
+linear_few_kernel(const __grid_constant__ CUtensorMap tmap_codes, const LinearArgs a, const Plan p,
+                  const uint8_t* __restrict__ ws_b, const uint8_t* __restrict__ ws_sfa) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~static_cast<uintptr_t>(1023));
     __shared__ uint64_t full_a[kMaxStages], full_b[kMaxStages], empty[kMaxStages], done[1];
+    __shared__ uint64_t code_full[kMaxSlots], code_empty[kMaxSlots];
     __shared__ uint32_t s_tmem;
     __shared__ volatile int s_abort, s_never;
     const int tid = threadIdx.x, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0), lane = tid & 31;
-    const int NS = p.stages;
+    const int NS = p.stages, CS = p.slots;
     const int rank = SPLIT > 1 ? static_cast<int>(ctarank()) : 0;
     const int64_t f = blockIdx.x / SPLIT;
     const int64_t tt = blockIdx.y;
@@ -270,33 +275,15 @@ linear_few_kernel(const LinearArgs a, const Plan p, const uint8_t* __restrict__ 
     const int j0 = rank * p.nk / SPLIT;
     const int n = (rank + 1) * p.nk / SPLIT - j0;
     constexpr int kFeat = kGated ? 64 : kBM;     // output features of the tile
+    uint8_t* codes = smem + NS * p.stage_bytes;  // the code slots lie behind the stages
 
-    // Codes: producer warp w brings rows 32 w .. 32 w + 31 of the tile; one copy of the warp
-    // is 4 rows x 64 bytes, 8 bytes (16 elements) into the low half of a 16-byte container;
-    // containers are swizzled within the row's 128 bytes.
-    const int c8 = lane & 7, r8 = lane >> 3;
-    const int64_t row0 = f * kFeat + (kGated ? 32 * (warp & 1) : 32 * warp) + r8;
-    const int64_t left = (kGated ? a.n_out : a.N) - row0;   // rows from row0 on
-    const uint8_t* src = a.codes + (row0 + (kGated && warp >= 2 ? a.n_out : 0)) * (a.K / 2) + 64LL * j0 + 8 * c8;
-    const int rows = left <= 0 ? 0 : left > 28 ? 8 : static_cast<int>(left + 3) / 4;   // copies 4 rows apart
-    const int k_left = static_cast<int>(a.K - static_cast<int64_t>(j0) * kBK) - 16 * c8;
-    const uint32_t to = smem_u32(smem) + (32 * warp + r8) * kBK + ((c8 ^ r8) << 4);
-    auto bring = [&](int i) {
-        const uint32_t dst = to + (i % NS) * p.stage_bytes;
-        if (i * kBK < k_left) {
-#pragma unroll
-            for (int q = 0; q < 8; ++q)
-                if (q < rows) cp_async8((dst + 512 * q) ^ (q & 1 ? 64u : 0u), src + q * 2 * a.K + 64 * i);
+    if (tid == 7 * 32) {
+        for (int s = 0; s < CS; ++s) {
+            mbar_init(&code_full[s], 1);
+            mbar_init(&code_empty[s], 4);   // one arrival per spreading warp
         }
-        cp_async_commit();
-    };
-    // the first stages need no barrier: their copies start before anything else
-    if (warp < 4) {
-        for (int i = 0; i < min(n, D); ++i) bring(i);
-    }
-    if (tid == 128) {
         for (int s = 0; s < NS; ++s) {
-            mbar_init(&full_a[s], 4);   // one arrival per producer warp
+            mbar_init(&full_a[s], 4);
             mbar_init(&full_b[s], 1);
             mbar_init(&empty[s], 1);
         }
@@ -304,6 +291,22 @@ linear_few_kernel(const LinearArgs a, const Plan p, const uint8_t* __restrict__ 
         s_abort = 0;
         s_never = 0;
         fence_mbar_init();
+    }
+    // code slot u % CS <- stages 2 u and 2 u + 1 of this CTA (past K: zero fill)
+    auto load_codes = [&](int u) {
+        uint8_t* dst = codes + u % CS * kCodeBytes;
+        const int x = 64 * j0 + 128 * u;
+        mbar_arrive_expect_tx(&code_full[u % CS], kCodeBytes);
+        if (kGated) {
+            tma_load_2d(dst, &tmap_codes, &code_full[u % CS], x, static_cast<int>(f * 64));
+            tma_load_2d(dst + kCodeBytes / 2, &tmap_codes, &code_full[u % CS], x, static_cast<int>(a.n_out + f * 64));
+        } else {
+            tma_load_2d(dst, &tmap_codes, &code_full[u % CS], x, static_cast<int>(f * kBM));
+        }
+    };
+    const int slots_used = (n + 1) / 2;
+    if (tid == 7 * 32) {   // the first copies start before the other warps are ready
+        for (int u = 0; u < min(slots_used, CS); ++u) load_codes(u);
     }
     if (warp == 6) {
         tmem_alloc(&s_tmem, kTmemCols);
@@ -315,36 +318,53 @@ linear_few_kernel(const LinearArgs a, const Plan p, const uint8_t* __restrict__ 
     const uint32_t tmem = s_tmem;
 
     if (warp < 4) {
-        // ---------------- codes
+        // ---------------- codes -> containers: 16 bytes of codes of a row are containers 2 ch and
+        // 2 ch + 1, swizzled within the row's 128 bytes
+        const int ch = tid & 3, r = tid >> 2;
+        const uint32_t from = smem_u32(codes) + r * 128 + 16 * ch;
+        const uint32_t to = smem_u32(smem) + r * kBK + (((2 * ch) ^ (r & 7)) << 4);
         bool ok = true;
-        auto finish = [&](int i) {   // stage i has landed for this thread
-            fence_async_proxy();
+        for (int i = 0; i < n; ++i) {
+            const int u = i >> 1;
+            bool got = (i & 1) || mbar_wait_spin(&code_full[u % CS], (u / CS) & 1, &s_abort);
+            if (got && i >= NS) got = mbar_wait_spin(&empty[i % NS], ((i / NS) & 1) ^ 1, &s_abort);
+            if (!__all_sync(0xFFFFFFFFu, got)) { ok = false; break; }
+            const uint32_t src = from + u % CS * kCodeBytes + (i & 1) * 64, dst = to + i % NS * p.stage_bytes;
+            uint4 v[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) v[q] = lds128(src + q * 32 * 128);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                sts64(dst + q * 32 * kBK, v[q].x, v[q].y);
+                sts64((dst ^ 16u) + q * 32 * kBK, v[q].z, v[q].w);
+            }
+            fence_async_proxy();   // generic writes -> the tensor core's reads
             __syncwarp();
-            if (lane == 0) mbar_arrive(&full_a[i % NS]);
-        };
-        for (int i = D; i < n; ++i) {
-            if (i >= NS && !__all_sync(0xFFFFFFFFu, mbar_wait_spin(&empty[i % NS], ((i / NS) & 1) ^ 1, &s_abort))) {
-                ok = false;
-                break;
+            if (lane == 0) {
+                mbar_arrive(&full_a[i % NS]);
+                if ((i & 1) || i + 1 == n) mbar_arrive(&code_empty[u % CS]);
             }
-            bring(i);
-            cp_async_wait<D>();
-            finish(i - D);
         }
-        if (ok) {
-            for (int d = n > D ? n - D : 0; d < n; ++d) {
-                // the n - 1 - d youngest groups may still be in flight
-                if (n - 1 - d >= 3) cp_async_wait<3>();
-                else if (n - 1 - d == 2) cp_async_wait<2>();
-                else if (n - 1 - d == 1) cp_async_wait<1>();
-                else cp_async_wait<0>();
-                finish(d);
-            }
-        } else {
+        if (!ok) {
             s_abort = 1;
             record_status(a.status, MXFP4_ERR_TIMEOUT);
         }
-        cp_async_wait<0>();
+    } else if (warp == 7) {
+        // ---------------- packed codes
+        if (lane == 0) {
+            bool ok = true;
+            int u = min(slots_used, CS);
+            for (; u < slots_used; ++u) {
+                if (!mbar_wait(&code_empty[u % CS], ((u / CS) & 1) ^ 1, &s_abort)) { ok = false; break; }
+                load_codes(u);
+            }
+            if (!ok) {
+                s_abort = 1;
+                record_status(a.status, MXFP4_ERR_TIMEOUT);
+            }
+            // every slot's last copy lands before the slots are used again or the CTA ends
+            for (int w = u > CS ? u - CS : 0; w < u; ++w) mbar_wait(&code_full[w % CS], (w / CS) & 1, &s_never);
+        }
     } else if (warp == 4) {
         // ---------------- prepared activations and scales
         if (lane == 0) {
@@ -415,6 +435,33 @@ linear_few_kernel(const LinearArgs a, const Plan p, const uint8_t* __restrict__ 
     }
     __syncwarp();
 
+    // ---------------- the finish: each CTA of the cluster takes a share of the tokens, a thread four
+    // features of every kStep-th token.  What it adds to the sums is loaded while the last MMAs run.
+    const int64_t t0 = tt * p.mp;
+    const int mt = static_cast<int>(min(static_cast<int64_t>(p.mp), a.M - t0));
+    constexpr int kQuads = kFeat / 4, kStep = kThreads / kQuads;
+    constexpr int kBatch = SPLIT >= 4 ? 1 : 4 / SPLIT;   // tokens whose loads are in flight together
+    const int c0 = rank * mt / SPLIT, c1 = (rank + 1) * mt / SPLIT;
+    const int qd = tid % kQuads;
+    const int64_t n0 = f * kFeat + 4 * qd;
+    const bool vec = a.n_out % 4 == 0;
+    const uint16_t* res = static_cast<const uint16_t*>(a.residual);
+    float bz[4], bu[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const bool in = n0 + j < a.n_out;
+        bz[j] = in ? bias_at(a, n0 + j) : 0.f;
+        bu[j] = kGated && in ? bias_at(a, n0 + j + a.n_out) : 0.f;
+    }
+    uint2 r[kBatch];
+    auto load_res = [&](int c) {
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b)
+            if (res && vec && n0 < a.n_out && c + b * kStep < c1)
+                r[b] = *reinterpret_cast<const uint2*>(res + (t0 + c + b * kStep) * a.n_out + n0);
+    };
+    load_res(c0 + tid / kQuads);
+
     // ---------------- partial sums -> shared memory [token][128 rows] (the idle ring)
     const bool got = mbar_wait(done, 0, &s_never);   // suspends: a spinning warp slows the issuer
     if (!__all_sync(0xFFFFFFFFu, got)) {
@@ -424,8 +471,6 @@ linear_few_kernel(const LinearArgs a, const Plan p, const uint8_t* __restrict__ 
     tc_fence_after();
     __syncthreads();   // no copy into the ring is in flight: its last stage has been multiplied
     float* part = reinterpret_cast<float*>(smem);
-    const int64_t t0 = tt * p.mp;
-    const int mt = static_cast<int>(min(static_cast<int64_t>(p.mp), a.M - t0));
     {
         const int q = warp & 3;
         const uint32_t base = tmem + (static_cast<uint32_t>(q * 32) << 16);
@@ -446,29 +491,12 @@ linear_few_kernel(const LinearArgs a, const Plan p, const uint8_t* __restrict__ 
     __syncwarp();
     if (SPLIT > 1) cluster_sync_all(); else __syncthreads();
 
-    // ---------------- each CTA finishes its share of the tokens, four features per thread;
-    // the loads of kBatch tokens from every CTA of the cluster are in flight together
     {
-        constexpr int kQuads = kFeat / 4, kStep = kThreads / kQuads;
-        constexpr int kBatch = SPLIT >= 4 ? 1 : 4 / SPLIT;
-        const int c0 = rank * mt / SPLIT, c1 = (rank + 1) * mt / SPLIT;
-        const int qd = tid % kQuads;
-        const int64_t n0 = f * kFeat + 4 * qd;
         const uint32_t mine = smem_u32(part) + 16 * qd;
-        const bool vec = a.n_out % 4 == 0;
-        const uint16_t* res = static_cast<const uint16_t*>(a.residual);
         uint16_t* y = static_cast<uint16_t*>(a.y);
-        float bz[4], bu[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const bool in = n0 + j < a.n_out;
-            bz[j] = in ? bias_at(a, n0 + j) : 0.f;
-            bu[j] = kGated && in ? bias_at(a, n0 + j + a.n_out) : 0.f;
-        }
         if (n0 < a.n_out) {
             for (int c = c0 + tid / kQuads; c < c1; c += kBatch * kStep) {
                 float4 v[kBatch][SPLIT], w[kBatch][SPLIT];
-                uint2 r[kBatch];
 #pragma unroll
                 for (int b = 0; b < kBatch; ++b) {
                     const int cc = c + b * kStep;
@@ -480,7 +508,6 @@ linear_few_kernel(const LinearArgs a, const Plan p, const uint8_t* __restrict__ 
                             v[b][q] = ld_cluster_f32x4(from);
                             if (kGated) w[b][q] = ld_cluster_f32x4(from + 64 * 4);
                         }
-                        if (res && vec) r[b] = *reinterpret_cast<const uint2*>(res + (t0 + cc) * a.n_out + n0);
                     }
                 }
 #pragma unroll
@@ -527,6 +554,7 @@ linear_few_kernel(const LinearArgs a, const Plan p, const uint8_t* __restrict__ 
                         }
                     }
                 }
+                load_res(c + kBatch * kStep);
             }
         }
     }
@@ -565,17 +593,16 @@ size_t linear_few_ws_bytes(int64_t M, int64_t K, int64_t n_out, bool gated) {
 
 namespace {
 
-template <bool kGated, int D, int SPLIT>
-cudaError_t launch_product(const LinearArgs& a, const Plan& p, const uint8_t* ws_b, const uint8_t* ws_sfa,
-                           cudaStream_t stream) {
-    auto kern = linear_few_kernel<kGated, D, SPLIT>;
-    const int part = p.mp * kBM * 4;
-    int smem = p.stages * p.stage_bytes;
-    smem = (smem > part ? smem : part) + 1024;
+template <bool kGated, int SPLIT>
+cudaError_t launch_product(const CUtensorMap& tmap_codes, const LinearArgs& a, const Plan& p, const uint8_t* ws_b,
+                           const uint8_t* ws_sfa, cudaStream_t stream) {
+    auto kern = linear_few_kernel<kGated, SPLIT>;
+    const int part = p.mp * kBM * 4, ring = p.stages * p.stage_bytes + p.slots * kCodeBytes;
+    const int smem = (ring > part ? ring : part) + 1024;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(p.w_tiles * p.split), static_cast<unsigned>(p.t_tiles), 1);
+    cfg.gridDim = dim3(static_cast<unsigned>(p.w_tiles * SPLIT), static_cast<unsigned>(p.t_tiles), 1);
     cfg.blockDim = dim3(kThreads, 1, 1);
     cfg.dynamicSmemBytes = static_cast<size_t>(smem);
     cfg.stream = stream;
@@ -583,37 +610,32 @@ cudaError_t launch_product(const LinearArgs& a, const Plan& p, const uint8_t* ws
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = static_cast<unsigned>(p.split);
+    attr[1].val.clusterDim.x = static_cast<unsigned>(SPLIT);
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, kern, a, p, ws_b, ws_sfa);
-}
-
-template <bool kGated, int D>
-cudaError_t launch_product(const LinearArgs& a, const Plan& p, const uint8_t* ws_b, const uint8_t* ws_sfa,
-                           cudaStream_t stream) {
-    switch (p.split) {
-        case 1: return launch_product<kGated, D, 1>(a, p, ws_b, ws_sfa, stream);
-        case 2: return launch_product<kGated, D, 2>(a, p, ws_b, ws_sfa, stream);
-        case 4: return launch_product<kGated, D, 4>(a, p, ws_b, ws_sfa, stream);
-        default: return launch_product<kGated, D, 8>(a, p, ws_b, ws_sfa, stream);
-    }
+    return cudaLaunchKernelEx(&cfg, kern, tmap_codes, a, p, ws_b, ws_sfa);
 }
 
 template <bool kGated>
-cudaError_t launch_few(const LinearArgs& a, Plan p, void* ws, int sm_count, cudaStream_t stream) {
-    // ring depth and resident CTAs per SM: two where at least four stages then fit each
+cudaError_t launch_few(const LinearArgs& a, const CUtensorMap& tmap_codes, Plan p, void* ws, int sm_count,
+                       cudaStream_t stream) {
+    // Rings: three stages, then code slots (what is in flight from memory), then a fourth stage;
+    // two resident CTAs per SM where each then has three stages and two slots.
     const int fixed = 1024 + 1024 + 512;   // alignment slack, the system's share, static shared memory
+    auto fit = [&](int room) {
+        p.stages = 3;
+        p.slots = (room - p.stages * p.stage_bytes) / kCodeBytes;
+        if (p.slots > kMaxSlots) p.slots = kMaxSlots;
+        if (p.slots >= 2 && room - p.slots * kCodeBytes >= kMaxStages * p.stage_bytes) p.stages = kMaxStages;
+        return p.slots >= 2;
+    };
     int occ = 2;
-    p.stages = (kSmemSm / 2 - fixed) / p.stage_bytes;
-    if (p.stages < 4) {
+    if (!fit(kSmemSm / 2 - fixed)) {
         occ = 1;
-        p.stages = (kSmemSm - fixed) / p.stage_bytes;
+        if (!fit(kSmemSm - fixed)) return cudaErrorInvalidConfiguration;
     }
-    if (p.stages > 6) p.stages = 6;
-    if (p.stages < 4) return cudaErrorInvalidConfiguration;
     // K split over a cluster while the CTAs fit the SMs at once
     p.split = 1;
     while (p.split < kMaxCluster && 2 * p.split <= p.nk &&
@@ -630,16 +652,22 @@ cudaError_t launch_few(const LinearArgs& a, Plan p, void* ws, int sm_count, cuda
     if (xg > 4LL * sm_count) xg = 4LL * sm_count;
     linear_few_prepare_kernel<kGated><<<static_cast<unsigned>(p.w_tiles + xg), kThreads, rows_smem, stream>>>(a, p, ws_b, ws_sfa);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    return p.stages >= 5 ? launch_product<kGated, 4>(a, p, ws_b, ws_sfa, stream)
-                         : launch_product<kGated, 3>(a, p, ws_b, ws_sfa, stream);
+    switch (p.split) {
+        case 1: return launch_product<kGated, 1>(tmap_codes, a, p, ws_b, ws_sfa, stream);
+        case 2: return launch_product<kGated, 2>(tmap_codes, a, p, ws_b, ws_sfa, stream);
+        case 4: return launch_product<kGated, 4>(tmap_codes, a, p, ws_b, ws_sfa, stream);
+        default: return launch_product<kGated, 8>(tmap_codes, a, p, ws_b, ws_sfa, stream);
+    }
 }
 
 }  // namespace
 
-cudaError_t launch_linear_few(const LinearArgs& a, void* ws, int sm_count, cudaStream_t stream) {
+cudaError_t launch_linear_few(const LinearArgs& a, const CUtensorMap& tmap_codes, void* ws, int sm_count,
+                              cudaStream_t stream) {
     const bool gated = a.act == MXFP4_ACT_SWIGLU;
     const Plan p = make_plan(a.M, a.K, a.n_out, gated);
-    return gated ? launch_few<true>(a, p, ws, sm_count, stream) : launch_few<false>(a, p, ws, sm_count, stream);
+    return gated ? launch_few<true>(a, tmap_codes, p, ws, sm_count, stream)
+                 : launch_few<false>(a, tmap_codes, p, ws, sm_count, stream);
 }
 
 }  // namespace mx
