@@ -25,6 +25,12 @@ __device__ __forceinline__ float activate(int act, float z, float u) {
     }
 }
 
+// Four outputs.  One copy of this code per kernel: inlined at every element, the activations fill
+// the instruction cache, and a launch this short meets its code cold.
+static __device__ __noinline__ float4 activate4(int act, float4 z, float4 u) {
+    return make_float4(activate(act, z.x, u.x), activate(act, z.y, u.y), activate(act, z.z, u.z), activate(act, z.w, u.w));
+}
+
 __device__ __forceinline__ float bias_at(const LinearArgs& a, int64_t n) {
     if (!a.bias) return 0.f;
     return a.bias_f32 ? static_cast<const float*>(a.bias)[n]

@@ -262,7 +262,7 @@ linear_few_kernel(const __grid_constant__ CUtensorMap tmap_codes, const LinearAr
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~static_cast<uintptr_t>(1023));
-    __shared__ uint64_t full_a[kMaxStages], full_b[kMaxStages], empty[kMaxStages], done[1];
+    __shared__ uint64_t full[kMaxStages], empty[kMaxStages], done[1];
     __shared__ uint64_t code_full[kMaxSlots], code_empty[kMaxSlots];
     __shared__ uint32_t s_tmem;
     __shared__ volatile int s_abort, s_never;
@@ -283,8 +283,7 @@ linear_few_kernel(const __grid_constant__ CUtensorMap tmap_codes, const LinearAr
             mbar_init(&code_empty[s], 4);   // one arrival per spreading warp
         }
         for (int s = 0; s < NS; ++s) {
-            mbar_init(&full_a[s], 4);
-            mbar_init(&full_b[s], 1);
+            mbar_init(&full[s], 5);   // four spreading warps and the copies of warp 4
             mbar_init(&empty[s], 1);
         }
         mbar_init(done, 1);
@@ -341,7 +340,7 @@ linear_few_kernel(const __grid_constant__ CUtensorMap tmap_codes, const LinearAr
             fence_async_proxy();   // generic writes -> the tensor core's reads
             __syncwarp();
             if (lane == 0) {
-                mbar_arrive(&full_a[i % NS]);
+                mbar_arrive(&full[i % NS]);
                 if ((i & 1) || i + 1 == n) mbar_arrive(&code_empty[u % CS]);
             }
         }
@@ -369,21 +368,22 @@ linear_few_kernel(const __grid_constant__ CUtensorMap tmap_codes, const LinearAr
         // ---------------- prepared activations and scales
         if (lane == 0) {
             grid_wait();   // the prepare kernel's writes are complete
-            int issued = 0;
             bool ok = true;
-            for (int i = 0; i < n; ++i, ++issued) {
+            for (int i = 0; i < n; ++i) {
                 const int s = i % NS;
                 if (!mbar_wait_spin(&empty[s], ((i / NS) & 1) ^ 1, &s_abort)) { ok = false; break; }
                 uint8_t* dst = smem + s * p.stage_bytes + kABytes;
-                mbar_arrive_expect_tx(&full_b[s], static_cast<uint32_t>(p.b_bytes + kAtom));
-                bulk_load(dst, ws_b + (tt * p.nk + j0 + i) * p.b_bytes, static_cast<uint32_t>(p.b_bytes), &full_b[s]);
-                bulk_load(dst + p.b_bytes, ws_sfa + (f * p.nk + j0 + i) * kAtom, kAtom, &full_b[s]);
+                mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(p.b_bytes + kAtom));
+                bulk_load(dst, ws_b + (tt * p.nk + j0 + i) * p.b_bytes, static_cast<uint32_t>(p.b_bytes), &full[s]);
+                bulk_load(dst + p.b_bytes, ws_sfa + (f * p.nk + j0 + i) * kAtom, kAtom, &full[s]);
             }
             if (!ok) {
                 s_abort = 1;
                 record_status(a.status, MXFP4_ERR_TIMEOUT);
-                for (int i = issued > NS ? issued - NS : 0; i < issued; ++i)
-                    mbar_wait(&full_b[i % NS], (i / NS) & 1, &s_never);
+                // let the copies in flight land: no barrier counts them alone, so a millisecond, far
+                // longer than a copy takes
+                const uint64_t w0 = globaltimer_ns();
+                while (globaltimer_ns() - w0 < 1000000ull) {}
             }
         }
     } else if (warp == 5) {
@@ -398,7 +398,7 @@ linear_few_kernel(const __grid_constant__ CUtensorMap tmap_codes, const LinearAr
         for (int i = 0; i < n; ++i) {
             const int s = i % NS;
             const uint32_t ph = (i / NS) & 1;
-            if (!__all_sync(0xFFFFFFFFu, mbar_wait_spin(&full_b[s], ph, &s_abort) && mbar_wait_spin(&full_a[s], ph, &s_abort))) {
+            if (!__all_sync(0xFFFFFFFFu, mbar_wait_spin(&full[s], ph, &s_abort))) {
                 ok = false;
                 break;
             }
@@ -456,9 +456,20 @@ linear_few_kernel(const __grid_constant__ CUtensorMap tmap_codes, const LinearAr
     uint2 r[kBatch];
     auto load_res = [&](int c) {
 #pragma unroll
-        for (int b = 0; b < kBatch; ++b)
-            if (res && vec && n0 < a.n_out && c + b * kStep < c1)
-                r[b] = *reinterpret_cast<const uint2*>(res + (t0 + c + b * kStep) * a.n_out + n0);
+        for (int b = 0; b < kBatch; ++b) {
+            r[b] = make_uint2(0u, 0u);
+            if (res && c + b * kStep < c1) {
+                const uint16_t* at = res + (t0 + c + b * kStep) * a.n_out + n0;
+                if (vec) {
+                    if (n0 < a.n_out) r[b] = *reinterpret_cast<const uint2*>(at);
+                } else {
+                    uint32_t half[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) half[j] = n0 + j < a.n_out ? at[j] : 0u;
+                    r[b] = make_uint2(half[0] | half[1] << 16, half[2] | half[3] << 16);
+                }
+            }
+        }
     };
     load_res(c0 + tid / kQuads);
 
@@ -534,24 +545,22 @@ linear_few_kernel(const __grid_constant__ CUtensorMap tmap_codes, const LinearAr
                             }
                         }
                     }
-                    float o[4];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        o[j] = activate(kGated ? static_cast<int>(MXFP4_ACT_SWIGLU) : a.act, z[j] + bz[j], u[j] + bu[j]);
+                    float4 o = make_float4(z[0] + bz[0], z[1] + bz[1], z[2] + bz[2], z[3] + bz[3]);
+                    if (kGated || a.act != MXFP4_ACT_NONE)
+                        o = activate4(kGated ? static_cast<int>(MXFP4_ACT_SWIGLU) : a.act, o,
+                                      make_float4(u[0] + bu[0], u[1] + bu[1], u[2] + bu[2], u[3] + bu[3]));
+                    if (res) {
+                        o.x += bf16_lo(r[b].x), o.y += bf16_hi(r[b].x);
+                        o.z += bf16_lo(r[b].y), o.w += bf16_hi(r[b].y);
+                    }
+                    const uint2 out = make_uint2(pack_bf16(o.x, o.y), pack_bf16(o.z, o.w));
                     if (vec) {
-                        if (res) {
-                            o[0] += bf16_lo(r[b].x), o[1] += bf16_hi(r[b].x);
-                            o[2] += bf16_lo(r[b].y), o[3] += bf16_hi(r[b].y);
-                        }
-                        *reinterpret_cast<uint2*>(y + at) = make_uint2(pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]));
+                        *reinterpret_cast<uint2*>(y + at) = out;
                     } else {
+                        const uint32_t half[4] = {out.x, out.x >> 16, out.y, out.y >> 16};
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            if (n0 + j < a.n_out) {
-                                if (res) o[j] += __uint_as_float(static_cast<uint32_t>(res[at + j]) << 16);
-                                y[at + j] = static_cast<uint16_t>(pack_bf16(o[j], o[j]));
-                            }
-                        }
+                        for (int j = 0; j < 4; ++j)
+                            if (n0 + j < a.n_out) y[at + j] = static_cast<uint16_t>(half[j]);
                     }
                 }
                 load_res(c + kBatch * kStep);

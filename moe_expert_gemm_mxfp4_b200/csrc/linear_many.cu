@@ -116,12 +116,18 @@ __device__ __forceinline__ void finish32(const LinearArgs& a, int64_t m, int64_t
 #pragma unroll
     for (int j = 0; j < 32; j += 4) {
         const float4 b = *reinterpret_cast<const float4*>(bz + j);
-        const float4 c = kGated ? *reinterpret_cast<const float4*>(bu + j) : b;
-        const float bj[4] = {b.x, b.y, b.z, b.w}, cj[4] = {c.x, c.y, c.z, c.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            v[j + i] = activate(kGated ? static_cast<int>(MXFP4_ACT_SWIGLU) : a.act, __uint_as_float(z[j + i]) + bj[i],
-                                kGated ? __uint_as_float(u[j + i]) + cj[i] : 0.f);
+        float4 o = make_float4(__uint_as_float(z[j]) + b.x, __uint_as_float(z[j + 1]) + b.y,
+                               __uint_as_float(z[j + 2]) + b.z, __uint_as_float(z[j + 3]) + b.w);
+        if (kGated) {
+            const float4 c = *reinterpret_cast<const float4*>(bu + j);
+            o.x = activate(MXFP4_ACT_SWIGLU, o.x, __uint_as_float(u[j]) + c.x);
+            o.y = activate(MXFP4_ACT_SWIGLU, o.y, __uint_as_float(u[j + 1]) + c.y);
+            o.z = activate(MXFP4_ACT_SWIGLU, o.z, __uint_as_float(u[j + 2]) + c.z);
+            o.w = activate(MXFP4_ACT_SWIGLU, o.w, __uint_as_float(u[j + 3]) + c.w);
+        } else if (a.act != MXFP4_ACT_NONE) {
+            o = activate4(a.act, o, o);
+        }
+        v[j] = o.x, v[j + 1] = o.y, v[j + 2] = o.z, v[j + 3] = o.w;
     }
     if (whole) {
 #pragma unroll
