@@ -12,23 +12,30 @@ namespace linear {
 // result here, far below bf16's half step.
 __device__ __forceinline__ float over_one_plus_exp(float z, float v) { return __fdividef(z, 1.f + __expf(-v)); }
 
-// The activation of one output in fp32 (u: the gated activation's second factor).
-__device__ __forceinline__ float activate(int act, float z, float u) {
-    switch (act) {
-        case MXFP4_ACT_RELU: return z < 0.f ? 0.f : z;   // keeps NaN
-        case MXFP4_ACT_SILU: return over_one_plus_exp(z, z);
-        case MXFP4_ACT_GELU: return 0.5f * z * erfcf(-0.70710678118654752f * z);   // 1 + erf without cancellation
-        case MXFP4_ACT_GELU_TANH:   // 0.5 (1 + tanh(v)) = 1 / (1 + e^(-2 v))
-            return over_one_plus_exp(z, 1.5957691216057308f * (z + 0.044715f * z * z * z));
-        case MXFP4_ACT_SWIGLU: return over_one_plus_exp(z, z) * u;
-        default: return z;
-    }
-}
-
-// Four outputs.  One copy of this code per kernel: inlined at every element, the activations fill
-// the instruction cache, and a launch this short meets its code cold.
+// z -> act(z) for four outputs in fp32 (u: the gated activation's second factors).  One copy of
+// this code per kernel and one switch per four outputs: inlined at every element, the
+// activations fill the instruction cache, and a launch this short meets its code cold.
 static __device__ __noinline__ float4 activate4(int act, float4 z, float4 u) {
-    return make_float4(activate(act, z.x, u.x), activate(act, z.y, u.y), activate(act, z.z, u.z), activate(act, z.w, u.w));
+    float v[4] = {z.x, z.y, z.z, z.w};
+    switch (act) {
+        case MXFP4_ACT_RELU:
+#pragma unroll
+            for (float& x : v) x = x < 0.f ? 0.f : x;   // keeps NaN
+            break;
+        case MXFP4_ACT_GELU:   // erfc: 1 + erf without cancellation
+#pragma unroll
+            for (float& x : v) x = 0.5f * x * erfcf(-0.70710678118654752f * x);
+            break;
+        case MXFP4_ACT_GELU_TANH:   // 0.5 (1 + tanh(v)) = 1 / (1 + e^(-2 v))
+#pragma unroll
+            for (float& x : v) x = over_one_plus_exp(x, 1.5957691216057308f * (x + 0.044715f * x * x * x));
+            break;
+        default:   // SILU, and SWIGLU's first factor
+#pragma unroll
+            for (float& x : v) x = over_one_plus_exp(x, x);
+    }
+    if (act == MXFP4_ACT_SWIGLU) v[0] *= u.x, v[1] *= u.y, v[2] *= u.z, v[3] *= u.w;
+    return make_float4(v[0], v[1], v[2], v[3]);
 }
 
 __device__ __forceinline__ float bias_at(const LinearArgs& a, int64_t n) {

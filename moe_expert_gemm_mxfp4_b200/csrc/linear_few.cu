@@ -45,6 +45,7 @@ constexpr int kMaxStages = 4;
 constexpr int kCodeBytes = kBM * 128;   // a code slot: 128 bytes (two stages) of each row
 constexpr int kMaxSlots = 4;
 constexpr int kSmemSm = 228 * 1024;  // per SM, 1 KB of it taken by each resident CTA
+constexpr int kSms = 148;            // what the launch geometry aims at
 constexpr int kMaxCluster = 8;
 constexpr uint32_t kTmemCols = 256, kSfCol = 128;   // D [0, 128), scale sets of 16 columns behind it
 
@@ -86,13 +87,6 @@ __device__ __forceinline__ void fence_async_proxy() { asm volatile("fence.proxy.
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void grid_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
-// r[0..7] <- 8 consecutive 32-bit TMEM columns of this thread's lane.
-__device__ __forceinline__ void tmem_ld_x8(uint32_t taddr, uint32_t* r) {
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-                 : "r"(taddr)
-                 : "memory");
-}
 // D[tmem] (+)= (A . 2^SFA) (B . 2^SFB)^T, one scale per 32 elements of K, K = 32.
 __device__ __forceinline__ void mma_mxf8f6f4(uint32_t d, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                              uint32_t sfa, uint32_t sfb, uint32_t acc) {
@@ -440,7 +434,7 @@ linear_few_kernel(const __grid_constant__ CUtensorMap tmap_codes, const LinearAr
     const int64_t t0 = tt * p.mp;
     const int mt = static_cast<int>(min(static_cast<int64_t>(p.mp), a.M - t0));
     constexpr int kQuads = kFeat / 4, kStep = kThreads / kQuads;
-    constexpr int kBatch = SPLIT >= 4 ? 1 : 4 / SPLIT;   // tokens whose loads are in flight together
+    constexpr int kBatch = SPLIT >= 3 ? 1 : 4 / SPLIT;   // tokens whose loads are in flight together
     const int c0 = rank * mt / SPLIT, c1 = (rank + 1) * mt / SPLIT;
     const int qd = tid % kQuads;
     const int64_t n0 = f * kFeat + 4 * qd;
@@ -486,13 +480,15 @@ linear_few_kernel(const __grid_constant__ CUtensorMap tmap_codes, const LinearAr
         const int q = warp & 3;
         const uint32_t base = tmem + (static_cast<uint32_t>(q * 32) << 16);
         float* to_row = part + 32 * q + lane;
-        for (int c = 8 * (warp >> 2); c < mt; c += 16) {
-            uint32_t v[8], w[8];
-            tmem_ld_x8(base + c, v);
-            if (p.stacked) tmem_ld_x8(base + p.mp + c, w);
+        // 16 columns at a time; the columns behind the tile's tokens (mp = 8, or an odd half) hold
+        // other rows' sums or nothing, and land behind the rows that are read
+        for (int c = 16 * (warp >> 2); c < mt; c += 32) {
+            uint32_t v[16], w[16];
+            tmem_ld_x16(base + c, v);
+            if (p.stacked) tmem_ld_x16(base + p.mp + c, w);
             tmem_wait_ld();
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
+            for (int j = 0; j < 16; ++j) {
                 float z = __uint_as_float(v[j]);
                 if (p.stacked) z += __uint_as_float(w[j]);
                 to_row[(c + j) * kBM] = z;
@@ -580,14 +576,17 @@ linear_few_kernel(const __grid_constant__ CUtensorMap tmap_codes, const LinearAr
 // The launch geometry.  Independent of the device, so that the workspace query and the call agree.
 Plan make_plan(int64_t M, int64_t K, int64_t n_out, bool gated) {
     Plan p{};
-    p.t_tiles = static_cast<int>((M + kMaxMp - 1) / kMaxMp);
-    const int per = static_cast<int>((M + p.t_tiles - 1) / p.t_tiles);
-    p.mp = per <= 8 ? 8 : (per + 15) / 16 * 16;
-    p.t_tiles = static_cast<int>((M + p.mp - 1) / p.mp);
-    p.stacked = 2 * p.mp <= 128;
     const int f = gated ? 64 : kBM;
     p.w_tiles = static_cast<int>((n_out + f - 1) / f);
     p.nk = static_cast<int>((K + kBK - 1) / kBK);
+    // As few token tiles as hold M (every one streams the weights), or, when those do not fill
+    // the SMs and K could not be split over what is left, as many as do.
+    int64_t tt = (M + kMaxMp - 1) / kMaxMp;
+    if (tt > 1 && tt * p.w_tiles <= kSms && 2 * tt * p.w_tiles > kSms) tt = kSms / p.w_tiles;
+    const int per = static_cast<int>((M + tt - 1) / tt);
+    p.mp = per <= 8 ? 8 : (per + 15) / 16 * 16;
+    p.t_tiles = static_cast<int>((M + p.mp - 1) / p.mp);
+    p.stacked = 2 * p.mp <= 128;
     p.b_bytes = 2 * p.mp * kBK + (p.stacked ? 1 : 2) * kAtom;
     p.stage_bytes = (kABytes + p.b_bytes + kAtom + 1023) / 1024 * 1024;
     return p;
@@ -606,7 +605,7 @@ template <bool kGated, int SPLIT>
 cudaError_t launch_product(const CUtensorMap& tmap_codes, const LinearArgs& a, const Plan& p, const uint8_t* ws_b,
                            const uint8_t* ws_sfa, cudaStream_t stream) {
     auto kern = linear_few_kernel<kGated, SPLIT>;
-    const int part = p.mp * kBM * 4, ring = p.stages * p.stage_bytes + p.slots * kCodeBytes;
+    const int part = (p.mp + 15) / 16 * 16 * kBM * 4, ring = p.stages * p.stage_bytes + p.slots * kCodeBytes;
     const int smem = (ring > part ? ring : part) + 1024;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
@@ -630,25 +629,28 @@ cudaError_t launch_product(const CUtensorMap& tmap_codes, const LinearArgs& a, c
 template <bool kGated>
 cudaError_t launch_few(const LinearArgs& a, const CUtensorMap& tmap_codes, Plan p, void* ws, int sm_count,
                        cudaStream_t stream) {
-    // Rings: three stages, then code slots (what is in flight from memory), then a fourth stage;
-    // two resident CTAs per SM where each then has three stages and two slots.
+    // Rings: `least` stages, then code slots (what is in flight from memory), then more stages.  Two
+    // resident CTAs per SM where each then has two stages and two slots: they hide each
+    // other's start and finish.
     const int fixed = 1024 + 1024 + 512;   // alignment slack, the system's share, static shared memory
-    auto fit = [&](int room) {
-        p.stages = 3;
+    auto fit = [&](int room, int least) {
+        p.stages = least;
         p.slots = (room - p.stages * p.stage_bytes) / kCodeBytes;
         if (p.slots > kMaxSlots) p.slots = kMaxSlots;
-        if (p.slots >= 2 && room - p.slots * kCodeBytes >= kMaxStages * p.stage_bytes) p.stages = kMaxStages;
-        return p.slots >= 2;
+        if (p.slots < 2) return false;
+        while (p.stages < kMaxStages && room - p.slots * kCodeBytes >= (p.stages + 1) * p.stage_bytes) ++p.stages;
+        return true;
     };
     int occ = 2;
-    if (!fit(kSmemSm / 2 - fixed)) {
+    if (!fit(kSmemSm / 2 - fixed, 3) && !fit(kSmemSm / 2 - fixed, 2)) {
         occ = 1;
-        if (!fit(kSmemSm - fixed)) return cudaErrorInvalidConfiguration;
+        if (!fit(kSmemSm - fixed, 3)) return cudaErrorInvalidConfiguration;
     }
-    // K split over a cluster while the CTAs fit the SMs at once
+    // K split over a cluster while the CTAs fit the SMs at once (a cluster of 3 would need SMs
+    // in threes: 135 CTAs of one per SM then take two rounds, 21 us against 15 at 64 tokens)
     p.split = 1;
     while (p.split < kMaxCluster && 2 * p.split <= p.nk &&
-           2LL * p.split * p.w_tiles * p.t_tiles <= static_cast<int64_t>(occ) * sm_count)
+           2LL * p.split * p.w_tiles * p.t_tiles <= static_cast<int64_t>(occ) * kSms)
         p.split *= 2;
     uint8_t* ws_b = static_cast<uint8_t*>(ws);
     uint8_t* ws_sfa = ws_b + static_cast<size_t>(p.t_tiles) * p.nk * p.b_bytes;

@@ -120,10 +120,10 @@ __device__ __forceinline__ void finish32(const LinearArgs& a, int64_t m, int64_t
                                __uint_as_float(z[j + 2]) + b.z, __uint_as_float(z[j + 3]) + b.w);
         if (kGated) {
             const float4 c = *reinterpret_cast<const float4*>(bu + j);
-            o.x = activate(MXFP4_ACT_SWIGLU, o.x, __uint_as_float(u[j]) + c.x);
-            o.y = activate(MXFP4_ACT_SWIGLU, o.y, __uint_as_float(u[j + 1]) + c.y);
-            o.z = activate(MXFP4_ACT_SWIGLU, o.z, __uint_as_float(u[j + 2]) + c.z);
-            o.w = activate(MXFP4_ACT_SWIGLU, o.w, __uint_as_float(u[j + 3]) + c.w);
+            o.x = over_one_plus_exp(o.x, o.x) * (__uint_as_float(u[j]) + c.x);
+            o.y = over_one_plus_exp(o.y, o.y) * (__uint_as_float(u[j + 1]) + c.y);
+            o.z = over_one_plus_exp(o.z, o.z) * (__uint_as_float(u[j + 2]) + c.z);
+            o.w = over_one_plus_exp(o.w, o.w) * (__uint_as_float(u[j + 3]) + c.w);
         } else if (a.act != MXFP4_ACT_NONE) {
             o = activate4(a.act, o, o);
         }
