@@ -15,6 +15,7 @@ scales uint8 [rows, cols/32].
 from __future__ import annotations
 
 import ctypes
+from functools import lru_cache
 
 import torch
 
@@ -47,8 +48,9 @@ def _p(t):
 
 
 def _stream(stream=None):
-    s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+    if stream is None:   # the current stream's handle, without building a Stream object (3 us)
+        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
+    return ctypes.c_void_p(stream.cuda_stream)
 
 
 def _need(t, name, dtype=None, shape=None):
@@ -174,20 +176,17 @@ def _used_on(stream, *tensors):
                 t.record_stream(stream)
 
 
+@lru_cache(maxsize=1024)
 def mxfp4_linear_workspace_size(M, K, N, act=ACT_NONE) -> int:
     return int(_lib.load().mxfp4_linear_workspace_size(M, K, N, int(act)))
 
 
-def mxfp4_linear(x: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Tensor, bias=None, act: int = ACT_NONE,
-                 residual=None, out=None, ws=None, stream=None):
-    """y bf16 [M, n_out] = act(x bf16 [M, K] . dequant(W)^T + bias) + residual (W4A16), W codes
-    [N, K/2] + scales [N, K/32]; bias bf16 or fp32 [N]; n_out = N, or N / 2 with ACT_SWIGLU
-    (W rows [0, N/2) gate, [N/2, N) up); residual bf16 [M, n_out], which may be `out`."""
+def _check_linear_operands(x, w_codes, w_scales, bias, act, residual, out, ws):
+    """Raise unless the linear layer's operands fit together; returns (M, K, N, n_out)."""
     _need_dims(x, "x", 2)
     _need_dims(w_codes, "w_codes", 2)
     M, K = x.shape
     N = w_codes.shape[0]
-    act = int(act)
     if act == ACT_SWIGLU and N % 2:
         raise ValueError(f"w_codes: the gated activation needs an even number of rows, got {N}")
     n_out = N // 2 if act == ACT_SWIGLU else N
@@ -205,19 +204,32 @@ def mxfp4_linear(x: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Tensor,
     if ws is not None:
         _need(ws, "ws")
     _on_current_device(x=x, w_codes=w_codes, w_scales=w_scales, bias=bias, residual=residual, out=out, ws=ws)
+    return M, K, N, n_out
+
+
+def mxfp4_linear(x: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Tensor, bias=None, act: int = ACT_NONE,
+                 residual=None, out=None, ws=None, stream=None):
+    """y bf16 [M, n_out] = act(x bf16 [M, K] . dequant(W)^T + bias) + residual (W4A16), W codes
+    [N, K/2] + scales [N, K/32]; bias bf16 or fp32 [N]; n_out = N, or N / 2 with ACT_SWIGLU
+    (W rows [0, N/2) gate, [N/2, N) up); residual bf16 [M, n_out], which may be `out`."""
+    act = int(act)
+    M, K, N, n_out = _check_linear_operands(x, w_codes, w_scales, bias, act, residual, out, ws)
     lib = _lib.load()
     new_out = new_ws = None
     if out is None:
-        out = new_out = _empty((M, n_out), torch.bfloat16, x)
+        out = new_out = x.new_empty((M, n_out))
     if ws is None:
-        need = int(lib.mxfp4_linear_workspace_size(M, K, N, act))
+        need = mxfp4_linear_workspace_size(M, K, N, act)
         if need:
-            ws = new_ws = _empty((need,), torch.uint8, x)
+            ws = new_ws = w_codes.new_empty((need,))
     nbytes = 0 if ws is None else ws.numel() * ws.element_size()
-    bias_dt = _lib.IN_F32 if bias is not None and bias.dtype == torch.float32 else _lib.IN_BF16
-    _lib.check("mxfp4_linear", lib.mxfp4_linear(_p(x), M, K, _p(w_codes), _p(w_scales), N, _p(bias), bias_dt, act,
-                                                _p(residual), _p(out), _p(ws), nbytes, _stream(stream)))
-    _used_on(stream, new_out, new_ws)
+    bias_dt = _lib.IN_F32 if bias is not None and bias.dtype is torch.float32 else _lib.IN_BF16
+    _lib.check("mxfp4_linear", lib.mxfp4_linear(
+        x.data_ptr(), M, K, w_codes.data_ptr(), w_scales.data_ptr(), N, None if bias is None else bias.data_ptr(),
+        bias_dt, act, None if residual is None else residual.data_ptr(), out.data_ptr(),
+        None if ws is None else ws.data_ptr(), nbytes, _stream(stream)))
+    if stream is not None:
+        _used_on(stream, new_out, new_ws)
     return out
 
 
@@ -286,6 +298,7 @@ def moe_mxfp4_route_project(x: torch.Tensor, w_router: torch.Tensor, top_k: int,
     return out
 
 
+@lru_cache(maxsize=1024)
 def moe_mxfp4_route_scored_workspace_size(T, E, top_k) -> int:
     return int(_lib.load().moe_mxfp4_route_scored_workspace_size(T, E, top_k))
 
@@ -313,24 +326,23 @@ def moe_mxfp4_route_scored(logits: torch.Tensor, top_k: int, score: int = SCORE_
     top_k = int(top_k)
     if top_k < 1:
         raise ValueError(f"top_k: expected at least 1, got {top_k}")
-    P = T * top_k
-    out = dict(ids=_empty((T, top_k), torch.int32, logits),
-               weights=_empty((T, top_k), torch.float32, logits),
-               counts=_empty((E,), torch.int32, logits),
-               offsets=_empty((E + 1,), torch.int32, logits),
-               perm=_empty((P,), torch.int32, logits),
-               inv=_empty((P,), torch.int32, logits))
+    ids = logits.new_empty((T, top_k), dtype=torch.int32)
+    perm = ids.new_empty((T * top_k,))
+    counts = ids.new_empty((E,))
+    out = dict(ids=ids, weights=torch.empty_like(ids, dtype=torch.float32), counts=counts,
+               offsets=ids.new_empty((E + 1,)), perm=perm, inv=torch.empty_like(perm))
     new_ws = None
     if ws is None:
-        need = int(lib.moe_mxfp4_route_scored_workspace_size(T, E, top_k))
+        need = moe_mxfp4_route_scored_workspace_size(T, E, top_k)
         if need:
-            ws = new_ws = _empty((need,), torch.uint8, logits)
+            ws = new_ws = ids.new_empty((need // 4,))
     nbytes = 0 if ws is None else ws.numel() * ws.element_size()
     _lib.check("moe_mxfp4_route_scored", lib.moe_mxfp4_route_scored(
-        _p(logits), dt, T, E, top_k, int(score), _p(bias), int(n_groups), int(top_groups), int(group_top),
-        int(bool(renorm)), float(scale), _p(out["ids"]), _p(out["weights"]), _p(out["counts"]), _p(out["offsets"]),
-        _p(out["perm"]), _p(out["inv"]), _p(ws), nbytes, _stream(stream)))
-    _used_on(stream, new_ws, *out.values())
+        logits.data_ptr(), dt, T, E, top_k, int(score), None if bias is None else bias.data_ptr(), int(n_groups),
+        int(top_groups), int(group_top), int(bool(renorm)), float(scale), *[t.data_ptr() for t in out.values()],
+        None if ws is None else ws.data_ptr(), nbytes, _stream(stream)))
+    if stream is not None:
+        _used_on(stream, new_ws, *out.values())
     return out
 
 
