@@ -251,7 +251,7 @@ __device__ __noinline__ float dot_direct(const LinearArgs& a, int64_t m, int64_t
 // SPLIT: CTAs of a cluster along K.
 template <bool kGated, int SPLIT>
 __global__ void __launch_bounds__(kThreads)
-linear_few_kernel(const __grid_constant__ CUtensorMap tmap_codes, const LinearArgs a, const Plan p,
+linear_few_kernel(const __grid_constant__ CUtensorMap tmap_codes, const __grid_constant__ LinearArgs a, const Plan p,
                   const uint8_t* __restrict__ ws_b, const uint8_t* __restrict__ ws_sfa) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &

@@ -8,15 +8,20 @@
 //   a group's value is the sum of its one or two largest c; the top_groups groups by
 //   (value desc, index asc) are kept; the top_k experts of those by (c desc, id asc);
 //   w_j = s_{id_j}, over their sum if renormalised, times scale.
-// The choice is made on c in 64-bit arithmetic, so that two experts whose scores lie a
-// rounding of fp32 apart are not swapped.
+// The choice is the one that 64-bit arithmetic makes, so that two experts whose scores lie a
+// rounding of fp32 apart are not swapped.  It is made in fp32 with a bound on the error of c;
+// where two neighbours of the chosen order (the first one left out among them) or the
+// groups on both sides of the cut lie closer than that, the token is chosen again in 64 bits
+// (a few tokens in a thousand; all of them in 64 bits took 2.8 times as long).
 //
-// Two kernels over at most kMaxChunks contiguous chunks of tokens (one CTA each):
+// Up to 256 tokens: one launch, a cluster of up to 8 CTAs with a warp per token; the CTAs exchange
+// their per-expert pair counts through distributed shared memory.  More tokens: two kernels over
+// at most kMaxChunks contiguous chunks of tokens (one CTA each), the second launched while
+// the first runs (programmatic dependent launch):
 //   route_scored_topk   one warp per token; the chunk's per-expert pair counts;
 //   route_scored_place  every CTA sums the chunk counts before its own and over all
-//                       (coalesced rows, from L2), scans the experts, and ranks its
+//                       (16-byte loads from L2), scans the experts, and ranks its
 //                       chunk's pairs in ascending order by warp match masks.
-// A batch of one chunk does both in one launch.
 #include "common.cuh"
 #include "internal.h"
 
@@ -24,10 +29,12 @@ namespace mx {
 
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
+constexpr int kFewWarps = 8;       // of a CTA at least, while the batch has fewer than 8 tokens per SM
+constexpr int kMaxCluster = 8;
+constexpr int kClusterTokens = kMaxCluster * kWarps;   // one warp per token, one launch
 constexpr int kMaxE = 256;
-constexpr int kMaxK = 8;
 constexpr int kMaxChunks = 148;    // one CTA per SM
 constexpr uint32_t kFull = 0xFFFFFFFFu;
 
@@ -47,25 +54,25 @@ __device__ __forceinline__ float load_logit(const void* p, int64_t i) {
 // Where expert items live in a warp: lanes in segments of `seg` (a power of two) per
 // group; item i of lane r of the segment is expert r + seg * i of the group.
 struct Lanes {
-    int g, r, seg, gs;
+    int g, r, seg, base, size;   // base: the lane's first expert; size: a group's experts
     bool on;
-    __device__ __forceinline__ Lanes(int lane, int n_groups, int E) {
-        seg = 32;
-        while (32 / seg < n_groups) seg >>= 1;
-        g = lane / seg;
-        r = lane % seg;
-        gs = E / n_groups;
-        on = g < n_groups;
+    __device__ __forceinline__ Lanes(const RouteScoredArgs& a, int lane) {
+        seg = 1 << a.seg_log2;
+        size = a.group_size;
+        g = lane >> a.seg_log2;
+        r = lane & (seg - 1);
+        base = g * size + r;
+        on = g < a.n_groups;
     }
-    __device__ __forceinline__ bool has(int i) const { return on && r + seg * i < gs; }
-    __device__ __forceinline__ int expert(int i) const { return g * gs + r + seg * i; }
+    __device__ __forceinline__ bool has(int i) const { return on && r + seg * i < size; }
+    __device__ __forceinline__ int expert(int i) const { return base + seg * i; }
 };
 
-// The chosen experts of one token: lane j < top_k returns the id of slot j.  NI items
-// per lane hold a whole row (E <= 256 over the lanes of n_groups segments).
+// The chosen experts of one token in 64 bits: lane j < top_k returns the id of slot j.  NI
+// items per lane hold a whole row (E <= 256 over the lanes of n_groups segments).
 template <bool kBf16, int NI>
-__device__ int choose64(const RouteScoredArgs& a, int64_t t, int lane) {
-    const Lanes L(lane, a.n_groups, a.E);
+__device__ __noinline__ int choose64(const RouteScoredArgs& a, int64_t t, int lane) {
+    const Lanes L(a, lane);
     double c[NI];
     uint32_t live = 0;   // items that may still be chosen
     const int64_t row = t * a.E;
@@ -168,30 +175,201 @@ __device__ int choose64(const RouteScoredArgs& a, int64_t t, int lane) {
     return mine;
 }
 
-// max and sum of exp(l - max) over the row's numbers (NaN left out, an infinite
-// maximum counts 1 for each of its experts)
+// The same order on 32 bits; 0 is left for items that are not in the running.
+__device__ __forceinline__ uint32_t order_key32(float v) {
+    const uint32_t u = __float_as_uint(v + 0.f);   // -0 + 0 = +0
+    return v != v ? 1u : (u >> 31) ? ~u : (u | 0x80000000u);
+}
+__device__ __forceinline__ float order_value32(uint32_t key) {
+    return __uint_as_float(key == 1u ? 0x7FC00000u : (key >> 31) ? (key & 0x7FFFFFFFu) : ~key);
+}
+
+// 2^x and 1 / x in hardware: off by at most 2^-22 and 2^-23 of the result (subnormals become 0).
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+constexpr float kLog2e = 1.4426950408889634f;
+
+// Descending, by a merge sort whose comparisons are fixed at compile time.
+template <int N>
+__device__ __forceinline__ void sort_descending(uint32_t* k) {
+#pragma unroll
+    for (int p = 1; p < N; p <<= 1) {
+#pragma unroll
+        for (int q = p; q >= 1; q >>= 1) {
+#pragma unroll
+            for (int x = 0; x < N; ++x) {
+                // Batcher's network: x and x + q meet where x lies in the first half of a block of 2 q
+                // (counted from q % p) and both are in the same block of 2 p
+                const int y = x + q;
+                if (y < N && x >= q % p && (x - q % p) % (2 * q) < q && x / (2 * p) == y / (2 * p)) {
+                    const uint32_t hi = max(k[x], k[y]), lo = min(k[x], k[y]);
+                    k[x] = hi;
+                    k[y] = lo;
+                }
+            }
+        }
+    }
+}
+
+// Steps of 2^-24 of the range that s + bias can have in this call; near: what rounding adds.
+struct Steps {
+    float lo, scale, near;
+    __device__ __forceinline__ Steps(const RouteScoredArgs& a, int lane) {
+        float b0 = a.bias ? INFINITY : 0.f, b1 = a.bias ? -INFINITY : 0.f;
+        if (a.bias) {
+            for (int e = lane; e < a.E; e += 32) {
+                const float b = __ldg(a.bias + e);
+                if (fabsf(b) < INFINITY) b0 = fminf(b0, b), b1 = fmaxf(b1, b);
+            }
+        }
+        b0 = -order_value32(__reduce_max_sync(kFull, order_key32(-b0)));
+        b1 = order_value32(__reduce_max_sync(kFull, order_key32(b1)));
+        if (!(b0 <= b1)) b0 = b1 = 0.f;   // no finite bias
+        lo = b0;
+        scale = (0x1p24f - 16.f) / (1.f + (b1 - b0));
+        near = fminf(0x1p-22f * (1.f + fmaxf(fabsf(b0), fabsf(b1))) * scale, 0x1p24f) + 3.f;
+    }
+};
+
+// The chosen experts of one token (lane j < top_k returns the id of slot j), and for
+// softmax scores that need them the row's maximum and sum of exp(l - m) (NaN left out, an
+// infinite maximum counts 1 for each of its experts).
+//
+// One key per item: 24 bits that order c, then the complement of the expert's id.  Every lane sorts
+// its items' keys; each round takes the largest head of the lanes' lists with one warp
+// reduction.  bf16 logits that order the choice themselves are exact in 16 of the 24 bits;
+// fp32 ones are taken in steps of 2^-24 of the row's range, scores in the call's Steps.
 template <bool kBf16, int NI>
-__device__ __forceinline__ void row_softmax(const RouteScoredArgs& a, int64_t t, int lane, float* m_out, float* sum_out) {
-    float l[NI];
-    float m = -INFINITY;
+__device__ __forceinline__ int choose(const RouteScoredArgs& a, const Steps& st, int64_t t, int lane, float* m_out,
+                                      float* sum_out) {
+    const Lanes L(a, lane);
+    const int64_t row = t * a.E + L.base;
+    float c[NI];
 #pragma unroll
-    for (int i = 0; i < NI; ++i) {
-        const int e = lane + 32 * i;
-        l[i] = e < a.E ? load_logit<kBf16>(a.logits, t * a.E + e) : -INFINITY;
-        m = fmaxf(m, l[i]);
+    for (int i = 0; i < NI; ++i) c[i] = L.has(i) ? load_logit<kBf16>(a.logits, row + L.seg * i) : -INFINITY;
+    float b[NI];
+#pragma unroll
+    for (int i = 0; i < NI; ++i) b[i] = a.bias && L.has(i) ? __ldg(a.bias + L.base + L.seg * i) : 0.f;
+    // Two exact c further apart than err keep their order in fp32.  With d = l - m: exp's argument
+    // is rounded (|d| 2^-23.4 of the result) and ex2 is off by 2^-22, so e^d by at most 2^-21.5
+    // absolutely; the sum of at most 21 rounded additions and the quotient keep s within 2^-18 of
+    // the largest score.  A sigmoid is within s (1 - s) |l| 2^-23.4 + 2^-21 < 2^-20.
+    float err = 0.f;
+    if (a.score == MXFP4_SCORE_SOFTMAX) {
+        if (!a.by_logit || !a.renorm) {
+            float m = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < NI; ++i) m = fmaxf(m, c[i]);
+            m = order_value32(__reduce_max_sync(kFull, order_key32(m)));
+            float sum = 0.f, e[NI];
+#pragma unroll
+            for (int i = 0; i < NI; ++i) {
+                e[i] = c[i] == -INFINITY ? 0.f : c[i] == m ? 1.f : ex2((c[i] - m) * kLog2e);
+                sum += e[i] == e[i] ? e[i] : 0.f;
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
+            *m_out = m;
+            *sum_out = sum;
+            if (!a.by_logit) {
+                const float inv = rcp(sum);
+                err = 0x1p-17f * inv;
+#pragma unroll
+                for (int i = 0; i < NI; ++i) c[i] = c[i] == -INFINITY ? -INFINITY : e[i] * inv + b[i];
+            }
+        }
+    } else if (!a.by_logit) {
+        err = 0x1p-19f;
+#pragma unroll
+        for (int i = 0; i < NI; ++i)
+            c[i] = c[i] == -INFINITY ? -INFINITY : rcp(1.f + ex2(-kLog2e * c[i])) + b[i];
     }
+    const bool exact = kBf16 && a.by_logit;
+    bool close = false;   // fp32 does not tell
+    bool on = L.on;
+    if (a.top_groups < a.n_groups) {
+        float t1 = -INFINITY, t2 = -INFINITY;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
-    float sum = 0.f;
-#pragma unroll
-    for (int i = 0; i < NI; ++i) {
-        const float z = l[i] == -INFINITY ? 0.f : l[i] == m ? 1.f : expf(l[i] - m);
-        if (z == z) sum += z;
+        for (int i = 0; i < NI; ++i) {   // NaN takes no part
+            t2 = fmaxf(t2, fminf(t1, c[i]));
+            t1 = fmaxf(t1, c[i]);
+        }
+        for (int o = L.seg >> 1; o > 0; o >>= 1) {
+            const float u1 = __shfl_xor_sync(kFull, t1, o), u2 = __shfl_xor_sync(kFull, t2, o);
+            t2 = fmaxf(fminf(t1, u1), fmaxf(t2, u2));
+            t1 = fmaxf(t1, u1);
+        }
+        const float second = a.group_top == 2 && t2 != -INFINITY ? t2 : 0.f;
+        // the group's place: its value in 27 bits, then the complement of its index
+        const uint32_t key = on ? (order_key32(t1 + second) & ~31u) | static_cast<uint32_t>(31 - L.g) : 0u;
+        int rank = 0;
+#pragma unroll 4
+        for (int g = 0; g < a.n_groups; ++g) rank += __shfl_sync(kFull, key, g << a.seg_log2) > key;
+        if (!exact) {   // the last group kept and the first left out
+            const uint32_t last = __reduce_max_sync(kFull, on && rank == a.top_groups - 1 ? key : 0u);
+            const uint32_t first = __reduce_max_sync(kFull, on && rank == a.top_groups ? key : 0u);
+            const bool edge = on && (rank == a.top_groups - 1 || rank == a.top_groups);
+            const float x = order_value32(last | 31u), y = order_value32(first & ~31u);
+            const float big = edge ? fmaxf(fabsf(t1), fabsf(second)) : 0.f;
+            close = edge && y > -INFINITY && !(x - y > 2.f * err + 0x1p-16f * fmaxf(fabsf(x), fabsf(y)) + 0x1p-21f * big);
+        }
+        on = on && rank < a.top_groups;
     }
+    uint32_t key[NI], near = 0;   // near: keys of neighbours no further apart are close
+    if (exact) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
-    *m_out = m;
-    *sum_out = sum;
+        for (int i = 0; i < NI; ++i)
+            key[i] = on && L.has(i) ? max(order_key32(c[i]) >> 16, 1u) << 8 | static_cast<uint32_t>(255 - L.expert(i)) : 0u;
+    } else {
+        float lo = st.lo, scale = st.scale;
+        if (a.by_logit) {
+            float x = INFINITY, y = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < NI; ++i) {
+                y = fmaxf(y, c[i]);
+                x = c[i] == -INFINITY ? x : fminf(x, c[i]);
+            }
+            y = order_value32(__reduce_max_sync(kFull, order_key32(y)));
+            lo = -order_value32(__reduce_max_sync(kFull, order_key32(-x)));
+            scale = y > lo ? fminf((0x1p24f - 16.f) / (y - lo), 0x1p100f) : 0.f;
+            near = 3u;    // the roundings of the difference and of the product
+        } else {
+            near = static_cast<uint32_t>(fminf(err * scale, 0x1p24f) + st.near);
+        }
+        float all = 0.f;
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+            // masked experts below all others, among themselves by id
+            const uint32_t q = c[i] == -INFINITY ? 1u : 4u + static_cast<uint32_t>((c[i] - lo) * scale);
+            key[i] = on && L.has(i) ? q << 8 | static_cast<uint32_t>(255 - L.expert(i)) : 0u;
+            all += c[i] == -INFINITY ? 0.f : c[i];
+        }
+        close |= !(fabsf(all) < INFINITY);   // NaN or an infinity, or sums past fp32's range
+    }
+    sort_descending<NI>(key);
+    int mine = 0;
+    uint32_t prev = 0xFFFFFFFFu;
+    const int rounds = exact ? a.top_k : a.top_k + 1;   // one more: the first left out
+#pragma unroll 1
+    for (int j = 0; j < rounds; ++j) {
+        const uint32_t top = __reduce_max_sync(kFull, key[0]);
+        if (!exact) close |= j > 0 && top >= 4u << 8 && (prev >> 8) - (top >> 8) <= near;
+        prev = top;
+        if (lane == j) mine = 255 - static_cast<int>(top & 255u);
+        const bool pop = key[0] == top;   // keys are distinct, but for the 0 of empty lists
+#pragma unroll
+        for (int i = 0; i < NI; ++i) key[i] = pop ? (i + 1 < NI ? key[i + 1] : 0u) : key[i];
+    }
+    if (__any_sync(kFull, close)) return choose64<kBf16, NI>(a, t, lane);
+    return mine;
 }
 
 // log of the smallest 64-bit number, 2^-1074, less half a step: scores below it are 0
@@ -201,39 +379,39 @@ constexpr float kLogTiny = -745.13f;
 // relative to the largest chosen logit, so that rows of very small scores keep their
 // precision.  A score that is 0 in 64 bits weighs 0 (l = -inf, or a mask of the type's
 // lowest value), and so does every slot of a token whose chosen scores are all 0.
-__device__ __forceinline__ float slot_weight(const RouteScoredArgs& a, float l, bool on, float m, float sum, int lane) {
-    float w = 0.f;
-    if (a.renorm) {
-        float top = on && l == l ? l : -INFINITY;
-#pragma unroll
-        for (int o = 4; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
-        const float ref = a.score == MXFP4_SCORE_SOFTMAX ? m : 0.f;
-        if (on && l != -INFINITY && !(l - ref < kLogTiny)) {
-            if (a.score == MXFP4_SCORE_SOFTMAX) w = l == top ? 1.f : expf(l - top);
-            else if (top < 0.f) w = (l == top ? 1.f : expf(l - top)) / (1.f + expf(l));
-            else w = 1.f / (1.f + expf(-l));
-        }
-        float s = w;
-#pragma unroll
-        for (int o = 4; o > 0; o >>= 1) s += __shfl_xor_sync(kFull, s, o);
-        w = s == 0.f ? 0.f : w / s;
-    } else if (on && l != -INFINITY) {
-        w = a.score == MXFP4_SCORE_SOFTMAX ? (l == m ? 1.f : expf(l - m)) / sum : 1.f / (1.f + expf(-l));
+__device__ __forceinline__ float slot_weight(const RouteScoredArgs& a, float l, bool on, float m, float sum) {
+    const bool soft = a.score == MXFP4_SCORE_SOFTMAX;
+    if (!a.renorm) {
+        const float w = soft ? (l == m ? 1.f : expf(l - m)) / sum : 1.f / (1.f + expf(-l));
+        return on && l != -INFINITY ? w * a.scale : 0.f;
     }
-    return w * a.scale;
+    float top = on && l == l ? l : -INFINITY;
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
+    // e^(l - top), of which a sigmoid is e^top / (1 + e^l) times; above 0 the sigmoid itself
+    const float d = !soft && top >= 0.f ? -l : l == top ? 0.f : l - top;
+    float w = expf(d);
+    if (!soft) w = top >= 0.f ? __fdividef(1.f, 1.f + w) : __fdividef(w, 1.f + expf(l));
+    // (where the logits order the choice, the row's largest is among the chosen)
+    const float ref = !soft ? 0.f : a.by_logit ? top : m;
+    if (!on || l == -INFINITY || l - ref < kLogTiny) w = 0.f;
+    float s = w;
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) s += __shfl_xor_sync(kFull, s, o);
+    return s == 0.f ? 0.f : w / s * a.scale;
 }
 
 // Top-k, weights and the pair counts of tokens [t0, t1); s_hist [E] zeroed before.
 template <bool kBf16, int NI>
 __device__ void topk_chunk(const RouteScoredArgs& a, int64_t t0, int64_t t1, int32_t* s_hist) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    for (int64_t t = t0 + warp; t < t1; t += kWarps) {
-        const int id = choose64<kBf16, NI>(a, t, lane);
-        float m = 0.f, sum = 1.f;
-        if (a.score == MXFP4_SCORE_SOFTMAX) row_softmax<kBf16, 8>(a, t, lane, &m, &sum);
+    const Steps st(a, lane);
+    for (int64_t t = t0 + warp; t < t1; t += blockDim.x / 32) {
+        float m = -INFINITY, sum = 1.f;
+        const int id = choose<kBf16, NI>(a, st, t, lane, &m, &sum);
         const bool on = lane < a.top_k;
         const float l = on ? load_logit<kBf16>(a.logits, t * a.E + id) : -INFINITY;
-        const float w = slot_weight(a, l, on, m, sum, lane);
+        const float w = slot_weight(a, l, on, m, sum);
         if (on) {
             a.ids[t * a.top_k + lane] = id;
             a.weights[t * a.top_k + lane] = w;
@@ -271,37 +449,47 @@ __device__ void scan_experts(const int32_t* s_tot, int32_t* s_off, int E) {
 
 // perm and inv of pairs [p0, p1): s_base[e] is the sorted position of the range's
 // first pair of expert e.  Each warp takes a contiguous run of 32-pair strips; the
-// lanes of a strip that hold the same expert are one match mask.  s_cnt: [kWarps][kMaxE].
-__device__ void place_chunk(const RouteScoredArgs& a, int64_t p0, int64_t p1, const int32_t* s_base, int32_t* s_cnt) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    for (int i = threadIdx.x; i < kWarps * kMaxE; i += kThreads) s_cnt[i] = 0;
+// lanes of a strip that hold the same expert are one match mask.  s_cnt: [warps][kMaxE].
+__device__ __forceinline__ void place_chunk(const RouteScoredArgs& a, int64_t p0, int64_t p1, const int32_t* s_base,
+                                            int32_t* s_cnt) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x / 32;
+    const int64_t strips = (p1 - p0 + 31) / 32, per = (strips + warps - 1) / warps;
+    const int used = static_cast<int>((strips + per - 1) / per);   // warps with strips
+    const int64_t s0 = min(strips, per * warp), s1 = min(strips, s0 + per);
+    for (int i = threadIdx.x; i < used * kMaxE; i += blockDim.x) s_cnt[i] = 0;
     __syncthreads();
-    const int64_t strips = (p1 - p0 + 31) / 32;
-    const int64_t s0 = strips * warp / kWarps, s1 = strips * (warp + 1) / kWarps;
     int32_t* cnt = s_cnt + warp * kMaxE;
     const uint32_t lt = (1u << lane) - 1u;
+    uint32_t mask = 0;
+    int e = 0;
     for (int64_t s = s0; s < s1; ++s) {
         const int64_t p = p0 + 32 * s + lane;
-        const int e = p < p1 ? a.ids[p] : kMaxE + lane;
-        const uint32_t mask = __match_any_sync(kFull, e);
+        e = p < p1 ? a.ids[p] : kMaxE + lane;
+        mask = __match_any_sync(kFull, e);
         if (p < p1 && (mask & lt) == 0) cnt[e] += __popc(mask);
         __syncwarp();
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < a.E; e += kThreads) {
-        int run = s_base[e];
+    for (int x = threadIdx.x; x < a.E; x += blockDim.x) {
+        int run = s_base[x];
+        for (int w = 0; w < used; w += 8) {
+            int v[8];
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            const int v = s_cnt[w * kMaxE + e];
-            s_cnt[w * kMaxE + e] = run;
-            run += v;
+            for (int i = 0; i < 8; ++i) v[i] = w + i < used ? s_cnt[(w + i) * kMaxE + x] : 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                if (w + i < used) s_cnt[(w + i) * kMaxE + x] = run;
+                run += v[i];
+            }
         }
     }
     __syncthreads();
     for (int64_t s = s0; s < s1; ++s) {
         const int64_t p = p0 + 32 * s + lane;
-        const int e = p < p1 ? a.ids[p] : kMaxE + lane;
-        const uint32_t mask = __match_any_sync(kFull, e);
+        if (per > 1) {   // else the first pass's strip is still at hand
+            e = p < p1 ? a.ids[p] : kMaxE + lane;
+            mask = __match_any_sync(kFull, e);
+        }
         const int first = p < p1 ? cnt[e] : 0;
         __syncwarp();
         if (p < p1) {
@@ -314,101 +502,176 @@ __device__ void place_chunk(const RouteScoredArgs& a, int64_t p0, int64_t p1, co
     }
 }
 
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_barrier() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ int32_t ld_rank(const int32_t* p, uint32_t rank) {   // CTA rank's copy of *p
+    uint32_t addr;
+    int32_t v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(smem_u32(p)), "r"(rank));
+    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+// The whole routing of at most kClusterTokens tokens: gridDim.x CTAs, one cluster.
 template <bool kBf16, int NI>
 __global__ void __launch_bounds__(kThreads)
-route_scored_one_kernel(const RouteScoredArgs a) {
-    __shared__ int32_t s_hist[kMaxE], s_off[kMaxE + 1], s_cnt[kWarps * kMaxE];
-    for (int e = threadIdx.x; e < kMaxE; e += kThreads) s_hist[e] = 0;
+route_scored_cluster_kernel(const __grid_constant__ RouteScoredArgs a) {
+    __shared__ int32_t s_hist[kMaxE], s_sum[kMaxE], s_base[kMaxE], s_off[kMaxE + 1], s_cnt[kWarps * kMaxE];
+    for (int e = threadIdx.x; e < kMaxE; e += blockDim.x) s_hist[e] = 0;
     __syncthreads();
-    topk_chunk<kBf16, NI>(a, 0, a.T, s_hist);
-    __syncthreads();   // the ids written above are read back below
-    scan_experts(s_hist, s_off, a.E);
-    __syncthreads();
-    for (int e = threadIdx.x; e <= a.E; e += kThreads) {
-        a.offsets[e] = s_off[e];
-        if (e < a.E) a.counts[e] = s_hist[e];
+    const int nb = gridDim.x, me = static_cast<int>(cluster_rank());
+    const int64_t t0 = a.T * me / nb, t1 = a.T * (me + 1) / nb;
+    topk_chunk<kBf16, NI>(a, t0, t1, s_hist);
+    __syncwarp();
+    cluster_barrier();   // every CTA's counts are there, and this one's ids
+    for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
+        int v[kMaxCluster], tot = 0, before = 0;
+#pragma unroll
+        for (int q = 0; q < kMaxCluster; ++q) v[q] = q < nb ? ld_rank(s_hist + e, q) : 0;
+#pragma unroll
+        for (int q = 0; q < kMaxCluster; ++q) {
+            tot += v[q];
+            before += q < me ? v[q] : 0;
+        }
+        s_sum[e] = tot;
+        s_base[e] = before;
     }
-    place_chunk(a, 0, a.T * a.top_k, s_off, s_cnt);
+    __syncwarp();
+    cluster_barrier();   // no CTA reads another's counts any more (and this one's sums are there)
+    scan_experts(s_sum, s_off, a.E);
+    __syncthreads();
+    for (int e = threadIdx.x; e <= a.E; e += blockDim.x) {
+        if (me == 0) a.offsets[e] = s_off[e];
+        if (e < a.E) {
+            if (me == 0) a.counts[e] = s_sum[e];
+            s_base[e] += s_off[e];
+        }
+    }
+    __syncthreads();
+    place_chunk(a, t0 * a.top_k, t1 * a.top_k, s_base, s_cnt);
 }
 
 template <bool kBf16, int NI>
 __global__ void __launch_bounds__(kThreads)
-route_scored_topk_kernel(const RouteScoredArgs a) {
+route_scored_topk_kernel(const __grid_constant__ RouteScoredArgs a) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     __shared__ int32_t s_hist[kMaxE];
-    for (int e = threadIdx.x; e < kMaxE; e += kThreads) s_hist[e] = 0;
+    for (int e = threadIdx.x; e < kMaxE; e += blockDim.x) s_hist[e] = 0;
     __syncthreads();
     const int64_t t0 = a.T * blockIdx.x / gridDim.x, t1 = a.T * (blockIdx.x + 1) / gridDim.x;
     topk_chunk<kBf16, NI>(a, t0, t1, s_hist);
     __syncthreads();
-    for (int e = threadIdx.x; e < a.E; e += kThreads) a.chunk_counts[blockIdx.x * a.E + e] = s_hist[e];
+    const int row = (a.E + 3) / 4 * 4;   // rows of whole 16-byte vectors
+    for (int e = threadIdx.x; e < row; e += blockDim.x) a.chunk_counts[blockIdx.x * row + e] = s_hist[e];
 }
 
 __global__ void __launch_bounds__(kThreads)
-route_scored_place_kernel(const RouteScoredArgs a) {
-    __shared__ int32_t s_tot[2][kMaxE], s_before[2][kMaxE], s_off[kMaxE + 1], s_cnt[kWarps * kMaxE];
-    static_assert(kThreads == 2 * kMaxE, "two threads per expert");
-    const int e = threadIdx.x & (kMaxE - 1), half = threadIdx.x / kMaxE;
+route_scored_place_kernel(const __grid_constant__ RouteScoredArgs a) {
+    // the threads in parts of kMaxE / 4, four experts per thread: part q sums chunks q, q + parts, ...
+    __shared__ int32_t s_off[kMaxE + 1], s_base[kMaxE], s_sum[kMaxE];
+    __shared__ __align__(16) int32_t s_cnt[kWarps * kMaxE];   // first the parts' sums, then the warps' counts
+    const int parts = blockDim.x / (kMaxE / 4);                // 2 parts * kMaxE <= warps * kMaxE
+    int4(*s_tot)[kMaxE / 4] = reinterpret_cast<int4(*)[kMaxE / 4]>(s_cnt);
+    int4(*s_before)[kMaxE / 4] = s_tot + parts;
     const int nb = gridDim.x, me = blockIdx.x;
-    if (e < a.E) {
+    const int e4 = threadIdx.x % (kMaxE / 4), part = threadIdx.x / (kMaxE / 4), row4 = (a.E + 3) / 4;
+    asm volatile("griddepcontrol.wait;" ::: "memory");   // the chunks' counts and ids are complete
+    if (e4 < row4 && part < parts) {
+        int4 tot = make_int4(0, 0, 0, 0), before = tot;
+        const int4* counts = reinterpret_cast<const int4*>(a.chunk_counts) + e4;
+#pragma unroll 10
+        for (int c = part; c < nb; c += parts) {
+            const int4 v = counts[c * row4];
+            tot.x += v.x, tot.y += v.y, tot.z += v.z, tot.w += v.w;
+            if (c < me) before.x += v.x, before.y += v.y, before.z += v.z, before.w += v.w;
+        }
+        s_tot[part][e4] = tot;
+        s_before[part][e4] = before;
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
         int tot = 0, before = 0;
-#pragma unroll 8
-        for (int c = half; c < nb; c += 2) {
-            const int v = a.chunk_counts[c * a.E + e];
-            tot += v;
-            if (c < me) before += v;
+        for (int q = 0; q < parts; ++q) {
+            tot += reinterpret_cast<const int32_t*>(s_tot[q])[e];
+            before += reinterpret_cast<const int32_t*>(s_before[q])[e];
         }
-        s_tot[half][e] = tot;
-        s_before[half][e] = before;
+        s_sum[e] = tot;
+        s_base[e] = before;
     }
     __syncthreads();
-    if (threadIdx.x < a.E) s_tot[0][e] += s_tot[1][e];
+    scan_experts(s_sum, s_off, a.E);
     __syncthreads();
-    scan_experts(s_tot[0], s_off, a.E);
-    __syncthreads();
-    if (me == 0) {
-        for (int i = threadIdx.x; i <= a.E; i += kThreads) {
-            a.offsets[i] = s_off[i];
-            if (i < a.E) a.counts[i] = s_tot[0][i];
+    for (int e = threadIdx.x; e <= a.E; e += blockDim.x) {
+        if (me == 0) a.offsets[e] = s_off[e];
+        if (e < a.E) {
+            if (me == 0) a.counts[e] = s_sum[e];
+            s_base[e] += s_off[e];
         }
     }
-    if (threadIdx.x < a.E) s_before[0][e] += s_before[1][e] + s_off[e];
     __syncthreads();
     const int64_t t0 = a.T * me / nb, t1 = a.T * (me + 1) / nb;
-    place_chunk(a, t0 * a.top_k, t1 * a.top_k, s_before[0], s_cnt);
+    place_chunk(a, t0 * a.top_k, t1 * a.top_k, s_base, s_cnt);
 }
 
-// Chunks of a batch: a warp per token while the SMs last, then one CTA per SM.
+// Chunks of a batch: 8 tokens each, a warp per token, while the SMs last, then one CTA per SM.
 int64_t chunks_of(int64_t T) {
-    const int64_t n = (T + kWarps - 1) / kWarps;
+    const int64_t n = (T + kFewWarps - 1) / kFewWarps;
     return n < kMaxChunks ? n : kMaxChunks;
 }
 
 template <bool kBf16, int NI>
 cudaError_t launch(const RouteScoredArgs& a, cudaStream_t stream) {
-    const unsigned nb = static_cast<unsigned>(chunks_of(a.T));
-    if (nb == 1) {
-        route_scored_one_kernel<kBf16, NI><<<1, kThreads, 0, stream>>>(a);
-        return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (a.T <= kClusterTokens) {
+        const int64_t n = (a.T + kFewWarps - 1) / kFewWarps;
+        const unsigned nc = static_cast<unsigned>(n < kMaxCluster ? n : kMaxCluster);
+        cfg.gridDim = dim3(nc, 1, 1);
+        cfg.blockDim = dim3(32 * static_cast<unsigned>((a.T + nc - 1) / nc), 1, 1);
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = nc;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        return cudaLaunchKernelEx(&cfg, route_scored_cluster_kernel<kBf16, NI>, a);
     }
-    route_scored_topk_kernel<kBf16, NI><<<nb, kThreads, 0, stream>>>(a);
+    const unsigned nb = static_cast<unsigned>(chunks_of(a.T));
+    const int64_t per = (a.T + nb - 1) / nb;   // tokens of a chunk
+    const int threads = 32 * static_cast<int>(per < kFewWarps ? kFewWarps : per > kWarps ? kWarps : per);
+    route_scored_topk_kernel<kBf16, NI><<<nb, threads, 0, stream>>>(a);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    route_scored_place_kernel<<<nb, kThreads, 0, stream>>>(a);
-    return cudaGetLastError();
+    cfg.gridDim = dim3(nb, 1, 1);
+    cfg.blockDim = dim3(threads, 1, 1);
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    return cudaLaunchKernelEx(&cfg, route_scored_place_kernel, a);
 }
 
 }  // namespace
 
 size_t route_scored_ws_bytes(int64_t T, int64_t E) {
     const int64_t n = chunks_of(T);
-    return n == 1 ? 0 : static_cast<size_t>(n * E) * sizeof(int32_t);
+    return T <= kClusterTokens ? 0 : static_cast<size_t>(n * ((E + 3) / 4 * 4)) * sizeof(int32_t);
 }
 
-cudaError_t launch_route_scored(const RouteScoredArgs& a, bool bf16, cudaStream_t stream) {
-    // items per lane: 8 hold E <= 256 over whole-warp or power-of-two segments, 16 any group count
-    int seg = 32;
-    while (32 / seg < a.n_groups) seg >>= 1;
-    const int items = (a.E / a.n_groups + seg - 1) / seg;
+cudaError_t launch_route_scored(RouteScoredArgs a, bool bf16, cudaStream_t stream) {
+    a.group_size = a.E / a.n_groups;
+    a.seg_log2 = 5;
+    while ((32 >> a.seg_log2) < a.n_groups) --a.seg_log2;
+    // items per lane: at most 8 where n_groups is a power of two, else at most 16
+    const int seg = 1 << a.seg_log2, items = (a.group_size + seg - 1) / seg;
+    if (items <= 1) return bf16 ? launch<true, 1>(a, stream) : launch<false, 1>(a, stream);
+    if (items <= 2) return bf16 ? launch<true, 2>(a, stream) : launch<false, 2>(a, stream);
+    if (items <= 4) return bf16 ? launch<true, 4>(a, stream) : launch<false, 4>(a, stream);
     if (items <= 8) return bf16 ? launch<true, 8>(a, stream) : launch<false, 8>(a, stream);
     return bf16 ? launch<true, 16>(a, stream) : launch<false, 16>(a, stream);
 }
