@@ -45,7 +45,8 @@ struct RouteScoredArgs {
     int E, top_k, score, n_groups, top_groups, group_top, renorm;
     int by_logit;              // the choice goes by the logits (no bias, no sums of scores)
     float scale;
-    int group_size, seg_log2;  // set by the launch: experts per group, lanes per group (2^seg_log2)
+    int group_size, seg_log2;  // set by the launch: experts per group, lanes per group (2^seg_log2),
+    int64_t chunk;             // tokens per CTA
 };
 
 // Arguments of the linear layer (see linear_few.cu, linear_many.cu).

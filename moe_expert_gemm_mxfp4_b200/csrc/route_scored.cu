@@ -9,10 +9,10 @@
 //   (value desc, index asc) are kept; the top_k experts of those by (c desc, id asc);
 //   w_j = s_{id_j}, over their sum if renormalised, times scale.
 // The choice is the one that 64-bit arithmetic makes, so that two experts whose scores lie a
-// rounding of fp32 apart are not swapped.  It is made in fp32 with a bound on the error of c;
-// where two neighbours of the chosen order (the first one left out among them) or the
-// groups on both sides of the cut lie closer than that, the token is chosen again in 64 bits
-// (a few tokens in a thousand; all of them in 64 bits took 2.8 times as long).
+// rounding of fp32 apart are not swapped.  It is made in fp32 with a bound on the error of c.
+// Where two neighbours of the chosen order (the first one left out among them) lie closer
+// than that, the candidates' c are computed again in 64 bits, a lane each, and ranked; where
+// the groups on both sides of the cut do, the whole token is.
 //
 // Up to 256 tokens: one launch, a cluster of up to 8 CTAs with a warp per token; the CTAs exchange
 // their per-expert pair counts through distributed shared memory.  More tokens: two kernels over
@@ -68,6 +68,11 @@ struct Lanes {
     __device__ __forceinline__ int expert(int i) const { return base + seg * i; }
 };
 
+// e^(l - m) for the row's largest logit m, which may be infinite (then 1 at each that is m).
+__device__ __forceinline__ double exp_below(float l, float m) {
+    return l == -INFINITY ? 0.0 : l == m ? 1.0 : exp(static_cast<double>(l) - m);
+}
+
 // The chosen experts of one token in 64 bits: lane j < top_k returns the id of slot j.  NI
 // items per lane hold a whole row (E <= 256 over the lanes of n_groups segments).
 template <bool kBf16, int NI>
@@ -102,7 +107,7 @@ __device__ __noinline__ int choose64(const RouteScoredArgs& a, int64_t t, int la
         for (int i = 0; i < NI; ++i) {
             const double d = l[i];
             if (a.score == MXFP4_SCORE_SOFTMAX) {
-                c[i] = l[i] == -INFINITY ? 0.0 : l[i] == m ? 1.0 : exp(d - m);
+                c[i] = exp_below(l[i], m);
                 if (c[i] == c[i]) sum += c[i];
             } else {
                 c[i] = 1.0 / (1.0 + exp(-d));
@@ -171,6 +176,45 @@ __device__ __noinline__ int choose64(const RouteScoredArgs& a, int64_t t, int la
         for (int i = 0; i < NI; ++i)
             if (L.has(i) && L.expert(i) == id) live &= ~(1u << i);
         if (lane == j) mine = id;
+    }
+    return mine;
+}
+
+// The first n lanes' experts (packed keys in fp32's order, at least the top_k best of the token and
+// nothing nearer than fp32 tells behind them) in the exact order: lane j < top_k returns slot j.
+template <bool kBf16>
+__device__ __noinline__ int resolve64(const RouteScoredArgs& a, int64_t t, int lane, uint32_t packed, int n) {
+    const int id = 255 - static_cast<int>(packed & 255u);
+    const int64_t row = t * a.E;
+    const float l = lane < n ? load_logit<kBf16>(a.logits, row + id) : -INFINITY;
+    double c = l;
+    if (!a.by_logit) {
+        if (a.score == MXFP4_SCORE_SOFTMAX) {   // (no NaN in a row that comes here)
+            float m = -INFINITY;
+            for (int e = lane; e < a.E; e += 32) m = fmaxf(m, load_logit<kBf16>(a.logits, row + e));
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
+            double sum = 0.0;
+            for (int e = lane; e < a.E; e += 32) sum += exp_below(load_logit<kBf16>(a.logits, row + e), m);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
+            c = exp_below(l, m) / sum;
+        } else {
+            c = 1.0 / (1.0 + exp(-c));
+        }
+        if (lane < n && a.bias) c += a.bias[id];
+        if (l == -INFINITY) c = -static_cast<double>(INFINITY);
+    }
+    int rank = 0;
+    for (int i = 0; i < n; ++i) {
+        const double u = __shfl_sync(kFull, c, i);
+        const int uid = __shfl_sync(kFull, id, i);
+        rank += u > c || (u == c && uid < id);
+    }
+    int mine = 0;
+    for (int i = 0; i < n; ++i) {
+        const int r = __shfl_sync(kFull, rank, i), e = __shfl_sync(kFull, id, i);
+        if (r == lane) mine = e;
     }
     return mine;
 }
@@ -261,7 +305,8 @@ __device__ __forceinline__ int choose(const RouteScoredArgs& a, const Steps& st,
     // Two exact c further apart than err keep their order in fp32.  With d = l - m: exp's argument
     // is rounded (|d| 2^-23.4 of the result) and ex2 is off by 2^-22, so e^d by at most 2^-21.5
     // absolutely; the sum of at most 21 rounded additions and the quotient keep s within 2^-18 of
-    // the largest score.  A sigmoid is within s (1 - s) |l| 2^-23.4 + 2^-21 < 2^-20.
+    // the largest score.  A sigmoid: (1 - s) s (|l| 2^-23.4 + 2^-22) for e^-l, 2^-24 s for the sum
+    // and 2^-23 s for the quotient, together below 2^-21.4.
     float err = 0.f;
     if (a.score == MXFP4_SCORE_SOFTMAX) {
         if (!a.by_logit || !a.renorm) {
@@ -287,7 +332,7 @@ __device__ __forceinline__ int choose(const RouteScoredArgs& a, const Steps& st,
             }
         }
     } else if (!a.by_logit) {
-        err = 0x1p-19f;
+        err = 0x1.8p-21f;   // twice 2^-21.4
 #pragma unroll
         for (int i = 0; i < NI; ++i)
             c[i] = c[i] == -INFINITY ? -INFINITY : rcp(1.f + ex2(-kLog2e * c[i])) + b[i];
@@ -308,18 +353,19 @@ __device__ __forceinline__ int choose(const RouteScoredArgs& a, const Steps& st,
             t1 = fmaxf(t1, u1);
         }
         const float second = a.group_top == 2 && t2 != -INFINITY ? t2 : 0.f;
-        // the group's place: its value in 27 bits, then the complement of its index
-        const uint32_t key = on ? (order_key32(t1 + second) & ~31u) | static_cast<uint32_t>(31 - L.g) : 0u;
+        const float v = t1 + second;
         int rank = 0;
 #pragma unroll 4
-        for (int g = 0; g < a.n_groups; ++g) rank += __shfl_sync(kFull, key, g << a.seg_log2) > key;
+        for (int g = 0; g < a.n_groups; ++g) {
+            const float u = __shfl_sync(kFull, v, g << a.seg_log2);
+            rank += u > v || (u == v && g < L.g);
+        }
         if (!exact) {   // the last group kept and the first left out
-            const uint32_t last = __reduce_max_sync(kFull, on && rank == a.top_groups - 1 ? key : 0u);
-            const uint32_t first = __reduce_max_sync(kFull, on && rank == a.top_groups ? key : 0u);
-            const bool edge = on && (rank == a.top_groups - 1 || rank == a.top_groups);
-            const float x = order_value32(last | 31u), y = order_value32(first & ~31u);
+            const bool kept = on && rank == a.top_groups - 1, edge = kept || (on && rank == a.top_groups);
+            const float x = order_value32(__reduce_max_sync(kFull, kept ? order_key32(v) : 0u));
+            const float y = order_value32(__reduce_max_sync(kFull, edge && !kept ? order_key32(v) : 0u));
             const float big = edge ? fmaxf(fabsf(t1), fabsf(second)) : 0.f;
-            close = edge && y > -INFINITY && !(x - y > 2.f * err + 0x1p-16f * fmaxf(fabsf(x), fabsf(y)) + 0x1p-21f * big);
+            close = edge && y > -INFINITY && !(x - y > 2.f * err + 0x1p-21f * big);
         }
         on = on && rank < a.top_groups;
     }
@@ -355,21 +401,40 @@ __device__ __forceinline__ int choose(const RouteScoredArgs& a, const Steps& st,
         close |= !(fabsf(all) < INFINITY);   // NaN or an infinity, or sums past fp32's range
     }
     sort_descending<NI>(key);
-    int mine = 0;
-    uint32_t prev = 0xFFFFFFFFu;
-    const int rounds = exact ? a.top_k : a.top_k + 1;   // one more: the first left out
-#pragma unroll 1
-    for (int j = 0; j < rounds; ++j) {
-        const uint32_t top = __reduce_max_sync(kFull, key[0]);
-        if (!exact) close |= j > 0 && top >= 4u << 8 && (prev >> 8) - (top >> 8) <= near;
-        prev = top;
-        if (lane == j) mine = 255 - static_cast<int>(top & 255u);
+    uint32_t got = 0, top = 0;   // lane j: the j-th best
+    auto next = [&] {
+        top = __reduce_max_sync(kFull, key[0]);
         const bool pop = key[0] == top;   // keys are distinct, but for the 0 of empty lists
 #pragma unroll
         for (int i = 0; i < NI; ++i) key[i] = pop ? (i + 1 < NI ? key[i + 1] : 0u) : key[i];
+    };
+    const int rounds = exact ? a.top_k : a.top_k + 1;   // one more: the first left out
+#pragma unroll 1
+    for (int j = 0; j < rounds; ++j) {
+        next();
+        if (lane == j) got = top;
     }
-    if (__any_sync(kFull, close)) return choose64<kBf16, NI>(a, t, lane);
-    return mine;
+    if (!exact) {
+        if (__any_sync(kFull, close)) return choose64<kBf16, NI>(a, t, lane);
+        const uint32_t prev = __shfl_up_sync(kFull, got, 1);
+        const bool tie = lane > 0 && got >= 4u << 8 && (prev >> 8) - (got >> 8) <= near;   // got is 0 past the rounds
+        const uint32_t ties = __ballot_sync(kFull, tie);
+        if (ties) {
+            int n = a.top_k;
+            if ((ties >> n) & 1u) {   // the first left out is close: so may be those behind it
+                uint32_t last = top;
+                for (++n; n < 32; ++n) {
+                    next();
+                    if (top < 4u << 8 || (last >> 8) - (top >> 8) > near) break;
+                    if (lane == n) got = top;
+                    last = top;
+                }
+                if (n == 32) return choose64<kBf16, NI>(a, t, lane);
+            }
+            return resolve64<kBf16>(a, t, lane, got, n);
+        }
+    }
+    return 255 - static_cast<int>(got & 255u);
 }
 
 // log of the smallest 64-bit number, 2^-1074, less half a step: scores below it are 0
@@ -526,7 +591,7 @@ route_scored_cluster_kernel(const __grid_constant__ RouteScoredArgs a) {
     for (int e = threadIdx.x; e < kMaxE; e += blockDim.x) s_hist[e] = 0;
     __syncthreads();
     const int nb = gridDim.x, me = static_cast<int>(cluster_rank());
-    const int64_t t0 = a.T * me / nb, t1 = a.T * (me + 1) / nb;
+    const int64_t t0 = min(a.T, a.chunk * me), t1 = min(a.T, t0 + a.chunk);
     topk_chunk<kBf16, NI>(a, t0, t1, s_hist);
     __syncwarp();
     cluster_barrier();   // every CTA's counts are there, and this one's ids
@@ -564,7 +629,7 @@ route_scored_topk_kernel(const __grid_constant__ RouteScoredArgs a) {
     __shared__ int32_t s_hist[kMaxE];
     for (int e = threadIdx.x; e < kMaxE; e += blockDim.x) s_hist[e] = 0;
     __syncthreads();
-    const int64_t t0 = a.T * blockIdx.x / gridDim.x, t1 = a.T * (blockIdx.x + 1) / gridDim.x;
+    const int64_t t0 = a.chunk * blockIdx.x, t1 = min(a.T, t0 + a.chunk);
     topk_chunk<kBf16, NI>(a, t0, t1, s_hist);
     __syncthreads();
     const int row = (a.E + 3) / 4 * 4;   // rows of whole 16-byte vectors
@@ -615,18 +680,18 @@ route_scored_place_kernel(const __grid_constant__ RouteScoredArgs a) {
         }
     }
     __syncthreads();
-    const int64_t t0 = a.T * me / nb, t1 = a.T * (me + 1) / nb;
+    const int64_t t0 = a.chunk * me, t1 = min(a.T, t0 + a.chunk);
     place_chunk(a, t0 * a.top_k, t1 * a.top_k, s_base, s_cnt);
 }
 
-// Chunks of a batch: 8 tokens each, a warp per token, while the SMs last, then one CTA per SM.
-int64_t chunks_of(int64_t T) {
-    const int64_t n = (T + kFewWarps - 1) / kFewWarps;
-    return n < kMaxChunks ? n : kMaxChunks;
+// Tokens of a chunk: 8, a warp per token, while the SMs last, then what fills one CTA per SM.
+int64_t chunk_of(int64_t T) {
+    const int64_t n = (T + kMaxChunks - 1) / kMaxChunks;
+    return n < kFewWarps ? kFewWarps : n;
 }
 
 template <bool kBf16, int NI>
-cudaError_t launch(const RouteScoredArgs& a, cudaStream_t stream) {
+cudaError_t launch(RouteScoredArgs a, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     cfg.stream = stream;
@@ -635,17 +700,18 @@ cudaError_t launch(const RouteScoredArgs& a, cudaStream_t stream) {
     if (a.T <= kClusterTokens) {
         const int64_t n = (a.T + kFewWarps - 1) / kFewWarps;
         const unsigned nc = static_cast<unsigned>(n < kMaxCluster ? n : kMaxCluster);
+        a.chunk = (a.T + nc - 1) / nc;
         cfg.gridDim = dim3(nc, 1, 1);
-        cfg.blockDim = dim3(32 * static_cast<unsigned>((a.T + nc - 1) / nc), 1, 1);
+        cfg.blockDim = dim3(32 * static_cast<unsigned>(a.chunk), 1, 1);
         attr[0].id = cudaLaunchAttributeClusterDimension;
         attr[0].val.clusterDim.x = nc;
         attr[0].val.clusterDim.y = 1;
         attr[0].val.clusterDim.z = 1;
         return cudaLaunchKernelEx(&cfg, route_scored_cluster_kernel<kBf16, NI>, a);
     }
-    const unsigned nb = static_cast<unsigned>(chunks_of(a.T));
-    const int64_t per = (a.T + nb - 1) / nb;   // tokens of a chunk
-    const int threads = 32 * static_cast<int>(per < kFewWarps ? kFewWarps : per > kWarps ? kWarps : per);
+    a.chunk = chunk_of(a.T);
+    const unsigned nb = static_cast<unsigned>((a.T + a.chunk - 1) / a.chunk);
+    const int threads = 32 * static_cast<int>(a.chunk > kWarps ? kWarps : a.chunk);
     route_scored_topk_kernel<kBf16, NI><<<nb, threads, 0, stream>>>(a);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
@@ -659,7 +725,7 @@ cudaError_t launch(const RouteScoredArgs& a, cudaStream_t stream) {
 }  // namespace
 
 size_t route_scored_ws_bytes(int64_t T, int64_t E) {
-    const int64_t n = chunks_of(T);
+    const int64_t n = (T + chunk_of(T) - 1) / chunk_of(T);
     return T <= kClusterTokens ? 0 : static_cast<size_t>(n * ((E + 3) / 4 * 4)) * sizeof(int32_t);
 }
 
