@@ -68,9 +68,40 @@ struct Lanes {
     __device__ __forceinline__ int expert(int i) const { return base + seg * i; }
 };
 
+// 64-bit arithmetic in few instructions: a launch meets this code once, cold, and fetching the
+// library functions' took longer than running them (a token in 64 bits cost 10 us).
+// 1 / k!, k = 0 .. 13
+__device__ __constant__ double kInvFact[14] = {1.0, 1.0, 1.0 / 2, 1.0 / 6, 1.0 / 24, 1.0 / 120, 1.0 / 720, 1.0 / 5040,
+                                               1.0 / 40320, 1.0 / 362880, 1.0 / 3628800, 1.0 / 39916800,
+                                               1.0 / 479001600, 1.0 / 6227020800.0};
+// e^x for x <= 0: x = n ln 2 + r, |r| <= 0.35, Taylor's series of e^r (the term after the last is
+// below 2^-57), ln 2 in two parts of which n times the first is exact.
+__device__ __forceinline__ double exp_neg(double x) {
+    if (x < -745.2) return 0.0;
+    const double n = rint(x * 1.4426950408889634);
+    double r = fma(n, -0x1.62e42fefp-1, x);
+    r = fma(n, -0x1.473de6af278edp-34, r);
+    double p = kInvFact[13];
+#pragma unroll 1
+    for (int k = 12; k >= 0; --k) p = fma(p, r, kInvFact[k]);
+    const int e = static_cast<int>(n), h = e / 2;      // 2^e in two factors: e reaches -1075
+    return p * __longlong_as_double(static_cast<int64_t>(1023 + h) << 52) *
+           __longlong_as_double(static_cast<int64_t>(1023 + e - h) << 52);
+}
+// 1 / x for x >= 1 in fp32's range: Newton's steps double the digits of the hardware's reciprocal.
+__device__ __forceinline__ double inv64(double x) {
+    double y = 1.f / static_cast<float>(x);
+#pragma unroll 1
+    for (int i = 0; i < 2; ++i) y = fma(y, fma(-x, y, 1.0), y);
+    return y;
+}
+__device__ __forceinline__ double sigmoid64(float l) {
+    const double t = exp_neg(-fabs(static_cast<double>(l))), y = inv64(1.0 + t);
+    return l < 0.f ? t * y : y;
+}
 // e^(l - m) for the row's largest logit m, which may be infinite (then 1 at each that is m).
 __device__ __forceinline__ double exp_below(float l, float m) {
-    return l == -INFINITY ? 0.0 : l == m ? 1.0 : exp(static_cast<double>(l) - m);
+    return l == -INFINITY ? 0.0 : l == m ? 1.0 : l != l ? static_cast<double>(l) : exp_neg(static_cast<double>(l) - m);
 }
 
 // The chosen experts of one token in 64 bits: lane j < top_k returns the id of slot j.  NI
@@ -83,7 +114,7 @@ __device__ __noinline__ int choose64(const RouteScoredArgs& a, int64_t t, int la
     const int64_t row = t * a.E;
     float l[NI];
     float m = -INFINITY;
-#pragma unroll
+#pragma unroll 1
     for (int i = 0; i < NI; ++i) {
         l[i] = -INFINITY;
         if (L.has(i)) {
@@ -94,41 +125,37 @@ __device__ __noinline__ int choose64(const RouteScoredArgs& a, int64_t t, int la
     }
     // without a bias the order of the scores is the order of the logits
     if (a.by_logit) {
-#pragma unroll
+#pragma unroll 1
         for (int i = 0; i < NI; ++i) c[i] = l[i];
     } else {
         double sum = 1.0;
         if (a.score == MXFP4_SCORE_SOFTMAX) {
-#pragma unroll
+#pragma unroll 1
             for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
             sum = 0.0;
         }
-#pragma unroll
+#pragma unroll 1
         for (int i = 0; i < NI; ++i) {
-            const double d = l[i];
-            if (a.score == MXFP4_SCORE_SOFTMAX) {
-                c[i] = exp_below(l[i], m);
-                if (c[i] == c[i]) sum += c[i];
-            } else {
-                c[i] = 1.0 / (1.0 + exp(-d));
-            }
+            c[i] = a.score == MXFP4_SCORE_SOFTMAX ? exp_below(l[i], m) : sigmoid64(l[i]);
+            if (a.score == MXFP4_SCORE_SOFTMAX && c[i] == c[i]) sum += c[i];
         }
         if (a.score == MXFP4_SCORE_SOFTMAX) {
-#pragma unroll
+#pragma unroll 1
             for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
         }
-#pragma unroll
+        const double scale = sum > 0.0 ? inv64(sum) : 0.0;   // a row's sum is 0, or at least 1
+#pragma unroll 1
         for (int i = 0; i < NI; ++i) {
             if (L.has(i)) {
                 const double b = a.bias ? a.bias[L.expert(i)] : 0.f;
-                c[i] = l[i] == -INFINITY ? -static_cast<double>(INFINITY) : c[i] / sum + b;
+                c[i] = l[i] == -INFINITY ? -static_cast<double>(INFINITY) : c[i] * scale + b;
             }
         }
     }
     if (a.n_groups > 1) {
         const double ninf = -static_cast<double>(INFINITY);
         double t1 = ninf, t2 = ninf;
-#pragma unroll
+#pragma unroll 1
         for (int i = 0; i < NI; ++i) {
             if (L.has(i) && c[i] == c[i]) {
                 t2 = c[i] > t1 ? t1 : (c[i] > t2 ? c[i] : t2);
@@ -152,7 +179,7 @@ __device__ __noinline__ int choose64(const RouteScoredArgs& a, int64_t t, int la
     for (int j = 0; j < a.top_k; ++j) {
         uint64_t best = 0;
         int id = 0x7FFFFFFF;
-#pragma unroll
+#pragma unroll 1
         for (int i = 0; i < NI; ++i) {
             if ((live >> i) & 1u) {
                 const uint64_t k = order_key(c[i]);
@@ -163,7 +190,7 @@ __device__ __noinline__ int choose64(const RouteScoredArgs& a, int64_t t, int la
                 }
             }
         }
-#pragma unroll
+#pragma unroll 1
         for (int o = 16; o > 0; o >>= 1) {
             const uint64_t ob = __shfl_xor_sync(kFull, best, o);
             const int oid = __shfl_xor_sync(kFull, id, o);
@@ -172,7 +199,7 @@ __device__ __noinline__ int choose64(const RouteScoredArgs& a, int64_t t, int la
                 id = oid;
             }
         }
-#pragma unroll
+#pragma unroll 1
         for (int i = 0; i < NI; ++i)
             if (L.has(i) && L.expert(i) == id) live &= ~(1u << i);
         if (lane == j) mine = id;
@@ -198,9 +225,9 @@ __device__ __noinline__ int resolve64(const RouteScoredArgs& a, int64_t t, int l
             for (int e = lane; e < a.E; e += 32) sum += exp_below(load_logit<kBf16>(a.logits, row + e), m);
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
-            c = exp_below(l, m) / sum;
+            c = exp_below(l, m) * inv64(sum);
         } else {
-            c = 1.0 / (1.0 + exp(-c));
+            c = sigmoid64(l);
         }
         if (lane < n && a.bias) c += a.bias[id];
         if (l == -INFINITY) c = -static_cast<double>(INFINITY);
@@ -513,57 +540,67 @@ __device__ void scan_experts(const int32_t* s_tot, int32_t* s_off, int E) {
 }
 
 // perm and inv of pairs [p0, p1): s_base[e] is the sorted position of the range's
-// first pair of expert e.  Each warp takes a contiguous run of 32-pair strips; the
+// first pair of expert e.  Each warp takes a run of up to kHold 32-pair strips at a time; the
 // lanes of a strip that hold the same expert are one match mask.  s_cnt: [warps][kMaxE].
-__device__ __forceinline__ void place_chunk(const RouteScoredArgs& a, int64_t p0, int64_t p1, const int32_t* s_base,
+constexpr int kHold = 4;
+__device__ __forceinline__ void place_chunk(const RouteScoredArgs& a, int64_t p0, int64_t p1, int32_t* s_base,
                                             int32_t* s_cnt) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x / 32;
-    const int64_t strips = (p1 - p0 + 31) / 32, per = (strips + warps - 1) / warps;
-    const int used = static_cast<int>((strips + per - 1) / per);   // warps with strips
-    const int64_t s0 = min(strips, per * warp), s1 = min(strips, s0 + per);
-    for (int i = threadIdx.x; i < used * kMaxE; i += blockDim.x) s_cnt[i] = 0;
-    __syncthreads();
-    int32_t* cnt = s_cnt + warp * kMaxE;
     const uint32_t lt = (1u << lane) - 1u;
-    uint32_t mask = 0;
-    int e = 0;
-    for (int64_t s = s0; s < s1; ++s) {
-        const int64_t p = p0 + 32 * s + lane;
-        e = p < p1 ? a.ids[p] : kMaxE + lane;
-        mask = __match_any_sync(kFull, e);
-        if (p < p1 && (mask & lt) == 0) cnt[e] += __popc(mask);
-        __syncwarp();
-    }
-    __syncthreads();
-    for (int x = threadIdx.x; x < a.E; x += blockDim.x) {
-        int run = s_base[x];
-        for (int w = 0; w < used; w += 8) {
-            int v[8];
+    int32_t* cnt = s_cnt + warp * kMaxE;
+    for (; p0 < p1; p0 += 32 * kHold * warps) {
+        const int strips = static_cast<int>(min(static_cast<int64_t>(kHold * warps), (p1 - p0 + 31) / 32));
+        const int per = (strips + warps - 1) / warps, used = (strips + per - 1) / per;   // strips a warp, warps
+        int e[kHold];
+        uint32_t mask[kHold];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = w + i < used ? s_cnt[(w + i) * kMaxE + x] : 0;
+        for (int s = 0; s < kHold; ++s) {
+            const int64_t p = p0 + 32 * (per * warp + s) + lane;
+            e[s] = s < per && p < p1 ? a.ids[p] : kMaxE + lane;
+        }
+        for (int i = threadIdx.x; i < used * (kMaxE / 4); i += blockDim.x)
+            reinterpret_cast<int4*>(s_cnt)[i] = make_int4(0, 0, 0, 0);
+        __syncthreads();
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                if (w + i < used) s_cnt[(w + i) * kMaxE + x] = run;
-                run += v[i];
+        for (int s = 0; s < kHold; ++s) {
+            if (s < per) {
+                mask[s] = __match_any_sync(kFull, e[s]);
+                if (e[s] < kMaxE && (mask[s] & lt) == 0) cnt[e[s]] += __popc(mask[s]);
+                __syncwarp();
             }
         }
-    }
-    __syncthreads();
-    for (int64_t s = s0; s < s1; ++s) {
-        const int64_t p = p0 + 32 * s + lane;
-        if (per > 1) {   // else the first pass's strip is still at hand
-            e = p < p1 ? a.ids[p] : kMaxE + lane;
-            mask = __match_any_sync(kFull, e);
+        __syncthreads();
+        for (int x = threadIdx.x; x < a.E; x += blockDim.x) {
+            int run = s_base[x];
+            for (int w = 0; w < used; w += 8) {
+                int v[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] = w + i < used ? s_cnt[(w + i) * kMaxE + x] : 0;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    if (w + i < used) s_cnt[(w + i) * kMaxE + x] = run;
+                    run += v[i];
+                }
+            }
+            s_base[x] = run;
         }
-        const int first = p < p1 ? cnt[e] : 0;
-        __syncwarp();
-        if (p < p1) {
-            const int pos = first + __popc(mask & lt);
-            a.perm[pos] = static_cast<int32_t>(p);
-            a.inv[p] = pos;
-            if ((mask & lt) == 0) cnt[e] = first + __popc(mask);
+        __syncthreads();
+#pragma unroll
+        for (int s = 0; s < kHold; ++s) {
+            if (s < per) {
+                const int64_t p = p0 + 32 * (per * warp + s) + lane;
+                const int first = e[s] < kMaxE ? cnt[e[s]] : 0;
+                __syncwarp();
+                if (e[s] < kMaxE) {
+                    const int pos = first + __popc(mask[s] & lt);
+                    a.perm[pos] = static_cast<int32_t>(p);
+                    a.inv[p] = pos;
+                    if ((mask[s] & lt) == 0) cnt[e[s]] = first + __popc(mask[s]);
+                }
+                __syncwarp();
+            }
         }
-        __syncwarp();
+        __syncthreads();   // the counts are used up
     }
 }
 
@@ -587,7 +624,8 @@ __device__ __forceinline__ int32_t ld_rank(const int32_t* p, uint32_t rank) {   
 template <bool kBf16, int NI>
 __global__ void __launch_bounds__(kThreads)
 route_scored_cluster_kernel(const __grid_constant__ RouteScoredArgs a) {
-    __shared__ int32_t s_hist[kMaxE], s_sum[kMaxE], s_base[kMaxE], s_off[kMaxE + 1], s_cnt[kWarps * kMaxE];
+    __shared__ int32_t s_hist[kMaxE], s_sum[kMaxE], s_base[kMaxE], s_off[kMaxE + 1];
+    __shared__ __align__(16) int32_t s_cnt[kWarps * kMaxE];
     for (int e = threadIdx.x; e < kMaxE; e += blockDim.x) s_hist[e] = 0;
     __syncthreads();
     const int nb = gridDim.x, me = static_cast<int>(cluster_rank());
@@ -638,23 +676,29 @@ route_scored_topk_kernel(const __grid_constant__ RouteScoredArgs a) {
 
 __global__ void __launch_bounds__(kThreads)
 route_scored_place_kernel(const __grid_constant__ RouteScoredArgs a) {
-    // the threads in parts of kMaxE / 4, four experts per thread: part q sums chunks q, q + parts, ...
+    // the threads in parts of kMaxE / 4, four experts per thread: part q sums chunks q, q + kParts, ...
     __shared__ int32_t s_off[kMaxE + 1], s_base[kMaxE], s_sum[kMaxE];
     __shared__ __align__(16) int32_t s_cnt[kWarps * kMaxE];   // first the parts' sums, then the warps' counts
-    const int parts = blockDim.x / (kMaxE / 4);                // 2 parts * kMaxE <= warps * kMaxE
+    constexpr int kParts = kThreads / (kMaxE / 4);
+    static_assert(2 * kParts * kMaxE <= kWarps * kMaxE, "the parts' sums fit");
     int4(*s_tot)[kMaxE / 4] = reinterpret_cast<int4(*)[kMaxE / 4]>(s_cnt);
-    int4(*s_before)[kMaxE / 4] = s_tot + parts;
+    int4(*s_before)[kMaxE / 4] = s_tot + kParts;
     const int nb = gridDim.x, me = blockIdx.x;
     const int e4 = threadIdx.x % (kMaxE / 4), part = threadIdx.x / (kMaxE / 4), row4 = (a.E + 3) / 4;
     asm volatile("griddepcontrol.wait;" ::: "memory");   // the chunks' counts and ids are complete
-    if (e4 < row4 && part < parts) {
+    if (e4 < row4) {
         int4 tot = make_int4(0, 0, 0, 0), before = tot;
-        const int4* counts = reinterpret_cast<const int4*>(a.chunk_counts) + e4;
-#pragma unroll 10
-        for (int c = part; c < nb; c += parts) {
-            const int4 v = counts[c * row4];
-            tot.x += v.x, tot.y += v.y, tot.z += v.z, tot.w += v.w;
-            if (c < me) before.x += v.x, before.y += v.y, before.z += v.z, before.w += v.w;
+        constexpr int kEach = (kMaxChunks + kParts - 1) / kParts;
+        int4 v[kEach];   // all in flight
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+            const int c = part + kParts * i;
+            v[i] = c < nb ? __ldcg(reinterpret_cast<const int4*>(a.chunk_counts) + c * row4 + e4) : make_int4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+            tot.x += v[i].x, tot.y += v[i].y, tot.z += v[i].z, tot.w += v[i].w;
+            if (part + kParts * i < me) before.x += v[i].x, before.y += v[i].y, before.z += v[i].z, before.w += v[i].w;
         }
         s_tot[part][e4] = tot;
         s_before[part][e4] = before;
@@ -662,7 +706,8 @@ route_scored_place_kernel(const __grid_constant__ RouteScoredArgs a) {
     __syncthreads();
     for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
         int tot = 0, before = 0;
-        for (int q = 0; q < parts; ++q) {
+#pragma unroll
+        for (int q = 0; q < kParts; ++q) {
             tot += reinterpret_cast<const int32_t*>(s_tot[q])[e];
             before += reinterpret_cast<const int32_t*>(s_before[q])[e];
         }
@@ -716,7 +761,7 @@ cudaError_t launch(RouteScoredArgs a, cudaStream_t stream) {
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     cfg.gridDim = dim3(nb, 1, 1);
-    cfg.blockDim = dim3(threads, 1, 1);
+    cfg.blockDim = dim3(kThreads, 1, 1);
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     return cudaLaunchKernelEx(&cfg, route_scored_place_kernel, a);
