@@ -46,6 +46,15 @@ __device__ __forceinline__ uint64_t order_key(double v) {
     return (u >> 63) ? ~u : (u | 0x8000000000000000ull);
 }
 
+// The same order on 32 bits; 0 is left for items that are not in the running.
+__device__ __forceinline__ uint32_t order_key32(float v) {
+    const uint32_t u = __float_as_uint(v + 0.f);   // -0 + 0 = +0
+    return v != v ? 1u : (u >> 31) ? ~u : (u | 0x80000000u);
+}
+__device__ __forceinline__ float order_value32(uint32_t key) {
+    return __uint_as_float(key == 1u ? 0x7FC00000u : (key >> 31) ? (key & 0x7FFFFFFFu) : ~key);
+}
+
 template <bool kBf16>
 __device__ __forceinline__ float load_logit(const void* p, int64_t i) {
     return kBf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]) : static_cast<const float*>(p)[i];
@@ -75,7 +84,7 @@ __device__ __constant__ double kInvFact[14] = {1.0, 1.0, 1.0 / 2, 1.0 / 6, 1.0 /
                                                1.0 / 40320, 1.0 / 362880, 1.0 / 3628800, 1.0 / 39916800,
                                                1.0 / 479001600, 1.0 / 6227020800.0};
 // e^x for x <= 0: x = n ln 2 + r, |r| <= 0.35, Taylor's series of e^r (the term after the last is
-// below 2^-57), ln 2 in two parts of which n times the first is exact.
+// below 2^-57), ln 2 in two parts of which n times the first is exact (Cody and Waite).
 __device__ __forceinline__ double exp_neg(double x) {
     if (x < -745.2) return 0.0;
     const double n = rint(x * 1.4426950408889634);
@@ -104,92 +113,99 @@ __device__ __forceinline__ double exp_below(float l, float m) {
     return l == -INFINITY ? 0.0 : l == m ? 1.0 : l != l ? static_cast<double>(l) : exp_neg(static_cast<double>(l) - m);
 }
 
-// The chosen experts of one token in 64 bits: lane j < top_k returns the id of slot j.  NI
-// items per lane hold a whole row (E <= 256 over the lanes of n_groups segments).
-template <bool kBf16, int NI>
-__device__ __noinline__ int choose64(const RouteScoredArgs& a, int64_t t, int lane) {
+// What a softmax score needs of its row, in 64 bits.
+struct Row64 {
+    float m;
+    double scale;   // 1 / sum of e^(l - m) over the row's numbers (0 for a row without any)
+};
+template <bool kBf16>
+__device__ __forceinline__ Row64 row64(const RouteScoredArgs& a, int64_t row, int lane) {
+    Row64 r = {-INFINITY, 0.0};
+    if (a.by_logit || a.score != MXFP4_SCORE_SOFTMAX) return r;
+    for (int e = lane; e < a.E; e += 32) r.m = fmaxf(r.m, load_logit<kBf16>(a.logits, row + e));   // NaN left out
+    r.m = order_value32(__reduce_max_sync(kFull, order_key32(r.m)));
+    double sum = 0.0;
+#pragma unroll 1
+    for (int e = lane; e < a.E; e += 32) {
+        const double z = exp_below(load_logit<kBf16>(a.logits, row + e), r.m);
+        sum += z == z ? z : 0.0;
+    }
+    __syncwarp();
+#pragma unroll 1
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
+    if (sum > 0.0) r.scale = inv64(sum);   // at least 1 then
+    return r;
+}
+// c of expert e, whose logit is l.
+__device__ __forceinline__ double choice64(const RouteScoredArgs& a, const Row64& r, float l, int e) {
+    if (a.by_logit) return l;
+    if (l == -INFINITY) return l;
+    const double s = a.score == MXFP4_SCORE_SOFTMAX ? exp_below(l, r.m) * r.scale : sigmoid64(l);
+    return s + (a.bias ? a.bias[e] : 0.f);
+}
+
+// The place of this lane's group among the groups, in 64 bits.
+template <bool kBf16>
+__device__ __noinline__ int group_rank64(const RouteScoredArgs& a, int64_t t, int lane) {
     const Lanes L(a, lane);
-    double c[NI];
-    uint32_t live = 0;   // items that may still be chosen
     const int64_t row = t * a.E;
-    float l[NI];
-    float m = -INFINITY;
+    const Row64 r64 = row64<kBf16>(a, row, lane);
+    const double ninf = -static_cast<double>(INFINITY);
+    double t1 = ninf, t2 = ninf;
 #pragma unroll 1
-    for (int i = 0; i < NI; ++i) {
-        l[i] = -INFINITY;
-        if (L.has(i)) {
-            l[i] = load_logit<kBf16>(a.logits, row + L.expert(i));
-            live |= 1u << i;
-            if (l[i] > m) m = l[i];
-        }
+    for (int i = 0; L.has(i); ++i) {
+        const int e = L.expert(i);
+        const double c = choice64(a, r64, load_logit<kBf16>(a.logits, row + e), e);   // NaN takes no part
+        t2 = c > t1 ? t1 : c > t2 ? c : t2;
+        t1 = c > t1 ? c : t1;
     }
-    // without a bias the order of the scores is the order of the logits
-    if (a.by_logit) {
+    __syncwarp();
 #pragma unroll 1
-        for (int i = 0; i < NI; ++i) c[i] = l[i];
-    } else {
-        double sum = 1.0;
-        if (a.score == MXFP4_SCORE_SOFTMAX) {
-#pragma unroll 1
-            for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
-            sum = 0.0;
-        }
-#pragma unroll 1
-        for (int i = 0; i < NI; ++i) {
-            c[i] = a.score == MXFP4_SCORE_SOFTMAX ? exp_below(l[i], m) : sigmoid64(l[i]);
-            if (a.score == MXFP4_SCORE_SOFTMAX && c[i] == c[i]) sum += c[i];
-        }
-        if (a.score == MXFP4_SCORE_SOFTMAX) {
-#pragma unroll 1
-            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
-        }
-        const double scale = sum > 0.0 ? inv64(sum) : 0.0;   // a row's sum is 0, or at least 1
-#pragma unroll 1
-        for (int i = 0; i < NI; ++i) {
-            if (L.has(i)) {
-                const double b = a.bias ? a.bias[L.expert(i)] : 0.f;
-                c[i] = l[i] == -INFINITY ? -static_cast<double>(INFINITY) : c[i] * scale + b;
-            }
-        }
+    for (int o = L.seg >> 1; o > 0; o >>= 1) {
+        const double u1 = __shfl_xor_sync(kFull, t1, o), u2 = __shfl_xor_sync(kFull, t2, o);
+        t2 = fmax(fmin(t1, u1), fmax(t2, u2));
+        t1 = fmax(t1, u1);
     }
-    if (a.n_groups > 1) {
-        const double ninf = -static_cast<double>(INFINITY);
-        double t1 = ninf, t2 = ninf;
+    const double v = a.group_top == 2 && t2 != ninf ? t1 + t2 : t1;
+    int rank = 0;
 #pragma unroll 1
-        for (int i = 0; i < NI; ++i) {
-            if (L.has(i) && c[i] == c[i]) {
-                t2 = c[i] > t1 ? t1 : (c[i] > t2 ? c[i] : t2);
-                t1 = c[i] > t1 ? c[i] : t1;
-            }
-        }
-        for (int o = L.seg >> 1; o > 0; o >>= 1) {
-            const double u1 = __shfl_xor_sync(kFull, t1, o), u2 = __shfl_xor_sync(kFull, t2, o);
-            t2 = fmax(fmin(t1, u1), fmax(t2, u2));
-            t1 = fmax(t1, u1);
-        }
-        const double v = a.group_top == 2 && t2 != ninf ? t1 + t2 : t1;
-        int rank = 0;
-        for (int g = 0; g < a.n_groups; ++g) {
-            const double u = __shfl_sync(kFull, v, g * L.seg);
-            rank += u > v || (u == v && g < L.g);
-        }
-        if (rank >= a.top_groups) live = 0;
+    for (int g = 0; g < a.n_groups; ++g) {
+        const double u = __shfl_sync(kFull, v, g << a.seg_log2);
+        rank += u > v || (u == v && g < L.g);
     }
+    return rank;
+}
+
+// The chosen experts of one token whose kept groups are known (on: this lane's is one), all in 64 bits:
+// for rows with NaN or infinities and for runs of close values longer than a warp.  Lane
+// j < top_k returns the id of slot j.
+template <bool kBf16>
+__device__ __noinline__ int choose64(const RouteScoredArgs& a, int64_t t, int lane, bool on) {
+    const Lanes L(a, lane);
+    const int64_t row = t * a.E;
+    const Row64 r64 = row64<kBf16>(a, row, lane);
+    uint32_t live = 0;   // items that may still be chosen
+    for (int i = 0; on && L.has(i); ++i) live |= 1u << i;
+    __syncwarp();
     int mine = 0;
+#pragma unroll 1
     for (int j = 0; j < a.top_k; ++j) {
         uint64_t best = 0;
-        int id = 0x7FFFFFFF;
+        int id = 0x7FFFFFFF, at = 0;
 #pragma unroll 1
-        for (int i = 0; i < NI; ++i) {
+        for (int i = 0; (live >> i) != 0; ++i) {
             if ((live >> i) & 1u) {
-                const uint64_t k = order_key(c[i]);
                 const int e = L.expert(i);
+                const uint64_t k = order_key(choice64(a, r64, load_logit<kBf16>(a.logits, row + e), e));
                 if (id == 0x7FFFFFFF || k > best) {   // items ascend in e: the first of equals stays
                     best = k;
                     id = e;
+                    at = i;
                 }
             }
         }
+        __syncwarp();
+        const int own = id;
 #pragma unroll 1
         for (int o = 16; o > 0; o >>= 1) {
             const uint64_t ob = __shfl_xor_sync(kFull, best, o);
@@ -199,9 +215,7 @@ __device__ __noinline__ int choose64(const RouteScoredArgs& a, int64_t t, int la
                 id = oid;
             }
         }
-#pragma unroll 1
-        for (int i = 0; i < NI; ++i)
-            if (L.has(i) && L.expert(i) == id) live &= ~(1u << i);
+        if (own == id) live &= ~(1u << at);
         if (lane == j) mine = id;
     }
     return mine;
@@ -213,25 +227,9 @@ template <bool kBf16>
 __device__ __noinline__ int resolve64(const RouteScoredArgs& a, int64_t t, int lane, uint32_t packed, int n) {
     const int id = 255 - static_cast<int>(packed & 255u);
     const int64_t row = t * a.E;
-    const float l = lane < n ? load_logit<kBf16>(a.logits, row + id) : -INFINITY;
-    double c = l;
-    if (!a.by_logit) {
-        if (a.score == MXFP4_SCORE_SOFTMAX) {   // (no NaN in a row that comes here)
-            float m = -INFINITY;
-            for (int e = lane; e < a.E; e += 32) m = fmaxf(m, load_logit<kBf16>(a.logits, row + e));
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
-            double sum = 0.0;
-            for (int e = lane; e < a.E; e += 32) sum += exp_below(load_logit<kBf16>(a.logits, row + e), m);
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
-            c = exp_below(l, m) * inv64(sum);
-        } else {
-            c = sigmoid64(l);
-        }
-        if (lane < n && a.bias) c += a.bias[id];
-        if (l == -INFINITY) c = -static_cast<double>(INFINITY);
-    }
+    const Row64 r64 = row64<kBf16>(a, row, lane);
+    const double c = choice64(a, r64, lane < n ? load_logit<kBf16>(a.logits, row + id) : -INFINITY, lane < n ? id : 0);
+    __syncwarp();
     int rank = 0;
     for (int i = 0; i < n; ++i) {
         const double u = __shfl_sync(kFull, c, i);
@@ -244,15 +242,6 @@ __device__ __noinline__ int resolve64(const RouteScoredArgs& a, int64_t t, int l
         if (r == lane) mine = e;
     }
     return mine;
-}
-
-// The same order on 32 bits; 0 is left for items that are not in the running.
-__device__ __forceinline__ uint32_t order_key32(float v) {
-    const uint32_t u = __float_as_uint(v + 0.f);   // -0 + 0 = +0
-    return v != v ? 1u : (u >> 31) ? ~u : (u | 0x80000000u);
-}
-__device__ __forceinline__ float order_value32(uint32_t key) {
-    return __uint_as_float(key == 1u ? 0x7FC00000u : (key >> 31) ? (key & 0x7FFFFFFFu) : ~key);
 }
 
 // 2^x and 1 / x in hardware: off by at most 2^-22 and 2^-23 of the result (subnormals become 0).
@@ -392,7 +381,8 @@ __device__ __forceinline__ int choose(const RouteScoredArgs& a, const Steps& st,
             const float x = order_value32(__reduce_max_sync(kFull, kept ? order_key32(v) : 0u));
             const float y = order_value32(__reduce_max_sync(kFull, edge && !kept ? order_key32(v) : 0u));
             const float big = edge ? fmaxf(fabsf(t1), fabsf(second)) : 0.f;
-            close = edge && y > -INFINITY && !(x - y > 2.f * err + 0x1p-21f * big);
+            const bool near = edge && y > -INFINITY && !(x - y > 2.f * err + 0x1p-21f * big);
+            if (__any_sync(kFull, near)) rank = group_rank64<kBf16>(a, t, lane);
         }
         on = on && rank < a.top_groups;
     }
@@ -442,7 +432,7 @@ __device__ __forceinline__ int choose(const RouteScoredArgs& a, const Steps& st,
         if (lane == j) got = top;
     }
     if (!exact) {
-        if (__any_sync(kFull, close)) return choose64<kBf16, NI>(a, t, lane);
+        if (__any_sync(kFull, close)) return choose64<kBf16>(a, t, lane, on);
         const uint32_t prev = __shfl_up_sync(kFull, got, 1);
         const bool tie = lane > 0 && got >= 4u << 8 && (prev >> 8) - (got >> 8) <= near;   // got is 0 past the rounds
         const uint32_t ties = __ballot_sync(kFull, tie);
@@ -456,7 +446,7 @@ __device__ __forceinline__ int choose(const RouteScoredArgs& a, const Steps& st,
                     if (lane == n) got = top;
                     last = top;
                 }
-                if (n == 32) return choose64<kBf16, NI>(a, t, lane);
+                if (n == 32) return choose64<kBf16>(a, t, lane, on);
             }
             return resolve64<kBf16>(a, t, lane, got, n);
         }
@@ -480,10 +470,14 @@ __device__ __forceinline__ float slot_weight(const RouteScoredArgs& a, float l, 
     float top = on && l == l ? l : -INFINITY;
 #pragma unroll
     for (int o = 4; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
+    top = __shfl_sync(kFull, top, 0);
     // e^(l - top), of which a sigmoid is e^top / (1 + e^l) times; above 0 the sigmoid itself
     const float d = !soft && top >= 0.f ? -l : l == top ? 0.f : l - top;
     float w = expf(d);
-    if (!soft) w = top >= 0.f ? __fdividef(1.f, 1.f + w) : __fdividef(w, 1.f + expf(l));
+    if (!soft) {
+        if (top >= 0.f) w = __fdividef(1.f, 1.f + w);
+        else w = __fdividef(w, 1.f + expf(l));
+    }
     // (where the logits order the choice, the row's largest is among the chosen)
     const float ref = !soft ? 0.f : a.by_logit ? top : m;
     if (!on || l == -INFINITY || l - ref < kLogTiny) w = 0.f;
@@ -505,8 +499,9 @@ __device__ void topk_chunk(const RouteScoredArgs& a, int64_t t0, int64_t t1, int
         const float l = on ? load_logit<kBf16>(a.logits, t * a.E + id) : -INFINITY;
         const float w = slot_weight(a, l, on, m, sum);
         if (on) {
-            a.ids[t * a.top_k + lane] = id;
-            a.weights[t * a.top_k + lane] = w;
+            const int p = static_cast<int>(t) * a.top_k + lane;
+            a.ids[p] = id;
+            a.weights[p] = w;
             atomicAdd(&s_hist[id], 1);   // a count: its order does not matter
         }
     }
