@@ -17,6 +17,8 @@
 //   linear_few_prepare  x -> hi and lo tiles in the tensor core's shared-memory image, their
 //                       scales and the weights' scales in its scale-factor layout;
 //   linear_few          one CTA per (128 weight rows, K range, token tile).
+// Up to 16 tokens the spreading warps prepare their CTA's own part instead, and there is one
+// launch: every CTA of a K range then splits the same activations, a few per lane.
 // Roles (8 warps): warp 7 streams packed codes (TMA, 128 bytes per row) into a ring of their own;
 // warps 0-3 spread them over the 16-element containers that the tensor core takes (8
 // bytes of codes, 8 of padding), three instructions per 16 bytes; warp 4 bulk-copies
@@ -41,6 +43,7 @@ constexpr int kBK = 128;             // K per stage: 128 one-byte containers per
 constexpr int kABytes = kBM * kBK;
 constexpr int kAtom = 512;           // scale atom: 128 rows x 4 scales
 constexpr int kMaxMp = 128;          // tokens per tile
+constexpr int kOwnMp = 16;           // largest token tile that is prepared where it is used
 constexpr int kMaxStages = 4;
 constexpr int kCodeBytes = kBM * 128;   // a code slot: 128 bytes (two stages) of each row
 constexpr int kMaxSlots = 4;
@@ -119,9 +122,42 @@ __device__ __forceinline__ void split2(float a, float b, float up, uint32_t& hi,
     lo = l;
 }
 
+// Four elements of a 32-block held by 8 lanes: their parts as four E4M3 bytes each, and the block's
+// scale bytes.  A block with Inf or NaN gets the scale NaN, and NaN elements.
+struct Parts {
+    uint32_t hi, lo, s_hi, s_lo;
+};
+__device__ __forceinline__ Parts split4(uint2 v) {
+    // bf16 magnitudes order as integers, infinities and NaN last
+    uint32_t amax = max(max(v.x & 0x7FFFu, (v.x >> 16) & 0x7FFFu), max(v.y & 0x7FFFu, (v.y >> 16) & 0x7FFFu));
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
+    const bool odd = amax >= 0x7F80u;
+    const int e = static_cast<int>(amax >> 7);          // biased exponent of the largest
+    const int s_hi = e > 7 ? e - 7 : 0, s_lo = s_hi > 5 ? s_hi - 5 : 0;
+    const float down = __uint_as_float(static_cast<uint32_t>(254 - s_hi) << 23);   // 2^(127 - s_hi)
+    const float up = __uint_as_float(static_cast<uint32_t>(127 + s_hi - s_lo) << 23);
+    uint32_t h0, h1, l0, l1;
+    split2(bf16_lo(v.x) * down, bf16_hi(v.x) * down, up, h0, l0);
+    split2(bf16_lo(v.y) * down, bf16_hi(v.y) * down, up, h1, l1);
+    Parts p;
+    p.hi = odd ? 0x7F7F7F7Fu : h0 | h1 << 16;
+    p.lo = odd ? 0u : l0 | l1 << 16;
+    p.s_hi = odd ? 255u : static_cast<uint32_t>(s_hi);
+    p.s_lo = odd ? 255u : static_cast<uint32_t>(s_lo);
+    return p;
+}
+// Byte offset of elements 4 lane .. 4 lane + 3 of a row in a swizzled tile, and of scale j of a row in
+// its atom.
+__device__ __forceinline__ int tile_at(int row, int lane) {
+    return row * kBK + (((lane >> 2) ^ (row & 7)) << 4) + 4 * (lane & 3);
+}
+__device__ __forceinline__ int atom_at(int row, int j) { return 16 * (row & 31) + 4 * (row >> 5) + j; }
+
 struct Plan {
     int mp;            // token rows of a tile (padded to 8 or a multiple of 16)
     int t_tiles;       // token tiles of mp rows
+    int own;           // the product's CTAs prepare their own part
     int stacked;       // hi and lo rows in one MMA of N = 2 mp
     int w_tiles;       // tiles of 128 weight rows
     int split;         // CTAs of a cluster along K
@@ -206,29 +242,15 @@ linear_few_prepare_kernel(const LinearArgs a, const Plan p, uint8_t* __restrict_
         const int64_t k = static_cast<int64_t>(j) * kBK + 4 * lane;
         uint2 v = make_uint2(0u, 0u);
         if (k < a.K) v = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.x) + t * a.K + k));
-        // bf16 magnitudes order as integers, infinities and NaN last
-        uint32_t amax = max(max(v.x & 0x7FFFu, (v.x >> 16) & 0x7FFFu), max(v.y & 0x7FFFu, (v.y >> 16) & 0x7FFFu));
-#pragma unroll
-        for (int o = 4; o > 0; o >>= 1) amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
-        const bool odd = amax >= 0x7F80u;
-        const int e = static_cast<int>(amax >> 7);          // biased exponent of the largest
-        const int s_hi = e > 7 ? e - 7 : 0, s_lo = s_hi > 5 ? s_hi - 5 : 0;
-        const float down = __uint_as_float(static_cast<uint32_t>(254 - s_hi) << 23);   // 2^(127 - s_hi)
-        const float up = __uint_as_float(static_cast<uint32_t>(127 + s_hi - s_lo) << 23);
-        uint32_t h0, h1, l0, l1;
-        split2(bf16_lo(v.x) * down, bf16_hi(v.x) * down, up, h0, l0);
-        split2(bf16_lo(v.y) * down, bf16_hi(v.y) * down, up, h1, l1);
-        const uint32_t hi = odd ? 0x7F7F7F7Fu : h0 | h1 << 16, lo = odd ? 0u : l0 | l1 << 16;
+        const Parts q = split4(v);
         uint8_t* blk = ws_b + (tt * p.nk + j) * p.b_bytes;
         const int r_lo = p.mp + r;
-        auto at = [&](int row) { return row * kBK + (((lane >> 2) ^ (row & 7)) << 4) + 4 * (lane & 3); };
-        *reinterpret_cast<uint32_t*>(blk + at(r)) = hi;
-        *reinterpret_cast<uint32_t*>(blk + at(r_lo)) = lo;
+        *reinterpret_cast<uint32_t*>(blk + tile_at(r, lane)) = q.hi;
+        *reinterpret_cast<uint32_t*>(blk + tile_at(r_lo, lane)) = q.lo;
         if ((lane & 7) == 0) {
             uint8_t* atom = blk + 2 * p.mp * kBK;
-            auto sf = [&](int row) { return 16 * (row & 31) + 4 * (row >> 5) + (lane >> 3); };
-            atom[sf(r)] = static_cast<uint8_t>(odd ? 255 : s_hi);
-            atom[p.stacked ? sf(r_lo) : kAtom + sf(r)] = static_cast<uint8_t>(odd ? 255 : s_lo);
+            atom[atom_at(r, lane >> 3)] = static_cast<uint8_t>(q.s_hi);
+            atom[p.stacked ? atom_at(r_lo, lane >> 3) : kAtom + atom_at(r, lane >> 3)] = static_cast<uint8_t>(q.s_lo);
         }
     }
 }
@@ -248,8 +270,8 @@ __device__ __noinline__ float dot_direct(const LinearArgs& a, int64_t m, int64_t
 }
 
 // ---------------------------------------------------------------- product
-// SPLIT: CTAs of a cluster along K.
-template <bool kGated, int SPLIT>
+// SPLIT: CTAs of a cluster along K.  kOwn: the CTA prepares its activations and scales itself.
+template <bool kGated, int SPLIT, bool kOwn>
 __global__ void __launch_bounds__(kThreads)
 linear_few_kernel(const __grid_constant__ CUtensorMap tmap_codes, const __grid_constant__ LinearArgs a, const Plan p,
                   const uint8_t* __restrict__ ws_b, const uint8_t* __restrict__ ws_sfa) {
@@ -265,6 +287,8 @@ linear_few_kernel(const __grid_constant__ CUtensorMap tmap_codes, const __grid_c
     const int rank = SPLIT > 1 ? static_cast<int>(ctarank()) : 0;
     const int64_t f = blockIdx.x / SPLIT;
     const int64_t tt = blockIdx.y;
+    const int64_t t0 = tt * p.mp;
+    const int mt = static_cast<int>(min(static_cast<int64_t>(p.mp), a.M - t0));   // the tile's tokens
     // this CTA's K stages [j0, j0 + n); the launch keeps SPLIT <= nk, so n >= 1
     const int j0 = rank * p.nk / SPLIT;
     const int n = (rank + 1) * p.nk / SPLIT - j0;
@@ -277,7 +301,7 @@ linear_few_kernel(const __grid_constant__ CUtensorMap tmap_codes, const __grid_c
             mbar_init(&code_empty[s], 4);   // one arrival per spreading warp
         }
         for (int s = 0; s < NS; ++s) {
-            mbar_init(&full[s], 5);   // four spreading warps and the copies of warp 4
+            mbar_init(&full[s], kOwn ? 4 : 5);   // four spreading warps and the copies of warp 4
             mbar_init(&empty[s], 1);
         }
         mbar_init(done, 1);
@@ -316,11 +340,58 @@ linear_few_kernel(const __grid_constant__ CUtensorMap tmap_codes, const __grid_c
         const int ch = tid & 3, r = tid >> 2;
         const uint32_t from = smem_u32(codes) + r * 128 + 16 * ch;
         const uint32_t to = smem_u32(smem) + r * kBK + (((2 * ch) ^ (r & 7)) << 4);
+        // kOwn: tokens warp, warp + 4, ... (at most 16) and the scales of row 32 warp + lane of a stage, one
+        // stage ahead in registers
+        uint2 xv[4];
+        uint32_t sv = 0;
+        const int kb = static_cast<int>(a.K / 32);
+        const int64_t my_row = weight_row<kGated>(a, f, 32 * warp + lane);
+        const uint8_t* my_scales = a.scales + (my_row < 0 ? 0 : my_row) * kb;
+        auto fetch = [&](int i) {
+            const int64_t k = static_cast<int64_t>(j0 + i) * kBK + 4 * lane;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int t = warp + 4 * q;
+                xv[q] = make_uint2(0u, 0u);
+                if (t < mt && k < a.K)
+                    xv[q] = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.x) + (t0 + t) * a.K + k));
+            }
+            uint32_t b[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int x = 4 * (j0 + i) + q;
+                b[q] = x < kb ? __ldg(my_scales + x) : 0x7Fu;
+            }
+            sv = b[0] | b[1] << 8 | b[2] << 16 | b[3] << 24;
+        };
+        auto prepare = [&](uint8_t* st) {   // into the stage's activation and scale parts
+            uint8_t* tile = st + kABytes;
+            uint8_t* atom = tile + 2 * p.mp * kBK;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int t = warp + 4 * q;
+                if (t < mt) {
+                    const Parts z = split4(xv[q]);
+                    *reinterpret_cast<uint32_t*>(tile + tile_at(t, lane)) = z.hi;
+                    *reinterpret_cast<uint32_t*>(tile + tile_at(p.mp + t, lane)) = z.lo;
+                    if ((lane & 7) == 0) {
+                        atom[atom_at(t, lane >> 3)] = static_cast<uint8_t>(z.s_hi);
+                        atom[atom_at(p.mp + t, lane >> 3)] = static_cast<uint8_t>(z.s_lo);
+                    }
+                }
+            }
+            *reinterpret_cast<uint32_t*>(tile + p.b_bytes + 16 * lane + 4 * warp) = sv;
+        };
+        if (kOwn) fetch(0);
         bool ok = true;
         for (int i = 0; i < n; ++i) {
             const int u = i >> 1;
-            bool got = (i & 1) || mbar_wait_spin(&code_full[u % CS], (u / CS) & 1, &s_abort);
-            if (got && i >= NS) got = mbar_wait_spin(&empty[i % NS], ((i / NS) & 1) ^ 1, &s_abort);
+            bool got = i < NS || mbar_wait_spin(&empty[i % NS], ((i / NS) & 1) ^ 1, &s_abort);
+            if (kOwn && __all_sync(0xFFFFFFFFu, got)) {
+                prepare(smem + i % NS * p.stage_bytes);
+                if (i + 1 < n) fetch(i + 1);
+            }
+            if (got && !(i & 1)) got = mbar_wait_spin(&code_full[u % CS], (u / CS) & 1, &s_abort);
             if (!__all_sync(0xFFFFFFFFu, got)) { ok = false; break; }
             const uint32_t src = from + u % CS * kCodeBytes + (i & 1) * 64, dst = to + i % NS * p.stage_bytes;
             uint4 v[4];
@@ -360,7 +431,7 @@ linear_few_kernel(const __grid_constant__ CUtensorMap tmap_codes, const __grid_c
         }
     } else if (warp == 4) {
         // ---------------- prepared activations and scales
-        if (lane == 0) {
+        if (!kOwn && lane == 0) {
             grid_wait();   // the prepare kernel's writes are complete
             bool ok = true;
             for (int i = 0; i < n; ++i) {
@@ -431,8 +502,6 @@ linear_few_kernel(const __grid_constant__ CUtensorMap tmap_codes, const __grid_c
 
     // ---------------- the finish: each CTA of the cluster takes a share of the tokens, a thread four
     // features of every kStep-th token.  What it adds to the sums is loaded while the last MMAs run.
-    const int64_t t0 = tt * p.mp;
-    const int mt = static_cast<int>(min(static_cast<int64_t>(p.mp), a.M - t0));
     constexpr int kQuads = kFeat / 4, kStep = kThreads / kQuads;
     constexpr int kBatch = SPLIT >= 3 ? 1 : 4 / SPLIT;   // tokens whose loads are in flight together
     const int c0 = rank * mt / SPLIT, c1 = (rank + 1) * mt / SPLIT;
@@ -586,6 +655,7 @@ Plan make_plan(int64_t M, int64_t K, int64_t n_out, bool gated) {
     const int per = static_cast<int>((M + tt - 1) / tt);
     p.mp = per <= 8 ? 8 : (per + 15) / 16 * 16;
     p.t_tiles = static_cast<int>((M + p.mp - 1) / p.mp);
+    p.own = p.mp <= kOwnMp;
     p.stacked = 2 * p.mp <= 128;
     p.b_bytes = 2 * p.mp * kBK + (p.stacked ? 1 : 2) * kAtom;
     p.stage_bytes = (kABytes + p.b_bytes + kAtom + 1023) / 1024 * 1024;
@@ -596,15 +666,16 @@ Plan make_plan(int64_t M, int64_t K, int64_t n_out, bool gated) {
 
 size_t linear_few_ws_bytes(int64_t M, int64_t K, int64_t n_out, bool gated) {
     const Plan p = make_plan(M, K, n_out, gated);
+    if (p.own) return 0;
     return static_cast<size_t>(p.t_tiles) * p.nk * p.b_bytes + static_cast<size_t>(p.w_tiles) * p.nk * kAtom;
 }
 
 namespace {
 
-template <bool kGated, int SPLIT>
+template <bool kGated, int SPLIT, bool kOwn>
 cudaError_t launch_product(const CUtensorMap& tmap_codes, const LinearArgs& a, const Plan& p, const uint8_t* ws_b,
                            const uint8_t* ws_sfa, cudaStream_t stream) {
-    auto kern = linear_few_kernel<kGated, SPLIT>;
+    auto kern = linear_few_kernel<kGated, SPLIT, kOwn>;
     const int part = (p.mp + 15) / 16 * 16 * kBM * 4, ring = p.stages * p.stage_bytes + p.slots * kCodeBytes;
     const int smem = (ring > part ? ring : part) + 1024;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
@@ -615,15 +686,26 @@ cudaError_t launch_product(const CUtensorMap& tmap_codes, const LinearArgs& a, c
     cfg.dynamicSmemBytes = static_cast<size_t>(smem);
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = static_cast<unsigned>(SPLIT);
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(SPLIT);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;   // after the prepare kernel
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 2;
+    cfg.numAttrs = kOwn ? 1 : 2;
     return cudaLaunchKernelEx(&cfg, kern, tmap_codes, a, p, ws_b, ws_sfa);
+}
+
+template <bool kGated, bool kOwn>
+cudaError_t launch_split(const CUtensorMap& tmap_codes, const LinearArgs& a, const Plan& p, const uint8_t* ws_b,
+                         const uint8_t* ws_sfa, cudaStream_t stream) {
+    switch (p.split) {
+        case 1: return launch_product<kGated, 1, kOwn>(tmap_codes, a, p, ws_b, ws_sfa, stream);
+        case 2: return launch_product<kGated, 2, kOwn>(tmap_codes, a, p, ws_b, ws_sfa, stream);
+        case 4: return launch_product<kGated, 4, kOwn>(tmap_codes, a, p, ws_b, ws_sfa, stream);
+        default: return launch_product<kGated, 8, kOwn>(tmap_codes, a, p, ws_b, ws_sfa, stream);
+    }
 }
 
 template <bool kGated>
@@ -652,6 +734,7 @@ cudaError_t launch_few(const LinearArgs& a, const CUtensorMap& tmap_codes, Plan 
     while (p.split < kMaxCluster && 2 * p.split <= p.nk &&
            2LL * p.split * p.w_tiles * p.t_tiles <= static_cast<int64_t>(occ) * kSms)
         p.split *= 2;
+    if (p.own) return launch_split<kGated, true>(tmap_codes, a, p, nullptr, nullptr, stream);
     uint8_t* ws_b = static_cast<uint8_t*>(ws);
     uint8_t* ws_sfa = ws_b + static_cast<size_t>(p.t_tiles) * p.nk * p.b_bytes;
     const int kb = static_cast<int>(a.K / 32);
@@ -663,12 +746,7 @@ cudaError_t launch_few(const LinearArgs& a, const CUtensorMap& tmap_codes, Plan 
     if (xg > 4LL * sm_count) xg = 4LL * sm_count;
     linear_few_prepare_kernel<kGated><<<static_cast<unsigned>(p.w_tiles + xg), kThreads, rows_smem, stream>>>(a, p, ws_b, ws_sfa);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    switch (p.split) {
-        case 1: return launch_product<kGated, 1>(tmap_codes, a, p, ws_b, ws_sfa, stream);
-        case 2: return launch_product<kGated, 2>(tmap_codes, a, p, ws_b, ws_sfa, stream);
-        case 4: return launch_product<kGated, 4>(tmap_codes, a, p, ws_b, ws_sfa, stream);
-        default: return launch_product<kGated, 8>(tmap_codes, a, p, ws_b, ws_sfa, stream);
-    }
+    return launch_split<kGated, false>(tmap_codes, a, p, ws_b, ws_sfa, stream);
 }
 
 }  // namespace
