@@ -568,13 +568,14 @@ mxfp4_status mxfp4_linear(const void* x_bf16, int64_t M, int64_t K, const uint8_
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e;
     if (linear_many(M, K)) {
-        const int nt = mx::linear_many_cols(M, n_out, act == MXFP4_ACT_SWIGLU, d->sm_count);
-        CUtensorMap tx, tw;
+        const mx::ManyPlan plan = mx::linear_many_plan(M, n_out, act == MXFP4_ACT_SWIGLU, d->sm_count);
+        CUtensorMap tx, tw, tn;
         if ((st = encode_act_map(&tx, x_bf16, K, M, 128)) != MXFP4_OK) return st;
-        if ((st = encode_act_map(&tw, ws, K, N, nt / 2)) != MXFP4_OK) return st;
-        if ((e = mx::launch_dequantize(w_codes, w_scales, N, K, ws, d->sm_count, d->status, s)) != cudaSuccess)
+        if ((st = encode_act_map(&tw, ws, K, N, plan.nt / 2)) != MXFP4_OK) return st;
+        if ((st = encode_act_map(&tn, ws, K, N, (plan.nt_narrow ? plan.nt_narrow : plan.nt) / 2)) != MXFP4_OK) return st;
+        if ((e = mx::launch_dequantize_kept(w_codes, w_scales, N, K, ws, d->sm_count, s)) != cudaSuccess)
             return cuda_fail(e);
-        e = mx::launch_linear_many(a, tx, tw, nt, d->sm_count, s);
+        e = mx::launch_linear_many(a, tx, tw, tn, plan, s);
     } else {
         CUtensorMap tc;
         if ((st = encode_rows_map(&tc, w_codes, K, N, act == MXFP4_ACT_SWIGLU ? 64 : 128)) != MXFP4_OK) return st;

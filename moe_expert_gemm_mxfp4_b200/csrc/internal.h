@@ -77,6 +77,8 @@ cudaError_t launch_quantize(const void* x, int is_f32, int64_t rows, int64_t col
 cudaError_t launch_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows,
                               int64_t cols, void* out, int sm_count, unsigned* status,
                               cudaStream_t stream);
+cudaError_t launch_dequantize_kept(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols,
+                                   void* out, int sm_count, cudaStream_t stream);
 cudaError_t launch_selftest_wait_timeout(unsigned* status, cudaStream_t stream);
 double selftest_mma_flops(int kind, int iters, int sm_count);
 cudaError_t launch_selftest_mma_rate(int kind, int iters, int sm_count, unsigned* status,
@@ -108,9 +110,14 @@ cudaError_t launch_route_scored(RouteScoredArgs a, bool bf16, cudaStream_t strea
 size_t linear_few_ws_bytes(int64_t M, int64_t K, int64_t n_out, bool gated);
 cudaError_t launch_linear_few(const LinearArgs& a, const CUtensorMap& tmap_codes, void* ws, int sm_count,
                               cudaStream_t stream);
-int linear_many_cols(int64_t M, int64_t n_out, bool gated, int sm_count);   // columns of a work tile
-cudaError_t launch_linear_many(const LinearArgs& a, const CUtensorMap& tmap_x, const CUtensorMap& tmap_w, int nt,
-                               int sm_count, cudaStream_t stream);
+// Tiling of the many-token linear layer (see linear_many.cu).
+struct ManyPlan {
+    int nt, nt_narrow, narrow_pairs;   // accumulator columns of full and narrow tiles (0: none); pairs that take the latter
+    int64_t pairs, full, m_tiles, cost;
+};
+ManyPlan linear_many_plan(int64_t M, int64_t n_out, bool gated, int sm_count);
+cudaError_t launch_linear_many(const LinearArgs& a, const CUtensorMap& tmap_x, const CUtensorMap& tmap_w,
+                               const CUtensorMap& tmap_narrow, const ManyPlan& p, cudaStream_t stream);
 TokenTiling pick_token_tiling(int64_t rows, int64_t groups);
 int64_t max_gemm_k();   // largest contraction length the grouped GEMM accepts
 

@@ -5,16 +5,23 @@
 // against 2 M N K operations), so that both operands of the product come by TMA and no
 // warp touches them: dequantizing inside the product costs one pass per token tile.
 //
-// Work tile: 256 tokens x nt output columns (nt a multiple of 32 up to 256; gated: nt / 2
-// gate and the same nt / 2 up features).  CTA r of the pair holds tokens 128 r .. 128 r + 127
+// Work tile: 256 tokens x nt accumulator columns (nt a multiple of 32 up to 256; gated: nt / 2
+// gate and the same nt / 2 up features); the columns that full tiles leave are tiles of their own
+// width, done last.  CTA r of the pair holds tokens 128 r .. 128 r + 127
 // as the MMA's A rows and half of the columns as its B rows; the leader (r = 0) issues
-// M = 256 MMAs that read both CTAs' shared memory and write 128 accumulator lanes in each.  A pair
-// thus stages 16 KB of A and nt / 2 rows of B per CTA and K stage of 64, half of the B
-// bytes of two single CTAs.
+// M = 256 MMAs that read both CTAs' shared memory and write 128 accumulator lanes in each.  Per 64
+// of K a CTA thus stages 16 KB of A and nt / 2 rows of B, half of the B bytes of two single CTAs.
+// K stages are 128 long: the issuer's and the producer's waits, once per stage, cost as much as
+// two MMAs (stages of 64 took 12% longer at nt = 160).
+//
+// What bounds it: the MMAs of a stage (4 nt cycles) where nt = 256 and the power limit; below that
+// the copies, about 47 bytes per cycle and SM from L2, so that a tile costs as 256 + nt.
 //
 // Roles in each CTA (8 warps): warp 0 producer (its own half of both tiles; completion is
 // counted on the leader's barrier), warp 1 MMA issuer (leader only), warps 4-7 epilogue (TMEM lane
 // quarters), accumulators double-buffered in TMEM (2 x 256 columns).  Every wait is bounded.
+#include <algorithm>
+
 #include "linear_epilogue.cuh"
 
 namespace mx {
@@ -24,8 +31,8 @@ namespace {
 using namespace linear;
 
 constexpr int kThreads = 256;
-constexpr int kBK = 64;                        // K per stage (128 bytes per row)
-constexpr int kXBytes = 128 * kBK * 2;         // A rows of one CTA
+constexpr int kBK = 128;                       // K per stage: two tiles of 64 (128 bytes per row)
+constexpr int kXTile = 128 * 64 * 2;           // A rows of one CTA, 64 of K
 constexpr int kMaxStages = 12;
 constexpr int kSmemLimit = 227 * 1024;
 constexpr int kBars = 2 * kMaxStages + 2 + 2 + 1;
@@ -36,7 +43,7 @@ struct Layout {
 
 __host__ __device__ inline Layout make_layout(int nt) {
     Layout L;
-    L.stage_bytes = kXBytes + nt / 2 * kBK * 2;
+    L.stage_bytes = 2 * (kXTile + nt / 2 * 64 * 2);
     const int fixed = 4 * 256 * 4 + kBars * 8 + 16 + 1024;
     L.stages = (kSmemLimit - fixed) / L.stage_bytes;
     if (L.stages > kMaxStages) L.stages = kMaxStages;
@@ -88,6 +95,34 @@ __device__ __forceinline__ void commit_pair(uint64_t* bar) {
         : "memory");
 }
 
+// The launch's tiles.  Pair p of P takes the full tiles p, p + P, ... (token tile fastest, so that the
+// pairs at work share weights), then, if it is one of the last narrow_pairs, every narrow_pairs-th
+// narrow one.
+struct Tiles {
+    int nt, nt_narrow;        // accumulator columns of a full and of a narrow tile
+    int m_tiles, full, narrow_pairs;
+};
+struct Tile {
+    int m, f, nt;
+};
+struct Walk {
+    int pair, pairs, n_full, n;
+    __device__ __forceinline__ Walk(const Tiles& t) {
+        pair = static_cast<int>(blockIdx.x >> 1);
+        pairs = static_cast<int>(gridDim.x >> 1);
+        n_full = pair < t.full ? (t.full - pair + pairs - 1) / pairs : 0;
+        const int q = pair - (pairs - t.narrow_pairs);
+        n = n_full + (t.narrow_pairs > 0 && q >= 0 && q < t.m_tiles ? (t.m_tiles - q + t.narrow_pairs - 1) / t.narrow_pairs : 0);
+    }
+    __device__ __forceinline__ Tile at(const Tiles& t, int k) const {
+        if (k < n_full) {
+            const int i = pair + k * pairs;
+            return {i % t.m_tiles, i / t.m_tiles, t.nt};
+        }
+        return {pair - (pairs - t.narrow_pairs) + (k - n_full) * t.narrow_pairs, t.full / t.m_tiles, t.nt_narrow};
+    }
+};
+
 struct Ring {
     int idx = 0;
     uint32_t ph = 0;
@@ -99,19 +134,13 @@ struct Ring {
     }
 };
 
-// 32 consecutive outputs of one token (columns n .. n + 31): z -> y.
+// 32 consecutive outputs of one token (columns n .. n + 31; the first at index at, nothing past the
+// tile's `limit` columns): z -> y.  r: their residual where they are whole vectors.
 template <bool kGated>
-__device__ __forceinline__ void finish32(const LinearArgs& a, int64_t m, int64_t n, const uint32_t* z, const uint32_t* u,
-                                         const float* bz, const float* bu, bool vec) {
-    const int64_t at = m * a.n_out + n;
+__device__ __forceinline__ void finish32(const LinearArgs& a, int64_t at, int limit, bool whole, const uint4* r,
+                                         const uint32_t* z, const uint32_t* u, const float* bz, const float* bu) {
     const uint16_t* res = static_cast<const uint16_t*>(a.residual);
     uint16_t* y = static_cast<uint16_t*>(a.y);
-    const bool whole = vec && n + 32 <= a.n_out;
-    uint4 r[4];
-    if (whole && res) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) r[i] = *reinterpret_cast<const uint4*>(res + at + 8 * i);
-    }
     float v[32];
 #pragma unroll
     for (int j = 0; j < 32; j += 4) {
@@ -147,7 +176,7 @@ __device__ __forceinline__ void finish32(const LinearArgs& a, int64_t m, int64_t
     } else {
 #pragma unroll
         for (int j = 0; j < 32; ++j) {
-            if (n + j < a.n_out) {
+            if (j < limit) {
                 float w = v[j];
                 if (res) w += __uint_as_float(static_cast<uint32_t>(res[at + j]) << 16);
                 y[at + j] = static_cast<uint16_t>(pack_bf16(w, w));
@@ -159,8 +188,9 @@ __device__ __forceinline__ void finish32(const LinearArgs& a, int64_t m, int64_t
 template <bool kGated>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 linear_many_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ CUtensorMap tmap_w,
-                   const LinearArgs a, int nt, int m_tiles, int tiles) {
-    const Layout Ly = make_layout(nt);
+                   const __grid_constant__ CUtensorMap tmap_narrow, const __grid_constant__ LinearArgs a,
+                   const Tiles tiles) {
+    const Layout Ly = make_layout(tiles.nt);
     const int S = Ly.stages;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -176,9 +206,9 @@ linear_many_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
     volatile int* s_never = reinterpret_cast<volatile int*>(smem + Ly.misc_off + 8);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t rank = cta_rank();
-    const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+    const Walk walk(tiles);
     const int nk = static_cast<int>((a.K + kBK - 1) / kBK);
-    const int cols = kGated ? nt / 2 : nt;   // output columns per tile
+    const int full_cols = kGated ? tiles.nt / 2 : tiles.nt;   // output columns of a full tile
 
     if (tid == 0) {
         for (int s = 0; s < S; ++s) {
@@ -195,6 +225,7 @@ linear_many_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
         fence_mbar_init();
         prefetch_tmap(&tmap_x);
         prefetch_tmap(&tmap_w);
+        prefetch_tmap(&tmap_narrow);
     }
     if (warp == 2) {
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(s_tmem)),
@@ -211,22 +242,26 @@ linear_many_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
     if (warp == 0) {
         // ---------------- producer
         if (lane == 0) {
+            asm volatile("griddepcontrol.wait;" ::: "memory");   // the bf16 weights are complete
             const uint32_t full0 = on_leader(full);
-            const int half = nt / 2;
             Ring c;
             int issued = 0;
             bool ok = true;
-            for (int t = pair; t < tiles && ok; t += pairs) {
-                const int m0 = t % m_tiles * 256 + static_cast<int>(rank) * 128;
-                const int f = t / m_tiles;
-                const int w0 = kGated ? static_cast<int>(rank * a.n_out) + f * half : f * nt + static_cast<int>(rank) * half;
+            for (int k = 0; k < walk.n && ok; ++k) {
+                const Tile t = walk.at(tiles, k);
+                const int m0 = t.m * 256 + static_cast<int>(rank) * 128, half = t.nt / 2;
+                const int w0 = t.f * full_cols + (kGated ? static_cast<int>(rank * a.n_out) : static_cast<int>(rank) * half);
+                const CUtensorMap* tw = k < walk.n_full ? &tmap_w : &tmap_narrow;
+                const uint32_t bytes = 2u * 2u * (kXTile + half * 128);   // both CTAs, two tiles of 64
                 for (int i = 0; i < nk; ++i) {
                     if (!mbar_wait(&empty[c.idx], c.ph ^ 1, s_abort)) { ok = false; break; }
                     uint8_t* dst = smem + c.idx * Ly.stage_bytes;
                     const uint32_t bar = full0 + 8 * c.idx;
-                    if (rank == 0) mbar_arrive_expect_tx(&full[c.idx], 2u * Ly.stage_bytes);
+                    if (rank == 0) mbar_arrive_expect_tx(&full[c.idx], bytes);
                     load_pair(dst, &tmap_x, bar, i * kBK, m0);
-                    load_pair(dst + kXBytes, &tmap_w, bar, i * kBK, w0);
+                    load_pair(dst + kXTile, &tmap_x, bar, i * kBK + 64, m0);
+                    load_pair(dst + 2 * kXTile, tw, bar, i * kBK, w0);
+                    load_pair(dst + 2 * kXTile + half * 128, tw, bar, i * kBK + 64, w0);
                     c.next(S);
                     ++issued;
                 }
@@ -252,12 +287,11 @@ linear_many_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
     } else if (warp == 1) {
         // ---------------- MMA issuer of the pair
         if (lane == 0 && rank == 0) {
-            const uint32_t idesc = idesc_bf16_f32(256, nt);
             Ring c;
-            int lt = 0;
             bool ok = true;
-            for (int t = pair; t < tiles && ok; t += pairs, ++lt) {
-                const int b = lt & 1;
+            for (int lt = 0; lt < walk.n && ok; ++lt) {
+                const int nt = walk.at(tiles, lt).nt, b = lt & 1;
+                const uint32_t idesc = idesc_bf16_f32(256, nt);
                 if (!mbar_wait(&accempty[b], ((lt >> 1) & 1) ^ 1, s_abort)) { ok = false; break; }
                 tc_fence_after();
                 const uint32_t d = tmem + b * 256;
@@ -265,10 +299,14 @@ linear_many_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
                     if (!mbar_wait(&full[c.idx], c.ph, s_abort)) { ok = false; break; }
                     tc_fence_after();
                     const uint32_t xa = smem_u32(smem + c.idx * Ly.stage_bytes);
-                    const uint64_t da = sw128_desc(xa), db = sw128_desc(xa + kXBytes);
+                    const uint64_t da = sw128_desc(xa), db = sw128_desc(xa + 2 * kXTile);
+                    const uint64_t next_b = static_cast<uint64_t>(nt / 2 * 128) >> 4;
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)   // 32 bytes of K per step
-                        mma_pair(d, da + 2 * j, db + 2 * j, idesc, (i | j) != 0 ? 1u : 0u);
+                    for (int j = 0; j < 8; ++j) {   // 32 bytes of K per step, four steps per tile
+                        if (j < 4 || i * kBK + 64 < a.K)
+                            mma_pair(d, da + (j & 3) * 2 + (j >> 2) * (kXTile >> 4), db + (j & 3) * 2 + (j >> 2) * next_b, idesc,
+                                     (i | j) != 0 ? 1u : 0u);
+                    }
                     commit_pair(&empty[c.idx]);
                     c.next(S);
                 }
@@ -289,30 +327,51 @@ linear_many_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
         float* s_bias = reinterpret_cast<float*>(smem + Ly.bias_off) + q * 256;
         const uint32_t accempty0 = on_leader(accempty);
         const bool vec = a.n_out % 8 == 0;
-        int lt = 0;
+        const uint16_t* res = static_cast<const uint16_t*>(a.residual);
         bool ok = true;
-        for (int t = pair; t < tiles && ok; t += pairs, ++lt) {
-            const int64_t m = static_cast<int64_t>(t % m_tiles) * 256 + rank * 128 + q * 32 + lane;
-            const int64_t n0 = static_cast<int64_t>(t / m_tiles) * cols;
-            const int b = lt & 1;
+        for (int lt = 0; lt < walk.n && ok; ++lt) {
+            const Tile t = walk.at(tiles, lt);
+            const int nt = t.nt, cols = kGated ? nt / 2 : nt, b = lt & 1;
+            const int64_t m = static_cast<int64_t>(t.m) * 256 + rank * 128 + q * 32 + lane;
+            const int64_t n0 = static_cast<int64_t>(t.f) * full_cols;
             __syncwarp();
             for (int j = lane; j < nt; j += 32) {
                 const int64_t n = n0 + (kGated && j >= cols ? j - cols : j);
                 s_bias[j] = n < a.n_out ? bias_at(a, kGated && j >= cols ? n + a.n_out : n) : 0.f;
             }
             __syncwarp();
+            // the residual of the next 32 columns is on its way while these are finished
+            uint4 r[2][4];
+            const int64_t at0 = m * a.n_out + n0;
+            const int limit = static_cast<int>(min(static_cast<int64_t>(cols), a.n_out - n0));
+            auto load_res = [&](int c, uint4* to) {
+                if (res && vec && m < a.M && c + 32 <= limit) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) to[i] = *reinterpret_cast<const uint4*>(res + at0 + c + 8 * i);
+                }
+            };
+            load_res(0, r[0]);
             if (!__all_sync(0xFFFFFFFFu, mbar_wait(&accfull[b], (lt >> 1) & 1, s_abort))) { ok = false; break; }
             tc_fence_after();
             const uint32_t base = tmem + (static_cast<uint32_t>(q * 32) << 16) + b * 256;
-#pragma unroll 1
-            for (int c = 0; c < cols; c += 32) {
-                if (n0 + c >= a.n_out) break;
+            auto finish = [&](int c, const uint4* rr) {
                 __syncwarp();
                 uint32_t z[32], u[32];
                 tmem_ld_x32(base + c, z);
                 if (kGated) tmem_ld_x32(base + cols + c, u);
                 tmem_wait_ld();
-                if (m < a.M) finish32<kGated>(a, m, n0 + c, z, u, s_bias + c, s_bias + (kGated ? cols : 0) + c, vec);
+                if (m < a.M)
+                    finish32<kGated>(a, at0 + c, limit - c, vec && c + 32 <= limit, rr, z, u, s_bias + c,
+                                     s_bias + (kGated ? cols : 0) + c);
+            };
+#pragma unroll 1
+            for (int c = 0; c < limit; c += 64) {
+                load_res(c + 32, r[1]);
+                finish(c, r[0]);
+                if (c + 32 < limit) {
+                    load_res(c + 64, r[0]);
+                    finish(c + 32, r[1]);
+                }
             }
             tc_fence_before();
             __syncwarp();
@@ -335,25 +394,52 @@ linear_many_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
 
 }  // namespace
 
-int linear_many_cols(int64_t M, int64_t n_out, bool gated, int sm_count) {
-    (void)M, (void)n_out, (void)gated, (void)sm_count;
-    return 256;
+// The tiling: of the widths of a full tile, and of the ways to deal the narrow tiles out (to all pairs, or
+// to those with one full tile less), the one whose longest pair is shortest, a tile counting as
+// 256 + nt.  (2048 x 7680 x 2880, by nt: 256 96 us, 192 86, 160 79, 128 105.)
+ManyPlan linear_many_plan(int64_t M, int64_t n_out, bool gated, int sm_count) {
+    const int64_t m_tiles = (M + 255) / 256;
+    ManyPlan best{};
+    for (int nt = 256; nt >= 96; nt -= 32) {
+        const int cols = gated ? nt / 2 : nt, unit = gated ? 16 : 32;
+        const int64_t full = m_tiles * (n_out / cols);
+        const int rem = static_cast<int>(n_out % cols);
+        const int narrow = rem == 0 ? 0 : std::max(64, (rem + unit - 1) / unit * 32);
+        const int64_t tiles = full + (narrow ? m_tiles : 0);
+        const int64_t pairs = std::min<int64_t>(sm_count / 2, tiles);
+        const int64_t more = full % pairs, light = pairs - more;   // pairs with one full tile more, and the others
+        for (int64_t np : {light, pairs}) {
+            // longest: a pair with `more` full tiles that takes narrow ones too (np == pairs), or a light one
+            const int64_t each = narrow ? (m_tiles + np - 1) / np : 0, base = full / pairs;
+            const int64_t heavy = (base + (more > 0)) * (256 + nt) + (np == pairs ? each * (256 + narrow) : 0);
+            const int64_t cost = std::max(heavy, base * (256 + nt) + each * (256 + narrow));
+            if (best.nt == 0 || cost < best.cost) best = {nt, narrow, static_cast<int>(narrow ? np : 0), pairs, full, m_tiles, cost};
+        }
+    }
+    return best;
 }
 
-cudaError_t launch_linear_many(const LinearArgs& a, const CUtensorMap& tmap_x, const CUtensorMap& tmap_w, int nt,
-                               int sm_count, cudaStream_t stream) {
+cudaError_t launch_linear_many(const LinearArgs& a, const CUtensorMap& tmap_x, const CUtensorMap& tmap_w,
+                               const CUtensorMap& tmap_narrow, const ManyPlan& p, cudaStream_t stream) {
     const bool gated = a.act == MXFP4_ACT_SWIGLU;
-    const int cols = gated ? nt / 2 : nt;
-    const int64_t m_tiles = (a.M + 255) / 256, tiles = m_tiles * ((a.n_out + cols - 1) / cols);
-    if (tiles >= (int64_t{1} << 31)) return cudaErrorInvalidValue;
-    const int64_t pairs = sm_count / 2 < tiles ? sm_count / 2 : tiles;
-    const Layout L = make_layout(nt);
+    if (p.full + p.m_tiles >= (int64_t{1} << 31)) return cudaErrorInvalidValue;
+    const Layout L = make_layout(p.nt);
     auto kern = gated ? linear_many_kernel<true> : linear_many_kernel<false>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L.total);
     if (e != cudaSuccess) return e;
-    kern<<<static_cast<unsigned>(2 * pairs), kThreads, L.total, stream>>>(tmap_x, tmap_w, a, nt, static_cast<int>(m_tiles),
-                                                                         static_cast<int>(tiles));
-    return cudaGetLastError();
+    // programmatic dependent launch: the set-up runs while the weights are still being dequantized
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(2 * p.pairs), 1, 1);
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.dynamicSmemBytes = static_cast<size_t>(L.total);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const Tiles t = {p.nt, p.nt_narrow, static_cast<int>(p.m_tiles), static_cast<int>(p.full), p.narrow_pairs};
+    return cudaLaunchKernelEx(&cfg, kern, tmap_x, tmap_w, tmap_narrow, a, t);
 }
 
 }  // namespace mx

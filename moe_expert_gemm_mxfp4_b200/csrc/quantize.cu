@@ -370,12 +370,16 @@ quantize_f32_kernel(const uint8_t* __restrict__ x, int64_t n_blocks, uint16_t* _
 // 32j + l of the unit (block 8j + l/4, whose scale byte lane 8j + l/4 loaded and a
 // shuffle hands over) and stores output vector 32j + l: every warp access is a
 // contiguous 128-byte (codes) or 512-byte (output) run.
+// kKeep: for a kernel that follows at once and reads the output from L2; plain stores, and its launch
+// may begin (programmatic dependent launch).
 constexpr int kDqThreads = 256;
 constexpr int kDqUnits = 2;
 
+template <bool kKeep>
 __global__ void __launch_bounds__(kDqThreads, 8)
 dequantize_kernel(const uint32_t* __restrict__ codes, const uint8_t* __restrict__ scales,
                   int64_t n_blocks, uint4* __restrict__ out) {
+    if (kKeep) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int lane = threadIdx.x & 31;
     const int64_t w0 = (static_cast<int64_t>(blockIdx.x) * kDqThreads + threadIdx.x) >> 5;
     const int64_t nw = (static_cast<int64_t>(gridDim.x) * kDqThreads) >> 5;
@@ -399,7 +403,11 @@ dequantize_kernel(const uint32_t* __restrict__ codes, const uint8_t* __restrict_
             for (int j = 0; j < 4; ++j) {
                 const uint32_t S = __shfl_sync(0xFFFFFFFFu, sb[k], 8 * j + (lane >> 2));
                 const int64_t blk = uk * 32 + 8 * j + (lane >> 2);
-                if (uk < n_units && blk < n_blocks) __stcs(out + uk * 128 + 32 * j + lane, dequant8_alu(cw[k][j], S));
+                if (uk < n_units && blk < n_blocks) {
+                    const uint4 v = dequant8_alu(cw[k][j], S);
+                    if (kKeep) out[uk * 128 + 32 * j + lane] = v;
+                    else __stcs(out + uk * 128 + 32 * j + lane, v);
+                }
             }
         }
     }
@@ -444,17 +452,27 @@ cudaError_t launch_quantize(const void* x, int is_f32, int64_t rows, int64_t col
     return cudaGetLastError();
 }
 
+static unsigned dequantize_grid(int64_t rows, int64_t cols, int sm_count) {
+    const int64_t n_units = (rows * (cols / 32) + 31) / 32;
+    int64_t g = (n_units + kDqUnits * (kDqThreads / 32) - 1) / (kDqUnits * (kDqThreads / 32));
+    const int64_t cap = static_cast<int64_t>(sm_count) * 16;   // two waves of 8 CTAs per SM
+    if (g > cap) g = cap;
+    return static_cast<unsigned>(g < 1 ? 1 : g);
+}
+
 cudaError_t launch_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows,
                               int64_t cols, void* out, int sm_count, unsigned* status,
                               cudaStream_t stream) {
     (void)status;   // no waits in this kernel
-    const int64_t n_blocks = rows * (cols / 32);
-    const int64_t n_units = (n_blocks + 31) / 32;
-    int64_t g = (n_units + kDqUnits * (kDqThreads / 32) - 1) / (kDqUnits * (kDqThreads / 32));
-    const int64_t cap = static_cast<int64_t>(sm_count) * 16;   // two waves of 8 CTAs per SM
-    if (g > cap) g = cap;
-    dequantize_kernel<<<static_cast<unsigned>(g < 1 ? 1 : g), kDqThreads, 0, stream>>>(
-        reinterpret_cast<const uint32_t*>(codes), scales, n_blocks, reinterpret_cast<uint4*>(out));
+    dequantize_kernel<false><<<dequantize_grid(rows, cols, sm_count), kDqThreads, 0, stream>>>(
+        reinterpret_cast<const uint32_t*>(codes), scales, rows * (cols / 32), reinterpret_cast<uint4*>(out));
+    return cudaGetLastError();
+}
+
+cudaError_t launch_dequantize_kept(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols,
+                                   void* out, int sm_count, cudaStream_t stream) {
+    dequantize_kernel<true><<<dequantize_grid(rows, cols, sm_count), kDqThreads, 0, stream>>>(
+        reinterpret_cast<const uint32_t*>(codes), scales, rows * (cols / 32), reinterpret_cast<uint4*>(out));
     return cudaGetLastError();
 }
 
