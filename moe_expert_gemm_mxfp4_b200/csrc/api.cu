@@ -518,15 +518,12 @@ mxfp4_status mxfp4_gemm(const void* x_bf16, int64_t M, int64_t K, const uint8_t*
     return e == cudaSuccess ? MXFP4_OK : cuda_fail(e);
 }
 
-// Whether a linear layer takes the many-token engine (weights dequantized once).  The other
-// keeps 128 rows of block scales in shared memory, which bounds K.
-static bool linear_many(int64_t M, int64_t K) { return M > 512 || K > 8192; }
-
 size_t mxfp4_linear_workspace_size(int64_t M, int64_t K, int64_t N, mxfp4_act act) {
     if (M <= 0 || K <= 0 || N <= 0) return 0;
-    if (linear_many(M, K)) return align_up(static_cast<size_t>(N) * K * 2, 256);   // W in bf16
     const bool gated = act == MXFP4_ACT_SWIGLU;
-    return align_up(mx::linear_few_ws_bytes(M, K, gated ? N / 2 : N, gated), 256);
+    const int64_t n_out = gated ? N / 2 : N;
+    if (mx::linear_is_few(M, K, n_out, gated)) return align_up(mx::linear_few_ws_bytes(M, K, n_out, gated), 256);
+    return align_up(static_cast<size_t>(N) * K * 2, 256);   // W in bf16
 }
 
 mxfp4_status mxfp4_linear(const void* x_bf16, int64_t M, int64_t K, const uint8_t* w_codes,
@@ -567,7 +564,7 @@ mxfp4_status mxfp4_linear(const void* x_bf16, int64_t M, int64_t K, const uint8_
     a.status = d->status;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e;
-    if (linear_many(M, K)) {
+    if (!mx::linear_is_few(M, K, n_out, act == MXFP4_ACT_SWIGLU)) {
         const mx::ManyPlan plan = mx::linear_many_plan(M, n_out, act == MXFP4_ACT_SWIGLU, d->sm_count);
         CUtensorMap tx, tw, tn;
         if ((st = encode_act_map(&tx, x_bf16, K, M, 128)) != MXFP4_OK) return st;

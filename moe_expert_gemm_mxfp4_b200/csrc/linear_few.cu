@@ -29,6 +29,8 @@
 // hi and lo rows lie next to each other in one MMA of N = 2 Mp columns while that fits the 128
 // rows of a scale atom (an MMA of N <= 64 costs the same whatever its N), else they are
 // two MMAs of N = Mp into the same accumulator.
+#include <atomic>
+
 #include "linear_epilogue.cuh"
 
 namespace mx {
@@ -160,7 +162,6 @@ struct Plan {
     int own;           // the product's CTAs prepare their own part
     int stacked;       // hi and lo rows in one MMA of N = 2 mp
     int w_tiles;       // tiles of 128 weight rows
-    int split;         // CTAs of a cluster along K
     int nk;            // K stages
     int stages;        // ring of stages (containers, activations, scales)
     int slots;         // ring of packed codes
@@ -664,6 +665,15 @@ Plan make_plan(int64_t M, int64_t K, int64_t n_out, bool gated) {
 
 }  // namespace
 
+// Few tokens as long as one round of CTAs holds them and three token tiles do: beyond, every round
+// streams the weights again, and dequantizing them once is less.  (2880 x 2880: 384 tokens 17 us here, 21 there,
+// 512 23 and 21; 5760 x 2880 gated: 384 24 and 27, 512 44 and 27; 11520 x 2880: 128 23 and 31, 192 38
+// and 32.)  The prepare kernel keeps 128 rows of block scales in shared memory, which bounds K.
+bool linear_is_few(int64_t M, int64_t K, int64_t n_out, bool gated) {
+    const int64_t t = (M + kMaxMp - 1) / kMaxMp, f = gated ? 64 : kBM, w = (n_out + f - 1) / f;
+    return K <= 8192 && (t == 1 || (t <= 3 && t * w <= kSms));
+}
+
 size_t linear_few_ws_bytes(int64_t M, int64_t K, int64_t n_out, bool gated) {
     const Plan p = make_plan(M, K, n_out, gated);
     if (p.own) return 0;
@@ -672,9 +682,11 @@ size_t linear_few_ws_bytes(int64_t M, int64_t K, int64_t n_out, bool gated) {
 
 namespace {
 
+// The product's launch with clusters of SPLIT CTAs; with `launch` false only how many such clusters
+// the GPU holds at once.
 template <bool kGated, int SPLIT, bool kOwn>
-cudaError_t launch_product(const CUtensorMap& tmap_codes, const LinearArgs& a, const Plan& p, const uint8_t* ws_b,
-                           const uint8_t* ws_sfa, cudaStream_t stream) {
+cudaError_t product(const CUtensorMap& tmap_codes, const LinearArgs& a, const Plan& p, const uint8_t* ws_b,
+                    const uint8_t* ws_sfa, cudaStream_t stream, bool launch, int* clusters) {
     auto kern = linear_few_kernel<kGated, SPLIT, kOwn>;
     const int part = (p.mp + 15) / 16 * 16 * kBM * 4, ring = p.stages * p.stage_bytes + p.slots * kCodeBytes;
     const int smem = (ring > part ? ring : part) + 1024;
@@ -694,18 +706,46 @@ cudaError_t launch_product(const CUtensorMap& tmap_codes, const LinearArgs& a, c
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = kOwn ? 1 : 2;
-    return cudaLaunchKernelEx(&cfg, kern, tmap_codes, a, p, ws_b, ws_sfa);
+    if (launch) return cudaLaunchKernelEx(&cfg, kern, tmap_codes, a, p, ws_b, ws_sfa);
+    // what a device of this kind holds does not change: asked once per kernel and tile size
+    static std::atomic<int> known[kMaxMp / 8 + 1];
+    std::atomic<int>& k = known[p.mp / 8];
+    if ((*clusters = k.load(std::memory_order_relaxed)) > 0) return cudaSuccess;
+    if (cudaOccupancyMaxActiveClusters(clusters, kern, &cfg) != cudaSuccess) {
+        (void)cudaGetLastError();   // clear a refusal: no such cluster fits
+        *clusters = 0;
+    }
+    k.store(*clusters, std::memory_order_relaxed);
+    return cudaSuccess;
 }
 
 template <bool kGated, bool kOwn>
-cudaError_t launch_split(const CUtensorMap& tmap_codes, const LinearArgs& a, const Plan& p, const uint8_t* ws_b,
-                         const uint8_t* ws_sfa, cudaStream_t stream) {
-    switch (p.split) {
-        case 1: return launch_product<kGated, 1, kOwn>(tmap_codes, a, p, ws_b, ws_sfa, stream);
-        case 2: return launch_product<kGated, 2, kOwn>(tmap_codes, a, p, ws_b, ws_sfa, stream);
-        case 4: return launch_product<kGated, 4, kOwn>(tmap_codes, a, p, ws_b, ws_sfa, stream);
-        default: return launch_product<kGated, 8, kOwn>(tmap_codes, a, p, ws_b, ws_sfa, stream);
+cudaError_t product_of(int split, const CUtensorMap& tmap_codes, const LinearArgs& a, const Plan& p, const uint8_t* ws_b,
+                       const uint8_t* ws_sfa, cudaStream_t stream, bool launch, int* clusters) {
+    switch (split) {
+        case 1: return product<kGated, 1, kOwn>(tmap_codes, a, p, ws_b, ws_sfa, stream, launch, clusters);
+        case 2: return product<kGated, 2, kOwn>(tmap_codes, a, p, ws_b, ws_sfa, stream, launch, clusters);
+        case 4: return product<kGated, 4, kOwn>(tmap_codes, a, p, ws_b, ws_sfa, stream, launch, clusters);
+        default: return product<kGated, 8, kOwn>(tmap_codes, a, p, ws_b, ws_sfa, stream, launch, clusters);
     }
+}
+
+// K split over the largest cluster of which the GPU holds all at once (a second round costs more than
+// the split saves: 64 x 2880 x 5760 gated took 21 us with 45 clusters of 3 in two rounds, 15 with
+// clusters of 2 in one).
+template <bool kGated, bool kOwn>
+cudaError_t launch_split(const CUtensorMap& tmap_codes, const LinearArgs& a, Plan p, const uint8_t* ws_b,
+                         const uint8_t* ws_sfa, cudaStream_t stream) {
+    const int64_t tiles = static_cast<int64_t>(p.w_tiles) * p.t_tiles;
+    int split = kMaxCluster;
+    for (; split > 1; split /= 2) {
+        int clusters = 0;
+        if (split > p.nk || tiles * split > 2LL * kSms) continue;   // two CTAs per SM at most
+        cudaError_t e = product_of<kGated, kOwn>(split, tmap_codes, a, p, ws_b, ws_sfa, stream, false, &clusters);
+        if (e != cudaSuccess) return e;
+        if (tiles <= clusters) break;
+    }
+    return product_of<kGated, kOwn>(split, tmap_codes, a, p, ws_b, ws_sfa, stream, true, nullptr);
 }
 
 template <bool kGated>
@@ -723,17 +763,8 @@ cudaError_t launch_few(const LinearArgs& a, const CUtensorMap& tmap_codes, Plan 
         while (p.stages < kMaxStages && room - p.slots * kCodeBytes >= (p.stages + 1) * p.stage_bytes) ++p.stages;
         return true;
     };
-    int occ = 2;
-    if (!fit(kSmemSm / 2 - fixed, 3) && !fit(kSmemSm / 2 - fixed, 2)) {
-        occ = 1;
-        if (!fit(kSmemSm - fixed, 3)) return cudaErrorInvalidConfiguration;
-    }
-    // K split over a cluster while the CTAs fit the SMs at once (a cluster of 3 would need SMs
-    // in threes: 135 CTAs of one per SM then take two rounds, 21 us against 15 at 64 tokens)
-    p.split = 1;
-    while (p.split < kMaxCluster && 2 * p.split <= p.nk &&
-           2LL * p.split * p.w_tiles * p.t_tiles <= static_cast<int64_t>(occ) * kSms)
-        p.split *= 2;
+    if (!fit(kSmemSm / 2 - fixed, 3) && !fit(kSmemSm / 2 - fixed, 2) && !fit(kSmemSm - fixed, 3))
+        return cudaErrorInvalidConfiguration;
     if (p.own) return launch_split<kGated, true>(tmap_codes, a, p, nullptr, nullptr, stream);
     uint8_t* ws_b = static_cast<uint8_t*>(ws);
     uint8_t* ws_sfa = ws_b + static_cast<size_t>(p.t_tiles) * p.nk * p.b_bytes;
