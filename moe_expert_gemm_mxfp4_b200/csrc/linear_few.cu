@@ -19,10 +19,11 @@
 //   linear_few          one CTA per (128 weight rows, K range, token tile).
 // Up to 16 tokens the spreading warps prepare their CTA's own part instead, and there is one
 // launch: every CTA of a K range then splits the same activations, a few per lane.
-// Roles (8 warps): warp 7 streams packed codes (TMA, 128 bytes per row) into a ring of their own;
-// warps 0-3 spread them over the 16-element containers that the tensor core takes (8
-// bytes of codes, 8 of padding), three instructions per 16 bytes; warp 4 bulk-copies
-// the prepared tiles; warp 5 issues scale copies and MMAs.  The CTAs of a cluster split K and sum
+// Roles (12 warps, one CTA per SM): warp 11 streams packed codes (TMA, 128 bytes per row) into a ring of
+// their own; warps 0-7 spread them over the 16-element containers that the tensor core takes (8
+// bytes of codes, 8 of padding), three instructions per 16 bytes; warp 8 bulk-copies
+// the prepared tiles; warp 9 issues scale copies and MMAs.  A stage is 256 of K (two tiles of
+// 128 containers): the waits and fences, once per stage, cost as much as its MMAs.  The CTAs of a cluster split K and sum
 // their partial results through distributed shared memory in rank order (the same on every
 // run); each finishes a share of the tokens.
 //
@@ -39,17 +40,20 @@ namespace {
 
 using namespace linear;
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 384;
+constexpr int kSpreadWarps = 8;
+constexpr int kPrepareThreads = 256;
 constexpr int kBM = 128;             // weight rows per tile
-constexpr int kBK = 128;             // K per stage: 128 one-byte containers per row
-constexpr int kABytes = kBM * kBK;
+constexpr int kRow = 128;            // bytes of a row of a tile: 128 one-byte containers, half a stage of K
+constexpr int kATile = kBM * kRow;
 constexpr int kAtom = 512;           // scale atom: 128 rows x 4 scales
-constexpr int kMaxMp = 128;          // tokens per tile
-constexpr int kOwnMp = 16;           // largest token tile that is prepared where it is used
-constexpr int kMaxStages = 4;
-constexpr int kCodeBytes = kBM * 128;   // a code slot: 128 bytes (two stages) of each row
-constexpr int kMaxSlots = 4;
-constexpr int kSmemSm = 228 * 1024;  // per SM, 1 KB of it taken by each resident CTA
+constexpr int kMaxMp = 112;          // tokens per tile: two stages and two code slots still fit
+constexpr int kOwnMp = 16;           // largest token tile that is prepared where it is used,
+constexpr int kOwnStages = 3;        // and the stages of a CTA it is loaded ahead for
+constexpr int kMaxStages = 3;
+constexpr int kCodeBytes = kBM * 128;   // a code slot: a stage's 128 bytes of each row
+constexpr int kMaxSlots = 6;
+constexpr int kSmemLimit = 227 * 1024;
 constexpr int kSms = 148;            // what the launch geometry aims at
 constexpr int kMaxCluster = 8;
 constexpr uint32_t kTmemCols = 256, kSfCol = 128;   // D [0, 128), scale sets of 16 columns behind it
@@ -152,7 +156,7 @@ __device__ __forceinline__ Parts split4(uint2 v) {
 // Byte offset of elements 4 lane .. 4 lane + 3 of a row in a swizzled tile, and of scale j of a row in
 // its atom.
 __device__ __forceinline__ int tile_at(int row, int lane) {
-    return row * kBK + (((lane >> 2) ^ (row & 7)) << 4) + 4 * (lane & 3);
+    return row * kRow + (((lane >> 2) ^ (row & 7)) << 4) + 4 * (lane & 3);
 }
 __device__ __forceinline__ int atom_at(int row, int j) { return 16 * (row & 31) + 4 * (row >> 5) + j; }
 
@@ -163,10 +167,11 @@ struct Plan {
     int stacked;       // hi and lo rows in one MMA of N = 2 mp
     int w_tiles;       // tiles of 128 weight rows
     int nk;            // K stages
+    int sfb_bytes;     // scale atoms of half a stage's activations
+    int b_bytes;       // prepared bytes per token tile and stage: both halves' hi and lo rows, then their scale atoms
+    int stage_bytes;
     int stages;        // ring of stages (containers, activations, scales)
     int slots;         // ring of packed codes
-    int b_bytes;       // prepared bytes per token tile and stage: hi and lo rows, scale atoms
-    int stage_bytes;
 };
 
 // First weight row of a tile's row r, or -1 past the end.  Gated tiles hold 64 gate rows and
@@ -182,16 +187,16 @@ __device__ __forceinline__ int64_t weight_row(const LinearArgs& a, int64_t f, in
 }
 
 // ---------------------------------------------------------------- prepare
-// The first w_tiles CTAs lay the weights' scales out: per tile and stage an atom of 512
-// bytes, scale j of row r at byte 16 (r % 32) + 4 (r / 32) + j.  The others take (token, stage)
-// items, one per warp: 4 elements per lane, 8 lanes to a block.
+// The first w_tiles CTAs lay the weights' scales out: per tile and half stage an atom of 512
+// bytes, scale j of row r at byte 16 (r % 32) + 4 (r / 32) + j.  The others take (token, half
+// stage) items, one per warp: 4 elements per lane, 8 lanes to a block.
 template <bool kGated>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kPrepareThreads)
 linear_few_prepare_kernel(const LinearArgs a, const Plan p, uint8_t* __restrict__ ws_b, uint8_t* __restrict__ ws_sfa) {
     grid_launch_dependents();
     extern __shared__ __align__(16) uint8_t s_rows[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int kb = static_cast<int>(a.K / 32);
+    const int kb = static_cast<int>(a.K / 32), halves = (kb + 3) / 4;
     if (static_cast<int>(blockIdx.x) < p.w_tiles) {
         const int64_t f = blockIdx.x;
         // the tile's scales: one run of rows (gated: one of gate, one of up rows)
@@ -206,13 +211,13 @@ linear_few_prepare_kernel(const LinearArgs a, const Plan p, uint8_t* __restrict_
             shift[h] = static_cast<int>(reinterpret_cast<uintptr_t>(src) & 15);
             uint8_t* dst = s_rows + h * (64 * kb + 32) / 16 * 16 + shift[h];
             const int head = min(len, (16 - shift[h]) & 15), body = (len - head) / 16;
-            for (int i = tid; i < body; i += kThreads)
+            for (int i = tid; i < body; i += kPrepareThreads)
                 reinterpret_cast<uint4*>(dst + head)[i] = __ldg(reinterpret_cast<const uint4*>(src + head) + i);
-            for (int i = tid; i < head; i += kThreads) dst[i] = src[i];
-            for (int i = head + 16 * body + tid; i < len; i += kThreads) dst[i] = src[i];
+            for (int i = tid; i < head; i += kPrepareThreads) dst[i] = src[i];
+            for (int i = head + 16 * body + tid; i < len; i += kPrepareThreads) dst[i] = src[i];
         }
         __syncthreads();
-        for (int j = warp; j < p.nk; j += kThreads / 32) {
+        for (int j = warp; j < halves; j += kPrepareThreads / 32) {
             uint32_t w[4];
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
@@ -229,27 +234,28 @@ linear_few_prepare_kernel(const LinearArgs a, const Plan p, uint8_t* __restrict_
                     }
                 }
             }
-            reinterpret_cast<uint4*>(ws_sfa + (f * p.nk + j) * kAtom)[lane] = make_uint4(w[0], w[1], w[2], w[3]);
+            reinterpret_cast<uint4*>(ws_sfa + (f * 2 * p.nk + j) * kAtom)[lane] = make_uint4(w[0], w[1], w[2], w[3]);
         }
         return;
     }
-    const int64_t items = a.M * p.nk;
-    const int64_t step = static_cast<int64_t>(gridDim.x - p.w_tiles) * (kThreads / 32);
-    for (int64_t it = static_cast<int64_t>(blockIdx.x - p.w_tiles) * (kThreads / 32) + warp; it < items; it += step) {
-        const int64_t t = it / p.nk;
-        const int j = static_cast<int>(it - t * p.nk);
+    const int64_t items = a.M * halves;
+    const int64_t step = static_cast<int64_t>(gridDim.x - p.w_tiles) * (kPrepareThreads / 32);
+    for (int64_t it = static_cast<int64_t>(blockIdx.x - p.w_tiles) * (kPrepareThreads / 32) + warp; it < items; it += step) {
+        const int64_t t = it / halves;
+        const int j = static_cast<int>(it - t * halves);
         const int64_t tt = t / p.mp;
         const int r = static_cast<int>(t - tt * p.mp);
-        const int64_t k = static_cast<int64_t>(j) * kBK + 4 * lane;
+        const int64_t k = static_cast<int64_t>(j) * kRow + 4 * lane;
         uint2 v = make_uint2(0u, 0u);
         if (k < a.K) v = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.x) + t * a.K + k));
         const Parts q = split4(v);
-        uint8_t* blk = ws_b + (tt * p.nk + j) * p.b_bytes;
+        uint8_t* blk = ws_b + (tt * p.nk + (j >> 1)) * p.b_bytes;
+        uint8_t* tile = blk + (j & 1) * 2 * p.mp * kRow;
         const int r_lo = p.mp + r;
-        *reinterpret_cast<uint32_t*>(blk + tile_at(r, lane)) = q.hi;
-        *reinterpret_cast<uint32_t*>(blk + tile_at(r_lo, lane)) = q.lo;
+        *reinterpret_cast<uint32_t*>(tile + tile_at(r, lane)) = q.hi;
+        *reinterpret_cast<uint32_t*>(tile + tile_at(r_lo, lane)) = q.lo;
         if ((lane & 7) == 0) {
-            uint8_t* atom = blk + 2 * p.mp * kBK;
+            uint8_t* atom = blk + 4 * p.mp * kRow + (j & 1) * p.sfb_bytes;
             atom[atom_at(r, lane >> 3)] = static_cast<uint8_t>(q.s_hi);
             atom[p.stacked ? atom_at(r_lo, lane >> 3) : kAtom + atom_at(r, lane >> 3)] = static_cast<uint8_t>(q.s_lo);
         }
@@ -293,16 +299,29 @@ linear_few_kernel(const __grid_constant__ CUtensorMap tmap_codes, const __grid_c
     // this CTA's K stages [j0, j0 + n); the launch keeps SPLIT <= nk, so n >= 1
     const int j0 = rank * p.nk / SPLIT;
     const int n = (rank + 1) * p.nk / SPLIT - j0;
+    const int k_left = static_cast<int>(a.K) - 256 * j0;   // of K from the CTA's first element on
     constexpr int kFeat = kGated ? 64 : kBM;     // output features of the tile
     uint8_t* codes = smem + NS * p.stage_bytes;  // the code slots lie behind the stages
 
-    if (tid == 7 * 32) {
-        for (int s = 0; s < CS; ++s) {
+    // code slot i % CS <- stage i (past K: zero fill)
+    auto load_codes = [&](int i) {
+        uint8_t* dst = codes + i % CS * kCodeBytes;
+        uint64_t* bar = &code_full[i % CS];
+        const int x = 128 * (j0 + i);
+        mbar_arrive_expect_tx(bar, kCodeBytes);
+        tma_load_2d(dst, &tmap_codes, bar, x, static_cast<int>(f * kFeat));
+        if (kGated) tma_load_2d(dst + kCodeBytes / 2, &tmap_codes, bar, x, static_cast<int>(a.n_out + f * kFeat));
+    };
+    if (tid == 11 * 32) {
+        for (int s = 0; s < kMaxSlots; ++s) {
             mbar_init(&code_full[s], 1);
-            mbar_init(&code_empty[s], 4);   // one arrival per spreading warp
+            mbar_init(&code_empty[s], kSpreadWarps);
         }
-        for (int s = 0; s < NS; ++s) {
-            mbar_init(&full[s], kOwn ? 4 : 5);   // four spreading warps and the copies of warp 4
+        fence_mbar_init();
+        // the first copies start before the other warps are ready
+        for (int i = 0; i < min(n, CS); ++i) load_codes(i);
+        for (int s = 0; s < kMaxStages; ++s) {
+            mbar_init(&full[s], kSpreadWarps + (kOwn ? 0 : 1));   // and the copies of warp 8
             mbar_init(&empty[s], 1);
         }
         mbar_init(done, 1);
@@ -310,138 +329,124 @@ linear_few_kernel(const __grid_constant__ CUtensorMap tmap_codes, const __grid_c
         s_never = 0;
         fence_mbar_init();
     }
-    // code slot u % CS <- stages 2 u and 2 u + 1 of this CTA (past K: zero fill)
-    auto load_codes = [&](int u) {
-        uint8_t* dst = codes + u % CS * kCodeBytes;
-        const int x = 64 * j0 + 128 * u;
-        mbar_arrive_expect_tx(&code_full[u % CS], kCodeBytes);
-        if (kGated) {
-            tma_load_2d(dst, &tmap_codes, &code_full[u % CS], x, static_cast<int>(f * 64));
-            tma_load_2d(dst + kCodeBytes / 2, &tmap_codes, &code_full[u % CS], x, static_cast<int>(a.n_out + f * 64));
-        } else {
-            tma_load_2d(dst, &tmap_codes, &code_full[u % CS], x, static_cast<int>(f * kBM));
-        }
-    };
-    const int slots_used = (n + 1) / 2;
-    if (tid == 7 * 32) {   // the first copies start before the other warps are ready
-        for (int u = 0; u < min(slots_used, CS); ++u) load_codes(u);
-    }
-    if (warp == 6) {
+    if (warp == 10) {
         tmem_alloc(&s_tmem, kTmemCols);
         tmem_relinquish();
+    }
+    // kOwn: spreading warp 4 h + w splits tokens w, w + 4, ... (at most 16) of half h of each stage and
+    // fetches the scales of its rows 32 w .. 32 w + 31; all stages' are on their way from the start
+    uint2 xv[kOwn ? kOwnStages : 1][4];
+    uint32_t sv[kOwn ? kOwnStages : 1];
+    if (kOwn && warp < kSpreadWarps) {
+        const int kb = static_cast<int>(a.K / 32), half = warp >> 2;
+        const int64_t row = weight_row<kGated>(a, f, 32 * (warp & 3) + lane);
+        const uint8_t* scales = a.scales + (row < 0 ? 0 : row) * kb;
+#pragma unroll
+        for (int i = 0; i < kOwnStages; ++i) {
+            const int64_t k = 256LL * (j0 + i) + 128 * half + 4 * lane;
+            uint32_t b[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int t = (warp & 3) + 4 * q, x = 8 * (j0 + i) + 4 * half + q;
+                xv[i][q] = make_uint2(0u, 0u);
+                if (i < n && t < mt && k < a.K)
+                    xv[i][q] = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.x) + (t0 + t) * a.K + k));
+                b[q] = i < n && x < kb ? __ldg(scales + x) : 0x7Fu;
+            }
+            sv[i] = b[0] | b[1] << 8 | b[2] << 16 | b[3] << 24;
+        }
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = s_tmem;
 
-    if (warp < 4) {
-        // ---------------- codes -> containers: 16 bytes of codes of a row are containers 2 ch and
-        // 2 ch + 1, swizzled within the row's 128 bytes
-        const int ch = tid & 3, r = tid >> 2;
-        const uint32_t from = smem_u32(codes) + r * 128 + 16 * ch;
-        const uint32_t to = smem_u32(smem) + r * kBK + (((2 * ch) ^ (r & 7)) << 4);
-        // kOwn: tokens warp, warp + 4, ... (at most 16) and the scales of row 32 warp + lane of a stage, one
-        // stage ahead in registers
-        uint2 xv[4];
-        uint32_t sv = 0;
-        const int kb = static_cast<int>(a.K / 32);
-        const int64_t my_row = weight_row<kGated>(a, f, 32 * warp + lane);
-        const uint8_t* my_scales = a.scales + (my_row < 0 ? 0 : my_row) * kb;
-        auto fetch = [&](int i) {
-            const int64_t k = static_cast<int64_t>(j0 + i) * kBK + 4 * lane;
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int t = warp + 4 * q;
-                xv[q] = make_uint2(0u, 0u);
-                if (t < mt && k < a.K)
-                    xv[q] = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.x) + (t0 + t) * a.K + k));
-            }
-            uint32_t b[4];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int x = 4 * (j0 + i) + q;
-                b[q] = x < kb ? __ldg(my_scales + x) : 0x7Fu;
-            }
-            sv = b[0] | b[1] << 8 | b[2] << 16 | b[3] << 24;
-        };
-        auto prepare = [&](uint8_t* st) {   // into the stage's activation and scale parts
-            uint8_t* tile = st + kABytes;
-            uint8_t* atom = tile + 2 * p.mp * kBK;
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int t = warp + 4 * q;
-                if (t < mt) {
-                    const Parts z = split4(xv[q]);
-                    *reinterpret_cast<uint32_t*>(tile + tile_at(t, lane)) = z.hi;
-                    *reinterpret_cast<uint32_t*>(tile + tile_at(p.mp + t, lane)) = z.lo;
-                    if ((lane & 7) == 0) {
-                        atom[atom_at(t, lane >> 3)] = static_cast<uint8_t>(z.s_hi);
-                        atom[atom_at(p.mp + t, lane >> 3)] = static_cast<uint8_t>(z.s_lo);
-                    }
-                }
-            }
-            *reinterpret_cast<uint32_t*>(tile + p.b_bytes + 16 * lane + 4 * warp) = sv;
-        };
-        if (kOwn) fetch(0);
+    if (warp < kSpreadWarps) {
+        // ---------------- codes -> containers: warps 0-3 the first half of a stage, 4-7 the second; 16
+        // bytes of codes of a row are containers 2 ch and 2 ch + 1, swizzled within the row's 128 bytes
+        const int half = warp >> 2, ch = tid & 3, r = (tid & 127) >> 2;
+        const uint32_t from = smem_u32(codes) + r * 128 + half * 64 + 16 * ch;
+        const uint32_t to = smem_u32(smem) + half * kATile + r * kRow + (((2 * ch) ^ (r & 7)) << 4);
         bool ok = true;
-        for (int i = 0; i < n; ++i) {
-            const int u = i >> 1;
+        auto spread = [&](int i, const uint2* x, uint32_t scales) {
             bool got = i < NS || mbar_wait_spin(&empty[i % NS], ((i / NS) & 1) ^ 1, &s_abort);
             if (kOwn && __all_sync(0xFFFFFFFFu, got)) {
-                prepare(smem + i % NS * p.stage_bytes);
-                if (i + 1 < n) fetch(i + 1);
+                uint8_t* tile = smem + i % NS * p.stage_bytes + 2 * kATile + half * 2 * p.mp * kRow;
+                uint8_t* atom = smem + i % NS * p.stage_bytes + 2 * kATile + 4 * p.mp * kRow + half * p.sfb_bytes;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const int t = (warp & 3) + 4 * q;
+                    if (t < mt) {
+                        const Parts z = split4(x[q]);
+                        *reinterpret_cast<uint32_t*>(tile + tile_at(t, lane)) = z.hi;
+                        *reinterpret_cast<uint32_t*>(tile + tile_at(p.mp + t, lane)) = z.lo;
+                        if ((lane & 7) == 0) {
+                            atom[atom_at(t, lane >> 3)] = static_cast<uint8_t>(z.s_hi);
+                            atom[atom_at(p.mp + t, lane >> 3)] = static_cast<uint8_t>(z.s_lo);
+                        }
+                    }
+                }
+                uint8_t* sfa = smem + i % NS * p.stage_bytes + 2 * kATile + p.b_bytes + half * kAtom;
+                *reinterpret_cast<uint32_t*>(sfa + 16 * lane + 4 * (warp & 3)) = scales;
             }
-            if (got && !(i & 1)) got = mbar_wait_spin(&code_full[u % CS], (u / CS) & 1, &s_abort);
-            if (!__all_sync(0xFFFFFFFFu, got)) { ok = false; break; }
-            const uint32_t src = from + u % CS * kCodeBytes + (i & 1) * 64, dst = to + i % NS * p.stage_bytes;
+            if (got) got = mbar_wait_spin(&code_full[i % CS], (i / CS) & 1, &s_abort);
+            if (!__all_sync(0xFFFFFFFFu, got)) return false;
+            const uint32_t src = from + i % CS * kCodeBytes, dst = to + i % NS * p.stage_bytes;
             uint4 v[4];
 #pragma unroll
             for (int q = 0; q < 4; ++q) v[q] = lds128(src + q * 32 * 128);
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                sts64(dst + q * 32 * kBK, v[q].x, v[q].y);
-                sts64((dst ^ 16u) + q * 32 * kBK, v[q].z, v[q].w);
+                sts64(dst + q * 32 * kRow, v[q].x, v[q].y);
+                sts64((dst ^ 16u) + q * 32 * kRow, v[q].z, v[q].w);
             }
             fence_async_proxy();   // generic writes -> the tensor core's reads
             __syncwarp();
             if (lane == 0) {
                 mbar_arrive(&full[i % NS]);
-                if ((i & 1) || i + 1 == n) mbar_arrive(&code_empty[u % CS]);
+                mbar_arrive(&code_empty[i % CS]);
             }
+            return true;
+        };
+        if (kOwn) {
+#pragma unroll
+            for (int i = 0; i < kOwnStages; ++i)
+                if (i < n && ok) ok = spread(i, xv[i], sv[i]);
+        } else {
+            for (int i = 0; i < n && ok; ++i) ok = spread(i, xv[0], 0u);
         }
         if (!ok) {
             s_abort = 1;
             record_status(a.status, MXFP4_ERR_TIMEOUT);
         }
-    } else if (warp == 7) {
+    } else if (warp == 11) {
         // ---------------- packed codes
         if (lane == 0) {
             bool ok = true;
-            int u = min(slots_used, CS);
-            for (; u < slots_used; ++u) {
-                if (!mbar_wait(&code_empty[u % CS], ((u / CS) & 1) ^ 1, &s_abort)) { ok = false; break; }
-                load_codes(u);
+            int i = min(n, CS);
+            for (; i < n; ++i) {
+                if (!mbar_wait(&code_empty[i % CS], ((i / CS) & 1) ^ 1, &s_abort)) { ok = false; break; }
+                load_codes(i);
             }
             if (!ok) {
                 s_abort = 1;
                 record_status(a.status, MXFP4_ERR_TIMEOUT);
             }
-            // every slot's last copy lands before the slots are used again or the CTA ends
-            for (int w = u > CS ? u - CS : 0; w < u; ++w) mbar_wait(&code_full[w % CS], (w / CS) & 1, &s_never);
+            // every slot's last copy lands before the CTA ends
+            for (int w = i > CS ? i - CS : 0; w < i; ++w) mbar_wait(&code_full[w % CS], (w / CS) & 1, &s_never);
         }
-    } else if (warp == 4) {
+    } else if (warp == 8) {
         // ---------------- prepared activations and scales
         if (!kOwn && lane == 0) {
             grid_wait();   // the prepare kernel's writes are complete
             bool ok = true;
             for (int i = 0; i < n; ++i) {
                 const int s = i % NS;
-                if (!mbar_wait_spin(&empty[s], ((i / NS) & 1) ^ 1, &s_abort)) { ok = false; break; }
-                uint8_t* dst = smem + s * p.stage_bytes + kABytes;
-                mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(p.b_bytes + kAtom));
+                if (!mbar_wait(&empty[s], ((i / NS) & 1) ^ 1, &s_abort)) { ok = false; break; }
+                uint8_t* dst = smem + s * p.stage_bytes + 2 * kATile;
+                mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(p.b_bytes + 2 * kAtom));
                 bulk_load(dst, ws_b + (tt * p.nk + j0 + i) * p.b_bytes, static_cast<uint32_t>(p.b_bytes), &full[s]);
-                bulk_load(dst + p.b_bytes, ws_sfa + (f * p.nk + j0 + i) * kAtom, kAtom, &full[s]);
+                bulk_load(dst + p.b_bytes, ws_sfa + (f * p.nk + j0 + i) * (2 * kAtom), 2 * kAtom, &full[s]);
             }
             if (!ok) {
                 s_abort = 1;
@@ -452,39 +457,43 @@ linear_few_kernel(const __grid_constant__ CUtensorMap tmap_codes, const __grid_c
                 while (globaltimer_ns() - w0 < 1000000ull) {}
             }
         }
-    } else if (warp == 5) {
+    } else if (warp == 9) {
         // ---------------- MMA issuer (the whole warp walks the loop, one lane issues)
         bool ok = true;
         const bool lead = elect_one();
         const uint32_t idesc = idesc_mxf8(p.stacked ? 2 * p.mp : p.mp, 0);
         constexpr uint32_t kNextId = (1u << 4) | (1u << 29);
-        const int k_all = static_cast<int>(a.K - static_cast<int64_t>(j0) * kBK);
-        const uint32_t b_lo = static_cast<uint32_t>(p.mp * kBK) >> 4;          // lo rows behind the hi rows
-        const uint32_t sf_at = kABytes + 2 * p.mp * kBK, sfa_at = kABytes + p.b_bytes;
+        const uint32_t tile_b = 2 * p.mp * kRow;                                  // a half's hi and lo rows
+        const uint32_t lo_b = static_cast<uint32_t>(p.mp * kRow) >> 4;            // lo rows behind the hi rows
+        const uint32_t sfb_at = 2 * kATile + 2 * tile_b, sfa_at = 2 * kATile + p.b_bytes;
         for (int i = 0; i < n; ++i) {
             const int s = i % NS;
-            const uint32_t ph = (i / NS) & 1;
-            if (!__all_sync(0xFFFFFFFFu, mbar_wait_spin(&full[s], ph, &s_abort))) {
+            if (!__all_sync(0xFFFFFFFFu, mbar_wait_spin(&full[s], (i / NS) & 1, &s_abort))) {
                 ok = false;
                 break;
             }
             tc_fence_after();
             const uint32_t st = smem_u32(smem) + s * p.stage_bytes;
-            const uint32_t set = tmem + kSfCol + 16 * (i & 1);
-            const uint64_t da = sw128_desc(st), db = sw128_desc(st + kABytes);
-            const int steps = (k_all - i * kBK) / 32;
+            const int steps = (k_left - 256 * i) / 32;
             if (lead) {
-                tmem_cp_32x128b_x4(set, rows16_desc(st + sfa_at));
-                tmem_cp_32x128b_x4(set + 4, rows16_desc(st + sf_at));
-                if (!p.stacked) tmem_cp_32x128b_x4(set + 8, rows16_desc(st + sf_at + kAtom));
 #pragma unroll
-                for (uint32_t q = 0; q < 4; ++q) {   // 32 elements of K per MMA, scale q of the stage
-                    if (static_cast<int>(q) < steps) {
-                        mma_mxf8f6f4(tmem, da + 2 * q, db + 2 * q, idesc + q * kNextId, set | (q << 30),
-                                     (set + 4) | (q << 30), q == 0 && i == 0 ? 0u : 1u);
-                        if (!p.stacked)
-                            mma_mxf8f6f4(tmem, da + 2 * q, db + b_lo + 2 * q, idesc + q * kNextId, set | (q << 30),
-                                         (set + 8) | (q << 30), 1u);
+                for (uint32_t h = 0; h < 2; ++h) {
+                    if (static_cast<int>(4 * h) < steps) {
+                        const uint32_t set = tmem + kSfCol + 32 * (i & 1) + 16 * h;
+                        const uint64_t da = sw128_desc(st + h * kATile), db = sw128_desc(st + 2 * kATile + h * tile_b);
+                        tmem_cp_32x128b_x4(set, rows16_desc(st + sfa_at + h * kAtom));
+                        tmem_cp_32x128b_x4(set + 4, rows16_desc(st + sfb_at + h * p.sfb_bytes));
+                        if (!p.stacked) tmem_cp_32x128b_x4(set + 8, rows16_desc(st + sfb_at + h * p.sfb_bytes + kAtom));
+#pragma unroll
+                        for (uint32_t q = 0; q < 4; ++q) {   // 32 elements of K per MMA, scale q of the half
+                            if (static_cast<int>(4 * h + q) < steps) {
+                                mma_mxf8f6f4(tmem, da + 2 * q, db + 2 * q, idesc + q * kNextId, set | (q << 30),
+                                             (set + 4) | (q << 30), (i | h | q) != 0 ? 1u : 0u);
+                                if (!p.stacked)
+                                    mma_mxf8f6f4(tmem, da + 2 * q, db + lo_b + 2 * q, idesc + q * kNextId, set | (q << 30),
+                                                 (set + 8) | (q << 30), 1u);
+                            }
+                        }
                     }
                 }
                 tc_commit(&empty[s]);
@@ -552,7 +561,7 @@ linear_few_kernel(const __grid_constant__ CUtensorMap tmap_codes, const __grid_c
         float* to_row = part + 32 * q + lane;
         // 16 columns at a time; the columns behind the tile's tokens (mp = 8, or an odd half) hold
         // other rows' sums or nothing, and land behind the rows that are read
-        for (int c = 16 * (warp >> 2); c < mt; c += 32) {
+        for (int c = 16 * (warp >> 2); c < mt; c += 16 * (kThreads / 128)) {
             uint32_t v[16], w[16];
             tmem_ld_x16(base + c, v);
             if (p.stacked) tmem_ld_x16(base + p.mp + c, w);
@@ -637,10 +646,17 @@ linear_few_kernel(const __grid_constant__ CUtensorMap tmap_codes, const __grid_c
     tc_fence_before();
     if (SPLIT > 1) cluster_sync_all();   // the partials are read: their CTAs may end
     __syncthreads();
-    if (warp == 6) {
+    if (warp == 10) {
         tc_fence_after();
         tmem_dealloc(tmem, kTmemCols);
     }
+}
+
+// CTAs along K of a tile that prepares its own part: clusters of 4 while the GPU holds that many at once.
+int own_split(const Plan& p) {
+    int split = p.w_tiles <= 30 ? 4 : 2;
+    while (split > p.nk) split /= 2;
+    return split;
 }
 
 // The launch geometry.  Independent of the device, so that the workspace query and the call agree.
@@ -648,7 +664,7 @@ Plan make_plan(int64_t M, int64_t K, int64_t n_out, bool gated) {
     Plan p{};
     const int f = gated ? 64 : kBM;
     p.w_tiles = static_cast<int>((n_out + f - 1) / f);
-    p.nk = static_cast<int>((K + kBK - 1) / kBK);
+    p.nk = static_cast<int>((K + 255) / 256);
     // As few token tiles as hold M (every one streams the weights), or, when those do not fill
     // the SMs and K could not be split over what is left, as many as do.
     int64_t tt = (M + kMaxMp - 1) / kMaxMp;
@@ -656,10 +672,17 @@ Plan make_plan(int64_t M, int64_t K, int64_t n_out, bool gated) {
     const int per = static_cast<int>((M + tt - 1) / tt);
     p.mp = per <= 8 ? 8 : (per + 15) / 16 * 16;
     p.t_tiles = static_cast<int>((M + p.mp - 1) / p.mp);
-    p.own = p.mp <= kOwnMp;
     p.stacked = 2 * p.mp <= 128;
-    p.b_bytes = 2 * p.mp * kBK + (p.stacked ? 1 : 2) * kAtom;
-    p.stage_bytes = (kABytes + p.b_bytes + kAtom + 1023) / 1024 * 1024;
+    p.sfb_bytes = (p.stacked ? 1 : 2) * kAtom;
+    p.b_bytes = 4 * p.mp * kRow + 2 * p.sfb_bytes;
+    p.stage_bytes = 2 * kATile + p.b_bytes + 2 * kAtom;
+    // rings: three stages where three code slots (what is in flight from memory) fit as well
+    const int room = kSmemLimit - 1024 - 512;   // the base's alignment, static shared memory
+    p.stages = kMaxStages;
+    if (room - p.stages * p.stage_bytes < 3 * kCodeBytes) p.stages = 2;
+    p.slots = (room - p.stages * p.stage_bytes) / kCodeBytes;
+    if (p.slots > kMaxSlots) p.slots = kMaxSlots;
+    p.own = p.mp <= kOwnMp && p.t_tiles == 1 && (p.nk + own_split(p) - 1) / own_split(p) <= kOwnStages;
     return p;
 }
 
@@ -671,13 +694,13 @@ Plan make_plan(int64_t M, int64_t K, int64_t n_out, bool gated) {
 // and 32.)  The prepare kernel keeps 128 rows of block scales in shared memory, which bounds K.
 bool linear_is_few(int64_t M, int64_t K, int64_t n_out, bool gated) {
     const int64_t t = (M + kMaxMp - 1) / kMaxMp, f = gated ? 64 : kBM, w = (n_out + f - 1) / f;
-    return K <= 8192 && (t == 1 || (t <= 3 && t * w <= kSms));
+    return K <= 8192 && (t == 1 || (t <= 4 && t * w <= kSms));
 }
 
 size_t linear_few_ws_bytes(int64_t M, int64_t K, int64_t n_out, bool gated) {
     const Plan p = make_plan(M, K, n_out, gated);
     if (p.own) return 0;
-    return static_cast<size_t>(p.t_tiles) * p.nk * p.b_bytes + static_cast<size_t>(p.w_tiles) * p.nk * kAtom;
+    return static_cast<size_t>(p.t_tiles) * p.nk * p.b_bytes + static_cast<size_t>(p.w_tiles) * p.nk * 2 * kAtom;
 }
 
 namespace {
@@ -737,10 +760,10 @@ template <bool kGated, bool kOwn>
 cudaError_t launch_split(const CUtensorMap& tmap_codes, const LinearArgs& a, Plan p, const uint8_t* ws_b,
                          const uint8_t* ws_sfa, cudaStream_t stream) {
     const int64_t tiles = static_cast<int64_t>(p.w_tiles) * p.t_tiles;
-    int split = kMaxCluster;
-    for (; split > 1; split /= 2) {
+    int split = kOwn ? own_split(p) : kMaxCluster;
+    for (; !kOwn && split > 1; split /= 2) {
         int clusters = 0;
-        if (split > p.nk || tiles * split > 2LL * kSms) continue;   // two CTAs per SM at most
+        if (split > p.nk || tiles * split > kSms) continue;
         cudaError_t e = product_of<kGated, kOwn>(split, tmap_codes, a, p, ws_b, ws_sfa, stream, false, &clusters);
         if (e != cudaSuccess) return e;
         if (tiles <= clusters) break;
@@ -751,20 +774,6 @@ cudaError_t launch_split(const CUtensorMap& tmap_codes, const LinearArgs& a, Pla
 template <bool kGated>
 cudaError_t launch_few(const LinearArgs& a, const CUtensorMap& tmap_codes, Plan p, void* ws, int sm_count,
                        cudaStream_t stream) {
-    // Rings: `least` stages, then code slots (what is in flight from memory), then more stages.  Two
-    // resident CTAs per SM where each then has two stages and two slots: they hide each
-    // other's start and finish.
-    const int fixed = 1024 + 1024 + 512;   // alignment slack, the system's share, static shared memory
-    auto fit = [&](int room, int least) {
-        p.stages = least;
-        p.slots = (room - p.stages * p.stage_bytes) / kCodeBytes;
-        if (p.slots > kMaxSlots) p.slots = kMaxSlots;
-        if (p.slots < 2) return false;
-        while (p.stages < kMaxStages && room - p.slots * kCodeBytes >= (p.stages + 1) * p.stage_bytes) ++p.stages;
-        return true;
-    };
-    if (!fit(kSmemSm / 2 - fixed, 3) && !fit(kSmemSm / 2 - fixed, 2) && !fit(kSmemSm - fixed, 3))
-        return cudaErrorInvalidConfiguration;
     if (p.own) return launch_split<kGated, true>(tmap_codes, a, p, nullptr, nullptr, stream);
     uint8_t* ws_b = static_cast<uint8_t*>(ws);
     uint8_t* ws_sfa = ws_b + static_cast<size_t>(p.t_tiles) * p.nk * p.b_bytes;
@@ -772,10 +781,10 @@ cudaError_t launch_few(const LinearArgs& a, const CUtensorMap& tmap_codes, Plan 
     const int rows_smem = kBM * kb + 2 * 48;
     cudaError_t e = cudaFuncSetAttribute(linear_few_prepare_kernel<kGated>, cudaFuncAttributeMaxDynamicSharedMemorySize, rows_smem);
     if (e != cudaSuccess) return e;
-    const int64_t items = a.M * p.nk;
-    int64_t xg = (items + kThreads / 32 - 1) / (kThreads / 32);
+    const int64_t items = a.M * ((kb + 3) / 4);
+    int64_t xg = (items + kPrepareThreads / 32 - 1) / (kPrepareThreads / 32);
     if (xg > 4LL * sm_count) xg = 4LL * sm_count;
-    linear_few_prepare_kernel<kGated><<<static_cast<unsigned>(p.w_tiles + xg), kThreads, rows_smem, stream>>>(a, p, ws_b, ws_sfa);
+    linear_few_prepare_kernel<kGated><<<static_cast<unsigned>(p.w_tiles + xg), kPrepareThreads, rows_smem, stream>>>(a, p, ws_b, ws_sfa);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     return launch_split<kGated, false>(tmap_codes, a, p, ws_b, ws_sfa, stream);
 }
