@@ -38,6 +38,15 @@ static __device__ __noinline__ float4 activate4(int act, float4 z, float4 u) {
     return make_float4(v[0], v[1], v[2], v[3]);
 }
 
+// mbar_wait_spin that polls a while before it first reads the clock: the read takes longer than the
+// waits that end soon.  Bounded the same way.
+__device__ __forceinline__ bool wait_poll(uint64_t* bar, uint32_t parity, volatile int* abort) {
+#pragma unroll 1
+    for (int i = 0; i < 64; ++i)
+        if (mbar_test_wait(bar, parity)) return true;
+    return mbar_wait_spin(bar, parity, abort);
+}
+
 __device__ __forceinline__ float bias_at(const LinearArgs& a, int64_t n) {
     if (!a.bias) return 0.f;
     return a.bias_f32 ? static_cast<const float*>(a.bias)[n]

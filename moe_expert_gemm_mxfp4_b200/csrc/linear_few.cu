@@ -187,8 +187,8 @@ __device__ __forceinline__ int64_t weight_row(const LinearArgs& a, int64_t f, in
 }
 
 // ---------------------------------------------------------------- prepare
-// The first w_tiles CTAs lay the weights' scales out: per tile and half stage an atom of 512
-// bytes, scale j of row r at byte 16 (r % 32) + 4 (r / 32) + j.  The others take (token, half
+// The first 4 w_tiles CTAs lay the weights' scales out, 32 rows each: per tile and half stage an atom of
+// 512 bytes, scale j of row r at byte 16 (r % 32) + 4 (r / 32) + j.  The others take (token, half
 // stage) items, one per warp: 4 elements per lane, 8 lanes to a block.
 template <bool kGated>
 __global__ void __launch_bounds__(kPrepareThreads)
@@ -197,50 +197,36 @@ linear_few_prepare_kernel(const LinearArgs a, const Plan p, uint8_t* __restrict_
     extern __shared__ __align__(16) uint8_t s_rows[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int kb = static_cast<int>(a.K / 32), halves = (kb + 3) / 4;
-    if (static_cast<int>(blockIdx.x) < p.w_tiles) {
-        const int64_t f = blockIdx.x;
-        // the tile's scales: one run of rows (gated: one of gate, one of up rows)
-        constexpr int kSeg = kGated ? 64 : kBM;
-        int shift[2] = {0, 0};
-#pragma unroll
-        for (int h = 0; h < (kGated ? 2 : 1); ++h) {
-            const int64_t row0 = f * kSeg + (h ? a.n_out : 0);
-            const int64_t left = (kGated ? a.n_out : a.N) - f * kSeg;
-            const int len = static_cast<int>((left < kSeg ? left : kSeg) * kb);
-            const uint8_t* src = a.scales + row0 * kb;
-            shift[h] = static_cast<int>(reinterpret_cast<uintptr_t>(src) & 15);
-            uint8_t* dst = s_rows + h * (64 * kb + 32) / 16 * 16 + shift[h];
-            const int head = min(len, (16 - shift[h]) & 15), body = (len - head) / 16;
-            for (int i = tid; i < body; i += kPrepareThreads)
-                reinterpret_cast<uint4*>(dst + head)[i] = __ldg(reinterpret_cast<const uint4*>(src + head) + i);
-            for (int i = tid; i < head; i += kPrepareThreads) dst[i] = src[i];
-            for (int i = head + 16 * body + tid; i < len; i += kPrepareThreads) dst[i] = src[i];
-        }
+    const int w_ctas = 4 * p.w_tiles;
+    if (static_cast<int>(blockIdx.x) < w_ctas) {
+        // 32 rows of a tile: one run of bytes, brought over in 16-byte vectors
+        const int64_t f = blockIdx.x / 4;
+        const int q = blockIdx.x % 4;
+        const int64_t row0 = kGated ? f * 64 + 32 * (q & 1) : f * kBM + 32 * q;
+        const int64_t left = (kGated ? a.n_out : a.N) - row0;
+        const int rows = left < 0 ? 0 : left > 32 ? 32 : static_cast<int>(left), len = rows * kb;
+        const uint8_t* src = a.scales + (row0 + (kGated && q >= 2 ? a.n_out : 0)) * kb;
+        const int shift = static_cast<int>(reinterpret_cast<uintptr_t>(src) & 15);
+        uint8_t* dst = s_rows + shift;
+        const int head = min(len, (16 - shift) & 15), body = (len - head) / 16;
+#pragma unroll 4
+        for (int i = tid; i < body; i += kPrepareThreads)
+            reinterpret_cast<uint4*>(dst + head)[i] = __ldg(reinterpret_cast<const uint4*>(src + head) + i);
+        for (int i = tid; i < head; i += kPrepareThreads) dst[i] = src[i];
+        for (int i = head + 16 * body + tid; i < len; i += kPrepareThreads) dst[i] = src[i];
         __syncthreads();
         for (int j = warp; j < halves; j += kPrepareThreads / 32) {
-            uint32_t w[4];
+            uint32_t w = 0;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int r = lane + 32 * q;
-                w[q] = 0x7F7F7F7Fu;
-                if (weight_row<kGated>(a, f, r) >= 0) {
-                    const int h = kGated && r >= 64;
-                    const uint8_t* row = s_rows + h * (64 * kb + 32) / 16 * 16 + shift[h] + (kGated ? r & 63 : r) * kb;
-                    w[q] = 0;
-#pragma unroll
-                    for (int b = 0; b < 4; ++b) {
-                        const uint32_t s = 4 * j + b < kb ? row[4 * j + b] : 0x7Fu;
-                        w[q] |= s << (8 * b);
-                    }
-                }
-            }
-            reinterpret_cast<uint4*>(ws_sfa + (f * 2 * p.nk + j) * kAtom)[lane] = make_uint4(w[0], w[1], w[2], w[3]);
+            for (int b = 0; b < 4; ++b)
+                w |= (lane < rows && 4 * j + b < kb ? dst[lane * kb + 4 * j + b] : 0x7Fu) << (8 * b);
+            *reinterpret_cast<uint32_t*>(ws_sfa + (f * 2 * p.nk + j) * kAtom + 16 * lane + 4 * q) = w;
         }
         return;
     }
     const int64_t items = a.M * halves;
-    const int64_t step = static_cast<int64_t>(gridDim.x - p.w_tiles) * (kPrepareThreads / 32);
-    for (int64_t it = static_cast<int64_t>(blockIdx.x - p.w_tiles) * (kPrepareThreads / 32) + warp; it < items; it += step) {
+    const int64_t step = static_cast<int64_t>(gridDim.x - w_ctas) * (kPrepareThreads / 32);
+    for (int64_t it = static_cast<int64_t>(blockIdx.x - w_ctas) * (kPrepareThreads / 32) + warp; it < items; it += step) {
         const int64_t t = it / halves;
         const int j = static_cast<int>(it - t * halves);
         const int64_t tt = t / p.mp;
@@ -369,7 +355,7 @@ linear_few_kernel(const __grid_constant__ CUtensorMap tmap_codes, const __grid_c
         const uint32_t to = smem_u32(smem) + half * kATile + r * kRow + (((2 * ch) ^ (r & 7)) << 4);
         bool ok = true;
         auto spread = [&](int i, const uint2* x, uint32_t scales) {
-            bool got = i < NS || mbar_wait_spin(&empty[i % NS], ((i / NS) & 1) ^ 1, &s_abort);
+            bool got = i < NS || wait_poll(&empty[i % NS], ((i / NS) & 1) ^ 1, &s_abort);
             if (kOwn && __all_sync(0xFFFFFFFFu, got)) {
                 uint8_t* tile = smem + i % NS * p.stage_bytes + 2 * kATile + half * 2 * p.mp * kRow;
                 uint8_t* atom = smem + i % NS * p.stage_bytes + 2 * kATile + 4 * p.mp * kRow + half * p.sfb_bytes;
@@ -389,7 +375,7 @@ linear_few_kernel(const __grid_constant__ CUtensorMap tmap_codes, const __grid_c
                 uint8_t* sfa = smem + i % NS * p.stage_bytes + 2 * kATile + p.b_bytes + half * kAtom;
                 *reinterpret_cast<uint32_t*>(sfa + 16 * lane + 4 * (warp & 3)) = scales;
             }
-            if (got) got = mbar_wait_spin(&code_full[i % CS], (i / CS) & 1, &s_abort);
+            if (got) got = wait_poll(&code_full[i % CS], (i / CS) & 1, &s_abort);
             if (!__all_sync(0xFFFFFFFFu, got)) return false;
             const uint32_t src = from + i % CS * kCodeBytes, dst = to + i % NS * p.stage_bytes;
             uint4 v[4];
@@ -468,7 +454,7 @@ linear_few_kernel(const __grid_constant__ CUtensorMap tmap_codes, const __grid_c
         const uint32_t sfb_at = 2 * kATile + 2 * tile_b, sfa_at = 2 * kATile + p.b_bytes;
         for (int i = 0; i < n; ++i) {
             const int s = i % NS;
-            if (!__all_sync(0xFFFFFFFFu, mbar_wait_spin(&full[s], (i / NS) & 1, &s_abort))) {
+            if (!__all_sync(0xFFFFFFFFu, wait_poll(&full[s], (i / NS) & 1, &s_abort))) {
                 ok = false;
                 break;
             }
@@ -691,7 +677,7 @@ Plan make_plan(int64_t M, int64_t K, int64_t n_out, bool gated) {
 // Few tokens as long as one round of CTAs holds them and three token tiles do: beyond, every round
 // streams the weights again, and dequantizing them once is less.  (2880 x 2880: 384 tokens 17 us here, 21 there,
 // 512 23 and 21; 5760 x 2880 gated: 384 24 and 27, 512 44 and 27; 11520 x 2880: 128 23 and 31, 192 38
-// and 32.)  The prepare kernel keeps 128 rows of block scales in shared memory, which bounds K.
+// and 32.)  The prepare kernel keeps 32 rows of block scales in shared memory, which bounds K.
 bool linear_is_few(int64_t M, int64_t K, int64_t n_out, bool gated) {
     const int64_t t = (M + kMaxMp - 1) / kMaxMp, f = gated ? 64 : kBM, w = (n_out + f - 1) / f;
     return K <= 8192 && (t == 1 || (t <= 4 && t * w <= kSms));
@@ -778,14 +764,13 @@ cudaError_t launch_few(const LinearArgs& a, const CUtensorMap& tmap_codes, Plan 
     uint8_t* ws_b = static_cast<uint8_t*>(ws);
     uint8_t* ws_sfa = ws_b + static_cast<size_t>(p.t_tiles) * p.nk * p.b_bytes;
     const int kb = static_cast<int>(a.K / 32);
-    const int rows_smem = kBM * kb + 2 * 48;
-    cudaError_t e = cudaFuncSetAttribute(linear_few_prepare_kernel<kGated>, cudaFuncAttributeMaxDynamicSharedMemorySize, rows_smem);
-    if (e != cudaSuccess) return e;
+    const int rows_smem = 32 * kb + 16;
     const int64_t items = a.M * ((kb + 3) / 4);
     int64_t xg = (items + kPrepareThreads / 32 - 1) / (kPrepareThreads / 32);
     if (xg > 4LL * sm_count) xg = 4LL * sm_count;
-    linear_few_prepare_kernel<kGated><<<static_cast<unsigned>(p.w_tiles + xg), kPrepareThreads, rows_smem, stream>>>(a, p, ws_b, ws_sfa);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    linear_few_prepare_kernel<kGated><<<static_cast<unsigned>(4 * p.w_tiles + xg), kPrepareThreads, rows_smem, stream>>>(a, p, ws_b, ws_sfa);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
     return launch_split<kGated, false>(tmap_codes, a, p, ws_b, ws_sfa, stream);
 }
 
