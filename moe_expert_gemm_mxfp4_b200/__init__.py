@@ -167,6 +167,13 @@ def mxfp4_gemm(x: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Tensor, m
     return out
 
 
+def _plain(t, dev, dtype, shape) -> bool:
+    """Whether `t` is a contiguous tensor of this dtype and shape on CUDA device `dev`: the
+    short form of ``_need`` and ``_on_current_device``, for calls that take a few
+    microseconds; what it turns down goes through those for the error."""
+    return t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous()
+
+
 def _used_on(stream, *tensors):
     """Tell the allocator that `stream`, if the caller gave one, uses these tensors: those
     allocated here belong to the current stream's pool and must not be reused before."""
@@ -213,16 +220,28 @@ def mxfp4_linear(x: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Tensor,
     [N, K/2] + scales [N, K/32]; bias bf16 or fp32 [N]; n_out = N, or N / 2 with ACT_SWIGLU
     (W rows [0, N/2) gate, [N/2, N) up); residual bf16 [M, n_out], which may be `out`."""
     act = int(act)
-    M, K, N, n_out = _check_linear_operands(x, w_codes, w_scales, bias, act, residual, out, ws)
+    try:
+        (M, K), (N, _), dev = x.shape, w_codes.shape, x.get_device()
+        n_out = N // 2 if act == ACT_SWIGLU else N
+        ready = (dev >= 0 and dev == torch.cuda.current_device() and out is None and ws is None
+                 and (act != ACT_SWIGLU or N % 2 == 0)
+                 and _plain(x, dev, torch.bfloat16, (M, K)) and _plain(w_codes, dev, torch.uint8, (N, K // 2))
+                 and _plain(w_scales, dev, torch.uint8, (N, K // 32))
+                 and (bias is None or _plain(bias, dev, torch.bfloat16, (N,)) or _plain(bias, dev, torch.float32, (N,)))
+                 and (residual is None or _plain(residual, dev, torch.bfloat16, (M, n_out))))
+    except (AttributeError, TypeError, ValueError):
+        ready = False
+    if not ready:
+        M, K, N, n_out = _check_linear_operands(x, w_codes, w_scales, bias, act, residual, out, ws)
     lib = _lib.load()
     new_out = new_ws = None
+    nbytes = 0 if ws is None else ws.numel() * ws.element_size()
     if out is None:
         out = new_out = x.new_empty((M, n_out))
     if ws is None:
-        need = mxfp4_linear_workspace_size(M, K, N, act)
-        if need:
-            ws = new_ws = w_codes.new_empty((need,))
-    nbytes = 0 if ws is None else ws.numel() * ws.element_size()
+        nbytes = mxfp4_linear_workspace_size(M, K, N, act)
+        if nbytes:
+            ws = new_ws = w_codes.new_empty((nbytes,))
     bias_dt = _lib.IN_F32 if bias is not None and bias.dtype is torch.float32 else _lib.IN_BF16
     _lib.check("mxfp4_linear", lib.mxfp4_linear(
         x.data_ptr(), M, K, w_codes.data_ptr(), w_scales.data_ptr(), N, None if bias is None else bias.data_ptr(),
@@ -303,17 +322,10 @@ def moe_mxfp4_route_scored_workspace_size(T, E, top_k) -> int:
     return int(_lib.load().moe_mxfp4_route_scored_workspace_size(T, E, top_k))
 
 
-def moe_mxfp4_route_scored(logits: torch.Tensor, top_k: int, score: int = SCORE_SOFTMAX, bias=None,
-                           n_groups: int = 1, top_groups: int = 1, group_top: int = 1, renorm: bool = True,
-                           scale: float = 1.0, ws=None, stream=None):
-    """Routing with softmax-over-all or sigmoid scores (see include/mxfp4.h): logits fp32 or
-    bf16 [T, E]; bias fp32 [E] is added to the scores for the choice only; of n_groups groups
-    the top_groups by their group_top largest choice values are kept; weights are the chosen
-    experts' scores, renormalised to their sum if `renorm`, times `scale`.  Returns the dict
-    of ``moe_mxfp4_route``."""
+def _check_scored_operands(logits, bias, ws):
+    """Raise unless the scored routing's operands fit together; returns (T, E)."""
     _need_dims(logits, "logits", 2)
-    dt = {torch.bfloat16: _lib.IN_BF16, torch.float32: _lib.IN_F32}.get(logits.dtype)
-    if dt is None:
+    if logits.dtype not in (torch.bfloat16, torch.float32):
         raise ValueError(f"logits: expected dtype bf16 or fp32, got {logits.dtype}")
     _need(logits, "logits")
     T, E = logits.shape
@@ -322,6 +334,27 @@ def moe_mxfp4_route_scored(logits: torch.Tensor, top_k: int, score: int = SCORE_
     if ws is not None:
         _need(ws, "ws")
     _on_current_device(logits=logits, bias=bias, ws=ws)
+    return T, E
+
+
+def moe_mxfp4_route_scored(logits: torch.Tensor, top_k: int, score: int = SCORE_SOFTMAX, bias=None,
+                           n_groups: int = 1, top_groups: int = 1, group_top: int = 1, renorm: bool = True,
+                           scale: float = 1.0, ws=None, stream=None):
+    """Routing with softmax-over-all or sigmoid scores (see include/mxfp4.h): logits fp32 or
+    bf16 [T, E]; bias fp32 [E] is added to the scores for the choice only; of n_groups groups
+    the top_groups by their group_top largest choice values are kept; weights are the chosen
+    experts' scores, renormalised to their sum if `renorm`, times `scale`.  Returns the dict
+    of ``moe_mxfp4_route``."""
+    try:
+        (T, E), dev, dtype = logits.shape, logits.get_device(), logits.dtype
+        ready = (dev >= 0 and dev == torch.cuda.current_device() and ws is None
+                 and (dtype is torch.float32 or dtype is torch.bfloat16) and logits.is_contiguous()
+                 and (bias is None or _plain(bias, dev, torch.float32, (E,))))
+    except (AttributeError, TypeError, ValueError):
+        ready = False
+    if not ready:
+        T, E = _check_scored_operands(logits, bias, ws)
+    dt = _lib.IN_F32 if logits.dtype is torch.float32 else _lib.IN_BF16
     lib = _lib.load()
     top_k = int(top_k)
     if top_k < 1:
@@ -332,11 +365,11 @@ def moe_mxfp4_route_scored(logits: torch.Tensor, top_k: int, score: int = SCORE_
     out = dict(ids=ids, weights=torch.empty_like(ids, dtype=torch.float32), counts=counts,
                offsets=ids.new_empty((E + 1,)), perm=perm, inv=torch.empty_like(perm))
     new_ws = None
-    if ws is None:
-        need = moe_mxfp4_route_scored_workspace_size(T, E, top_k)
-        if need:
-            ws = new_ws = ids.new_empty((need // 4,))
     nbytes = 0 if ws is None else ws.numel() * ws.element_size()
+    if ws is None:
+        nbytes = moe_mxfp4_route_scored_workspace_size(T, E, top_k)
+        if nbytes:
+            ws = new_ws = ids.new_empty((nbytes // 4,))
     _lib.check("moe_mxfp4_route_scored", lib.moe_mxfp4_route_scored(
         logits.data_ptr(), dt, T, E, top_k, int(score), None if bias is None else bias.data_ptr(), int(n_groups),
         int(top_groups), int(group_top), int(bool(renorm)), float(scale), *[t.data_ptr() for t in out.values()],
