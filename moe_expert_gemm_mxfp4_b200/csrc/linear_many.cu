@@ -17,9 +17,13 @@
 // What bounds it: the MMAs of a stage (4 nt cycles) where nt = 256 and the power limit; below that
 // the copies, about 47 bytes per cycle and SM from L2, so that a tile costs as 256 + nt.
 //
-// Roles in each CTA (8 warps): warp 0 producer (its own half of both tiles; completion is
-// counted on the leader's barrier), warp 1 MMA issuer (leader only), warps 4-7 epilogue (TMEM lane
-// quarters), accumulators double-buffered in TMEM (2 x 256 columns).  Every wait is bounded.
+// Roles in each CTA (12 warps): warp 0 producer (its own half of both tiles; completion is
+// counted on the leader's barrier), warp 1 MMA issuer (leader only), warps 4-11 epilogue (TMEM lane
+// quarters, two warps each on alternate 16-column chunks), accumulators double-buffered in TMEM
+// (2 x 256 columns).  Every wait is bounded.  An epilogue warp holds a token per lane; it passes the
+// finished chunk through shared memory, so that its residual loads and its stores cover whole
+// 32-byte sectors of a row, whatever the row's alignment (with a lane storing its own row, 5470 x
+// 160 x 1950 took 246 us).
 #include <algorithm>
 
 #include "linear_epilogue.cuh"
@@ -30,7 +34,9 @@ namespace {
 
 using namespace linear;
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 384;
+constexpr int kEpiWarps = 8;
+constexpr int kPitch = 20;                     // floats per row of a staged chunk: 16 and a conflict-free stride
 constexpr int kBK = 128;                       // K per stage: two tiles of 64 (128 bytes per row)
 constexpr int kXTile = 128 * 64 * 2;           // A rows of one CTA, 64 of K
 constexpr int kMaxStages = 12;
@@ -38,17 +44,18 @@ constexpr int kSmemLimit = 227 * 1024;
 constexpr int kBars = 2 * kMaxStages + 2 + 2 + 1;
 
 struct Layout {
-    int stage_bytes, stages, bias_off, bar_off, misc_off, total;
+    int stage_bytes, stages, bias_off, out_off, bar_off, misc_off, total;
 };
 
 __host__ __device__ inline Layout make_layout(int nt) {
     Layout L;
     L.stage_bytes = 2 * (kXTile + nt / 2 * 64 * 2);
-    const int fixed = 4 * 256 * 4 + kBars * 8 + 16 + 1024;
+    const int fixed = kEpiWarps * (256 + 32 * kPitch) * 4 + kBars * 8 + 16 + 1024;
     L.stages = (kSmemLimit - fixed) / L.stage_bytes;
     if (L.stages > kMaxStages) L.stages = kMaxStages;
     L.bias_off = L.stages * L.stage_bytes;
-    L.bar_off = L.bias_off + 4 * 256 * 4;      // per epilogue warp: the tile's bias
+    L.out_off = L.bias_off + kEpiWarps * 256 * 4;          // per epilogue warp: the tile's bias,
+    L.bar_off = L.out_off + kEpiWarps * 32 * kPitch * 4;   // and a chunk of 32 rows
     L.misc_off = L.bar_off + kBars * 8;
     L.total = L.misc_off + 16 + 1024;          // + slack for the 1024-B alignment of the base
     return L;
@@ -134,54 +141,101 @@ struct Ring {
     }
 };
 
-// 32 consecutive outputs of one token (columns n .. n + 31; the first at index at, nothing past the
-// tile's `limit` columns): z -> y.  r: their residual where they are whole vectors.
-template <bool kGated>
-__device__ __forceinline__ void finish32(const LinearArgs& a, int64_t at, int limit, bool whole, const uint4* r,
-                                         const uint32_t* z, const uint32_t* u, const float* bz, const float* bu) {
-    const uint16_t* res = static_cast<const uint16_t*>(a.residual);
-    uint16_t* y = static_cast<uint16_t*>(a.y);
-    float v[32];
+// A chunk's way out: 32 rows (tokens) x 16 columns that start at element `at` of y, in units of `W` elements
+// (8 where rows are whole 16-byte vectors, 2 where they are whole words, else 1).  Lane l takes
+// units l % (16 / W) of rows l / (16 / W), + 2 W, ...; `rows` and `cols` are what the output has.
+template <int W>
+struct Chunk {
+    static constexpr int kUnits = 16 / W, kStep = 32 / kUnits, kIters = 32 / kStep;
+    __device__ __forceinline__ static void load(const uint16_t* res, int64_t at, int64_t ld, int rows, int cols, int lane,
+                                                uint32_t* r) {
+        const int row = lane / kUnits, col = lane % kUnits * W;
+        const uint16_t* from = res + at + row * ld + col;
 #pragma unroll
-    for (int j = 0; j < 32; j += 4) {
-        const float4 b = *reinterpret_cast<const float4*>(bz + j);
-        float4 o = make_float4(__uint_as_float(z[j]) + b.x, __uint_as_float(z[j + 1]) + b.y,
-                               __uint_as_float(z[j + 2]) + b.z, __uint_as_float(z[j + 3]) + b.w);
-        if (kGated) {
-            const float4 c = *reinterpret_cast<const float4*>(bu + j);
-            o.x = over_one_plus_exp(o.x, o.x) * (__uint_as_float(u[j]) + c.x);
-            o.y = over_one_plus_exp(o.y, o.y) * (__uint_as_float(u[j + 1]) + c.y);
-            o.z = over_one_plus_exp(o.z, o.z) * (__uint_as_float(u[j + 2]) + c.z);
-            o.w = over_one_plus_exp(o.w, o.w) * (__uint_as_float(u[j + 3]) + c.w);
-        } else if (a.act != MXFP4_ACT_NONE) {
-            o = activate4(a.act, o, o);
-        }
-        v[j] = o.x, v[j + 1] = o.y, v[j + 2] = o.z, v[j + 3] = o.w;
-    }
-    if (whole) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            float* w = v + 8 * i;
-            if (res) {
-                const uint32_t q[4] = {r[i].x, r[i].y, r[i].z, r[i].w};
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    w[2 * k] += bf16_lo(q[k]);
-                    w[2 * k + 1] += bf16_hi(q[k]);
+        for (int i = 0; i < kIters; ++i) {
+            if (row + i * kStep < rows && col < cols) {
+                if (W == 8) {
+                    const uint4 v = *reinterpret_cast<const uint4*>(from + i * kStep * ld);
+                    r[4 * i] = v.x, r[4 * i + 1] = v.y, r[4 * i + 2] = v.z, r[4 * i + 3] = v.w;
+                } else if (W == 2) {
+                    r[i] = *reinterpret_cast<const uint32_t*>(from + i * kStep * ld);
+                } else {
+                    r[i] = from[i * kStep * ld];
                 }
             }
-            *reinterpret_cast<uint4*>(y + at + 8 * i) =
-                make_uint4(pack_bf16(w[0], w[1]), pack_bf16(w[2], w[3]), pack_bf16(w[4], w[5]), pack_bf16(w[6], w[7]));
         }
-    } else {
+    }
+    __device__ __forceinline__ static void store(uint16_t* y, int64_t at, int64_t ld, int rows, int cols, int lane,
+                                                 const float* staged, bool add, const uint32_t* r) {
+        const int row = lane / kUnits, col = lane % kUnits * W;
+        uint16_t* to = y + at + row * ld + col;
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
-            if (j < limit) {
-                float w = v[j];
-                if (res) w += __uint_as_float(static_cast<uint32_t>(res[at + j]) << 16);
-                y[at + j] = static_cast<uint16_t>(pack_bf16(w, w));
+        for (int i = 0; i < kIters; ++i) {
+            const float* z = staged + (row + i * kStep) * kPitch + col;
+            if (row + i * kStep < rows && col < cols) {
+                if (W == 8) {
+                    const float4 a = *reinterpret_cast<const float4*>(z), b = *reinterpret_cast<const float4*>(z + 4);
+                    float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+                    if (add) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            v[2 * k] += bf16_lo(r[4 * i + k]);
+                            v[2 * k + 1] += bf16_hi(r[4 * i + k]);
+                        }
+                    }
+                    *reinterpret_cast<uint4*>(to + i * kStep * ld) =
+                        make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+                } else if (W == 2) {
+                    float2 v = *reinterpret_cast<const float2*>(z);
+                    if (add) v.x += bf16_lo(r[i]), v.y += bf16_hi(r[i]);
+                    *reinterpret_cast<uint32_t*>(to + i * kStep * ld) = pack_bf16(v.x, v.y);
+                } else {
+                    const float v = add ? *z + bf16_lo(r[i]) : *z;
+                    to[i * kStep * ld] = static_cast<uint16_t>(pack_bf16(v, v));
+                }
             }
         }
+    }
+};
+
+// The epilogue of one tile by one warp: the chunks c0, c0 + 32, ... of the tile's `limit` columns.
+// base: this warp's TMEM lanes; bias: the tile's, gate then up.
+template <bool kGated, int W>
+__device__ __forceinline__ void finish_tile(const LinearArgs& a, int64_t at, int rows, int limit, int c0, int cols,
+                                            uint32_t base, const float* bias, float* staged, int lane) {
+    const uint16_t* res = static_cast<const uint16_t*>(a.residual);
+    uint16_t* y = static_cast<uint16_t*>(a.y);
+    uint32_t r[16];
+    if (res && c0 < limit) Chunk<W>::load(res, at + c0, a.n_out, rows, limit - c0, lane, r);
+#pragma unroll 1
+    for (int c = c0; c < limit; c += 32) {
+        __syncwarp();
+        uint32_t z[16], u[16];
+        tmem_ld_x16(base + c, z);
+        if (kGated) tmem_ld_x16(base + cols + c, u);
+        tmem_wait_ld();
+#pragma unroll
+        for (int j = 0; j < 16; j += 4) {
+            const float4 b = *reinterpret_cast<const float4*>(bias + c + j);
+            float4 o = make_float4(__uint_as_float(z[j]) + b.x, __uint_as_float(z[j + 1]) + b.y,
+                                   __uint_as_float(z[j + 2]) + b.z, __uint_as_float(z[j + 3]) + b.w);
+            if (kGated) {
+                const float4 d = *reinterpret_cast<const float4*>(bias + cols + c + j);
+                o.x = over_one_plus_exp(o.x, o.x) * (__uint_as_float(u[j]) + d.x);
+                o.y = over_one_plus_exp(o.y, o.y) * (__uint_as_float(u[j + 1]) + d.y);
+                o.z = over_one_plus_exp(o.z, o.z) * (__uint_as_float(u[j + 2]) + d.z);
+                o.w = over_one_plus_exp(o.w, o.w) * (__uint_as_float(u[j + 3]) + d.w);
+            } else if (a.act != MXFP4_ACT_NONE) {
+                o = activate4(a.act, o, o);
+            }
+            *reinterpret_cast<float4*>(staged + lane * kPitch + j) = o;
+        }
+        __syncwarp();
+        uint32_t next[16];
+        if (res && c + 32 < limit) Chunk<W>::load(res, at + c + 32, a.n_out, rows, limit - c - 32, lane, next);
+        Chunk<W>::store(y, at + c, a.n_out, rows, limit - c, lane, staged, res != nullptr, r);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) r[i] = next[i];
     }
 }
 
@@ -217,7 +271,7 @@ linear_many_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&accfull[b], 1);
-            mbar_init(&accempty[b], 8);
+            mbar_init(&accempty[b], 2 * kEpiWarps);
         }
         mbar_init(drain, 1);
         *s_abort = 0;
@@ -323,56 +377,32 @@ linear_many_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
         }
     } else if (warp >= 4) {
         // ---------------- epilogue: TMEM lane = token
-        const int q = warp & 3;
-        float* s_bias = reinterpret_cast<float*>(smem + Ly.bias_off) + q * 256;
+        const int q = warp & 3, w = warp - 4;
+        float* s_bias = reinterpret_cast<float*>(smem + Ly.bias_off) + w * 256;
+        float* staged = reinterpret_cast<float*>(smem + Ly.out_off) + w * 32 * kPitch;
         const uint32_t accempty0 = on_leader(accempty);
-        const bool vec = a.n_out % 8 == 0;
-        const uint16_t* res = static_cast<const uint16_t*>(a.residual);
         bool ok = true;
         for (int lt = 0; lt < walk.n && ok; ++lt) {
             const Tile t = walk.at(tiles, lt);
             const int nt = t.nt, cols = kGated ? nt / 2 : nt, b = lt & 1;
-            const int64_t m = static_cast<int64_t>(t.m) * 256 + rank * 128 + q * 32 + lane;
+            const int64_t m = static_cast<int64_t>(t.m) * 256 + rank * 128 + q * 32;
             const int64_t n0 = static_cast<int64_t>(t.f) * full_cols;
+            const int rows = static_cast<int>(max(static_cast<int64_t>(0), min(static_cast<int64_t>(32), a.M - m)));
+            const int limit = static_cast<int>(min(static_cast<int64_t>(cols), a.n_out - n0));
             __syncwarp();
             for (int j = lane; j < nt; j += 32) {
                 const int64_t n = n0 + (kGated && j >= cols ? j - cols : j);
                 s_bias[j] = n < a.n_out ? bias_at(a, kGated && j >= cols ? n + a.n_out : n) : 0.f;
             }
             __syncwarp();
-            // the residual of the next 32 columns is on its way while these are finished
-            uint4 r[2][4];
-            const int64_t at0 = m * a.n_out + n0;
-            const int limit = static_cast<int>(min(static_cast<int64_t>(cols), a.n_out - n0));
-            auto load_res = [&](int c, uint4* to) {
-                if (res && vec && m < a.M && c + 32 <= limit) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) to[i] = *reinterpret_cast<const uint4*>(res + at0 + c + 8 * i);
-                }
-            };
-            load_res(0, r[0]);
             if (!__all_sync(0xFFFFFFFFu, mbar_wait(&accfull[b], (lt >> 1) & 1, s_abort))) { ok = false; break; }
             tc_fence_after();
             const uint32_t base = tmem + (static_cast<uint32_t>(q * 32) << 16) + b * 256;
-            auto finish = [&](int c, const uint4* rr) {
-                __syncwarp();
-                uint32_t z[32], u[32];
-                tmem_ld_x32(base + c, z);
-                if (kGated) tmem_ld_x32(base + cols + c, u);
-                tmem_wait_ld();
-                if (m < a.M)
-                    finish32<kGated>(a, at0 + c, limit - c, vec && c + 32 <= limit, rr, z, u, s_bias + c,
-                                     s_bias + (kGated ? cols : 0) + c);
-            };
-#pragma unroll 1
-            for (int c = 0; c < limit; c += 64) {
-                load_res(c + 32, r[1]);
-                finish(c, r[0]);
-                if (c + 32 < limit) {
-                    load_res(c + 64, r[0]);
-                    finish(c + 32, r[1]);
-                }
-            }
+            const int64_t at = m * a.n_out + n0;
+            const int c0 = 16 * (w >> 2);
+            if (a.n_out % 8 == 0) finish_tile<kGated, 8>(a, at, rows, limit, c0, cols, base, s_bias, staged, lane);
+            else if (a.n_out % 2 == 0) finish_tile<kGated, 2>(a, at, rows, limit, c0, cols, base, s_bias, staged, lane);
+            else finish_tile<kGated, 1>(a, at, rows, limit, c0, cols, base, s_bias, staged, lane);
             tc_fence_before();
             __syncwarp();
             if (lane == 0) arrive_cluster(accempty0 + 8 * b);
