@@ -36,6 +36,7 @@ using namespace linear;
 
 constexpr int kThreads = 384;
 constexpr int kEpiWarps = 8;
+constexpr int kStaged = 16;                    // rows of a chunk staged at a time
 constexpr int kPitch = 20;                     // floats per row of a staged chunk: 16 and a conflict-free stride
 constexpr int kBK = 128;                       // K per stage: two tiles of 64 (128 bytes per row)
 constexpr int kXTile = 128 * 64 * 2;           // A rows of one CTA, 64 of K
@@ -50,12 +51,12 @@ struct Layout {
 __host__ __device__ inline Layout make_layout(int nt) {
     Layout L;
     L.stage_bytes = 2 * (kXTile + nt / 2 * 64 * 2);
-    const int fixed = kEpiWarps * (256 + 32 * kPitch) * 4 + kBars * 8 + 16 + 1024;
+    const int fixed = kEpiWarps * (128 + kStaged * kPitch) * 4 + kBars * 8 + 16 + 1024;
     L.stages = (kSmemLimit - fixed) / L.stage_bytes;
     if (L.stages > kMaxStages) L.stages = kMaxStages;
     L.bias_off = L.stages * L.stage_bytes;
-    L.out_off = L.bias_off + kEpiWarps * 256 * 4;          // per epilogue warp: the tile's bias,
-    L.bar_off = L.out_off + kEpiWarps * 32 * kPitch * 4;   // and a chunk of 32 rows
+    L.out_off = L.bias_off + kEpiWarps * 128 * 4;          // per epilogue warp: its columns' bias,
+    L.bar_off = L.out_off + kEpiWarps * kStaged * kPitch * 4;   // and half a chunk's rows
     L.misc_off = L.bar_off + kBars * 8;
     L.total = L.misc_off + 16 + 1024;          // + slack for the 1024-B alignment of the base
     return L;
@@ -165,33 +166,35 @@ struct Chunk {
             }
         }
     }
-    __device__ __forceinline__ static void store(uint16_t* y, int64_t at, int64_t ld, int rows, int cols, int lane,
+    // rows 16 half .. 16 half + 15 of the chunk, which are the ones staged
+    __device__ __forceinline__ static void store(uint16_t* y, int64_t at, int64_t ld, int rows, int cols, int lane, int half,
                                                  const float* staged, bool add, const uint32_t* r) {
         const int row = lane / kUnits, col = lane % kUnits * W;
-        uint16_t* to = y + at + row * ld + col;
+        uint16_t* to = y + at + (16 * half + row) * ld + col;
 #pragma unroll
-        for (int i = 0; i < kIters; ++i) {
-            const float* z = staged + (row + i * kStep) * kPitch + col;
-            if (row + i * kStep < rows && col < cols) {
+        for (int k = 0; k < kIters / 2; ++k) {
+            const float* z = staged + (row + k * kStep) * kPitch + col;
+            if (16 * half + row + k * kStep < rows && col < cols) {
+                const int i = half * (kIters / 2) + k;
                 if (W == 8) {
                     const float4 a = *reinterpret_cast<const float4*>(z), b = *reinterpret_cast<const float4*>(z + 4);
                     float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
                     if (add) {
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            v[2 * k] += bf16_lo(r[4 * i + k]);
-                            v[2 * k + 1] += bf16_hi(r[4 * i + k]);
+                        for (int x = 0; x < 4; ++x) {
+                            v[2 * x] += bf16_lo(r[4 * i + x]);
+                            v[2 * x + 1] += bf16_hi(r[4 * i + x]);
                         }
                     }
-                    *reinterpret_cast<uint4*>(to + i * kStep * ld) =
+                    *reinterpret_cast<uint4*>(to + k * kStep * ld) =
                         make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
                 } else if (W == 2) {
                     float2 v = *reinterpret_cast<const float2*>(z);
                     if (add) v.x += bf16_lo(r[i]), v.y += bf16_hi(r[i]);
-                    *reinterpret_cast<uint32_t*>(to + i * kStep * ld) = pack_bf16(v.x, v.y);
+                    *reinterpret_cast<uint32_t*>(to + k * kStep * ld) = pack_bf16(v.x, v.y);
                 } else {
                     const float v = add ? *z + bf16_lo(r[i]) : *z;
-                    to[i * kStep * ld] = static_cast<uint16_t>(pack_bf16(v, v));
+                    to[k * kStep * ld] = static_cast<uint16_t>(pack_bf16(v, v));
                 }
             }
         }
@@ -199,7 +202,7 @@ struct Chunk {
 };
 
 // The epilogue of one tile by one warp: the chunks c0, c0 + 32, ... of the tile's `limit` columns.
-// base: this warp's TMEM lanes; bias: the tile's, gate then up.
+// base: this warp's TMEM lanes; bias: its chunks' (gated: the up's from 64 on).
 template <bool kGated, int W>
 __device__ __forceinline__ void finish_tile(const LinearArgs& a, int64_t at, int rows, int limit, int c0, int cols,
                                             uint32_t base, const float* bias, float* staged, int lane) {
@@ -209,18 +212,18 @@ __device__ __forceinline__ void finish_tile(const LinearArgs& a, int64_t at, int
     if (res && c0 < limit) Chunk<W>::load(res, at + c0, a.n_out, rows, limit - c0, lane, r);
 #pragma unroll 1
     for (int c = c0; c < limit; c += 32) {
-        __syncwarp();
         uint32_t z[16], u[16];
         tmem_ld_x16(base + c, z);
         if (kGated) tmem_ld_x16(base + cols + c, u);
         tmem_wait_ld();
+        float4 v[4];
 #pragma unroll
         for (int j = 0; j < 16; j += 4) {
-            const float4 b = *reinterpret_cast<const float4*>(bias + c + j);
+            const float4 b = *reinterpret_cast<const float4*>(bias + (c - c0) / 2 + j);
             float4 o = make_float4(__uint_as_float(z[j]) + b.x, __uint_as_float(z[j + 1]) + b.y,
                                    __uint_as_float(z[j + 2]) + b.z, __uint_as_float(z[j + 3]) + b.w);
             if (kGated) {
-                const float4 d = *reinterpret_cast<const float4*>(bias + cols + c + j);
+                const float4 d = *reinterpret_cast<const float4*>(bias + 64 + (c - c0) / 2 + j);
                 o.x = over_one_plus_exp(o.x, o.x) * (__uint_as_float(u[j]) + d.x);
                 o.y = over_one_plus_exp(o.y, o.y) * (__uint_as_float(u[j + 1]) + d.y);
                 o.z = over_one_plus_exp(o.z, o.z) * (__uint_as_float(u[j + 2]) + d.z);
@@ -228,12 +231,20 @@ __device__ __forceinline__ void finish_tile(const LinearArgs& a, int64_t at, int
             } else if (a.act != MXFP4_ACT_NONE) {
                 o = activate4(a.act, o, o);
             }
-            *reinterpret_cast<float4*>(staged + lane * kPitch + j) = o;
+            v[j / 4] = o;
         }
-        __syncwarp();
         uint32_t next[16];
         if (res && c + 32 < limit) Chunk<W>::load(res, at + c + 32, a.n_out, rows, limit - c - 32, lane, next);
-        Chunk<W>::store(y, at + c, a.n_out, rows, limit - c, lane, staged, res != nullptr, r);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            if (lane / 16 == half) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) *reinterpret_cast<float4*>(staged + (lane & 15) * kPitch + 4 * j) = v[j];
+            }
+            __syncwarp();
+            Chunk<W>::store(y, at + c, a.n_out, rows, limit - c, lane, half, staged, res != nullptr, r);
+            __syncwarp();
+        }
 #pragma unroll
         for (int i = 0; i < 16; ++i) r[i] = next[i];
     }
@@ -378,8 +389,8 @@ linear_many_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
     } else if (warp >= 4) {
         // ---------------- epilogue: TMEM lane = token
         const int q = warp & 3, w = warp - 4;
-        float* s_bias = reinterpret_cast<float*>(smem + Ly.bias_off) + w * 256;
-        float* staged = reinterpret_cast<float*>(smem + Ly.out_off) + w * 32 * kPitch;
+        float* s_bias = reinterpret_cast<float*>(smem + Ly.bias_off) + w * 128;
+        float* staged = reinterpret_cast<float*>(smem + Ly.out_off) + w * kStaged * kPitch;
         const uint32_t accempty0 = on_leader(accempty);
         bool ok = true;
         for (int lt = 0; lt < walk.n && ok; ++lt) {
@@ -388,18 +399,18 @@ linear_many_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_cons
             const int64_t m = static_cast<int64_t>(t.m) * 256 + rank * 128 + q * 32;
             const int64_t n0 = static_cast<int64_t>(t.f) * full_cols;
             const int rows = static_cast<int>(max(static_cast<int64_t>(0), min(static_cast<int64_t>(32), a.M - m)));
-            const int limit = static_cast<int>(min(static_cast<int64_t>(cols), a.n_out - n0));
+            const int limit = static_cast<int>(min(static_cast<int64_t>(cols), a.n_out - n0)), c0 = 16 * (w >> 2);
             __syncwarp();
-            for (int j = lane; j < nt; j += 32) {
-                const int64_t n = n0 + (kGated && j >= cols ? j - cols : j);
-                s_bias[j] = n < a.n_out ? bias_at(a, kGated && j >= cols ? n + a.n_out : n) : 0.f;
+            // the bias of the warp's chunks, 16 values each; gated: the gate's, then at 64 the up's
+            for (int x = lane; x < 128; x += 32) {
+                const int col = c0 + (kGated ? x & 63 : x) / 16 * 32 + x % 16;
+                s_bias[x] = col < limit ? bias_at(a, n0 + col + (kGated && x >= 64 ? a.n_out : 0)) : 0.f;
             }
             __syncwarp();
             if (!__all_sync(0xFFFFFFFFu, mbar_wait(&accfull[b], (lt >> 1) & 1, s_abort))) { ok = false; break; }
             tc_fence_after();
             const uint32_t base = tmem + (static_cast<uint32_t>(q * 32) << 16) + b * 256;
             const int64_t at = m * a.n_out + n0;
-            const int c0 = 16 * (w >> 2);
             if (a.n_out % 8 == 0) finish_tile<kGated, 8>(a, at, rows, limit, c0, cols, base, s_bias, staged, lane);
             else if (a.n_out % 2 == 0) finish_tile<kGated, 2>(a, at, rows, limit, c0, cols, base, s_bias, staged, lane);
             else finish_tile<kGated, 1>(a, at, rows, limit, c0, cols, base, s_bias, staged, lane);
