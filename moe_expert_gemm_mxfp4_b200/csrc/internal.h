@@ -45,8 +45,10 @@ struct RouteScoredArgs {
     int E, top_k, score, n_groups, top_groups, group_top, renorm;
     int by_logit;              // the choice goes by the logits (no bias, no sums of scores)
     float scale;
-    int group_size, seg_log2;  // set by the launch: experts per group, lanes per group (2^seg_log2),
-    int64_t chunk;             // tokens per CTA
+    // set by the launch: experts per group, lanes per group (2^seg_log2), experts per lane, whether those
+    // are aligned vectors; tokens per CTA
+    int group_size, seg_log2, per, vec;
+    int64_t chunk;
 };
 
 // Arguments of the linear layer (see linear_few.cu, linear_many.cu).

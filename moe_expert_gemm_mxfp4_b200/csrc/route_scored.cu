@@ -60,22 +60,54 @@ __device__ __forceinline__ float load_logit(const void* p, int64_t i) {
     return kBf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]) : static_cast<const float*>(p)[i];
 }
 
-// Where expert items live in a warp: lanes in segments of `seg` (a power of two) per
-// group; item i of lane r of the segment is expert r + seg * i of the group.
+// Where expert items live in a warp: 2^seg_log2 lanes per group, `per` consecutive experts of it
+// per lane (fewer, or none, at the group's end).
 struct Lanes {
-    int g, r, seg, base, size;   // base: the lane's first expert; size: a group's experts
-    bool on;
+    int g, base, n;   // the lane's group, first expert and number of experts
     __device__ __forceinline__ Lanes(const RouteScoredArgs& a, int lane) {
-        seg = 1 << a.seg_log2;
-        size = a.group_size;
         g = lane >> a.seg_log2;
-        r = lane & (seg - 1);
-        base = g * size + r;
-        on = g < a.n_groups;
+        const int first = (lane & ((1 << a.seg_log2) - 1)) * a.per;
+        base = g * a.group_size + first;
+        n = g < a.n_groups ? max(0, min(a.per, a.group_size - first)) : 0;
     }
-    __device__ __forceinline__ bool has(int i) const { return on && r + seg * i < size; }
-    __device__ __forceinline__ int expert(int i) const { return base + seg * i; }
+    __device__ __forceinline__ bool has(int i) const { return i < n; }
+    __device__ __forceinline__ int expert(int i) const { return base + i; }
 };
+
+// The lane's values of a row of logits (or of the bias); -inf past its experts.  vec: every lane has NI or
+// none, and they are aligned vectors.
+template <bool kBf16, int NI>
+__device__ __forceinline__ void load_items(const void* row, int64_t at, int n, bool vec, float* c) {
+    constexpr int kBytes = NI * (kBf16 ? 2 : 4);
+    uint32_t w[kBytes >= 4 ? kBytes / 4 : 1];
+    if (NI > 1 && vec) {
+        const char* p = static_cast<const char*>(row) + at * (kBf16 ? 2 : 4);
+#pragma unroll
+        for (int i = 0; i < kBytes / 4; ++i) w[i] = 0xFF80FF80u;
+        if (n > 0) {
+            if (kBytes >= 16) {
+#pragma unroll
+                for (int i = 0; i < kBytes / 16; ++i) {
+                    const uint4 v = __ldg(reinterpret_cast<const uint4*>(p) + i);
+                    w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
+                }
+            } else if (kBytes == 8) {
+                const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
+                w[0] = v.x, w[kBytes >= 8 ? 1 : 0] = v.y;
+            } else {
+                w[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+            if (kBf16) c[i] = __uint_as_float(i & 1 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
+            else c[i] = n > 0 ? __uint_as_float(w[i]) : -INFINITY;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < NI; ++i) c[i] = i < n ? load_logit<kBf16>(row, at + i) : -INFINITY;
+    }
+}
 
 // 64-bit arithmetic in few instructions: a launch meets this code once, cold, and fetching the
 // library functions' took longer than running them (a token in 64 bits cost 10 us).
@@ -161,7 +193,7 @@ __device__ __noinline__ int group_rank64(const RouteScoredArgs& a, int64_t t, in
     }
     __syncwarp();
 #pragma unroll 1
-    for (int o = L.seg >> 1; o > 0; o >>= 1) {
+    for (int o = (1 << a.seg_log2) >> 1; o > 0; o >>= 1) {
         const double u1 = __shfl_xor_sync(kFull, t1, o), u2 = __shfl_xor_sync(kFull, t2, o);
         t2 = fmax(fmin(t1, u1), fmax(t2, u2));
         t1 = fmax(t1, u1);
@@ -311,13 +343,13 @@ template <bool kBf16, int NI>
 __device__ __forceinline__ int choose(const RouteScoredArgs& a, const Steps& st, int64_t t, int lane, float* m_out,
                                       float* sum_out) {
     const Lanes L(a, lane);
-    const int64_t row = t * a.E + L.base;
-    float c[NI];
+    float c[NI], b[NI];
+    load_items<kBf16, NI>(a.logits, t * a.E + L.base, L.n, a.vec, c);
+    if (a.bias) load_items<false, NI>(a.bias, L.base, L.n, a.vec, b);
+    else {
 #pragma unroll
-    for (int i = 0; i < NI; ++i) c[i] = L.has(i) ? load_logit<kBf16>(a.logits, row + L.seg * i) : -INFINITY;
-    float b[NI];
-#pragma unroll
-    for (int i = 0; i < NI; ++i) b[i] = a.bias && L.has(i) ? __ldg(a.bias + L.base + L.seg * i) : 0.f;
+        for (int i = 0; i < NI; ++i) b[i] = 0.f;
+    }
     // Two exact c further apart than err keep their order in fp32.  With d = l - m: exp's argument
     // is rounded (|d| 2^-23.4 of the result) and ex2 is off by 2^-22, so e^d by at most 2^-21.5
     // absolutely; the sum of at most 21 rounded additions and the quotient keep s within 2^-18 of
@@ -355,7 +387,7 @@ __device__ __forceinline__ int choose(const RouteScoredArgs& a, const Steps& st,
     }
     const bool exact = kBf16 && a.by_logit;
     bool close = false;   // fp32 does not tell
-    bool on = L.on;
+    bool on = true;       // the lane's group is kept
     if (a.top_groups < a.n_groups) {
         float t1 = -INFINITY, t2 = -INFINITY;
 #pragma unroll
@@ -363,34 +395,38 @@ __device__ __forceinline__ int choose(const RouteScoredArgs& a, const Steps& st,
             t2 = fmaxf(t2, fminf(t1, c[i]));
             t1 = fmaxf(t1, c[i]);
         }
-        for (int o = L.seg >> 1; o > 0; o >>= 1) {
+        for (int o = (1 << a.seg_log2) >> 1; o > 0; o >>= 1) {
             const float u1 = __shfl_xor_sync(kFull, t1, o), u2 = __shfl_xor_sync(kFull, t2, o);
             t2 = fmaxf(fminf(t1, u1), fmaxf(t2, u2));
             t1 = fmaxf(t1, u1);
         }
         const float second = a.group_top == 2 && t2 != -INFINITY ? t2 : 0.f;
-        const float v = t1 + second;
-        int rank = 0;
-#pragma unroll 4
-        for (int g = 0; g < a.n_groups; ++g) {
-            const float u = __shfl_sync(kFull, v, g << a.seg_log2);
-            rank += u > v || (u == v && g < L.g);
+        const bool real = L.g < a.n_groups;
+        uint32_t left = real ? order_key32(t1 + second) : 0u;   // 0 once the group is kept
+        uint32_t last = 0;
+        bool won = false;
+#pragma unroll 1
+        for (int j = 0; j < a.top_groups; ++j) {   // the best of those left, the first of equals
+            last = __reduce_max_sync(kFull, left);
+            const int first = __ffs(static_cast<int>(__ballot_sync(kFull, left == last))) - 1;
+            won = L.g == first >> a.seg_log2;
+            if (won) left = 0u;
         }
+        on = left == 0u;
         if (!exact) {   // the last group kept and the first left out
-            const bool kept = on && rank == a.top_groups - 1, edge = kept || (on && rank == a.top_groups);
-            const float x = order_value32(__reduce_max_sync(kFull, kept ? order_key32(v) : 0u));
-            const float y = order_value32(__reduce_max_sync(kFull, edge && !kept ? order_key32(v) : 0u));
-            const float big = edge ? fmaxf(fabsf(t1), fabsf(second)) : 0.f;
-            const bool near = edge && y > -INFINITY && !(x - y > 2.f * err + 0x1p-21f * big);
-            if (__any_sync(kFull, near)) rank = group_rank64<kBf16>(a, t, lane);
+            const uint32_t out = __reduce_max_sync(kFull, left);
+            const float x = order_value32(last), y = order_value32(out);
+            const float big = real && (won || left == out) ? fmaxf(fabsf(t1), fabsf(second)) : 0.f;
+            const bool near = y > -INFINITY && !(x - y > 2.f * err + 0x1p-21f * big);
+            if (__any_sync(kFull, near)) on = group_rank64<kBf16>(a, t, lane) < a.top_groups;
         }
-        on = on && rank < a.top_groups;
     }
     uint32_t key[NI], near = 0;   // near: keys of neighbours no further apart are close
+    const int n = on ? L.n : 0;
+    const uint32_t id0 = static_cast<uint32_t>(255 - L.base);
     if (exact) {
 #pragma unroll
-        for (int i = 0; i < NI; ++i)
-            key[i] = on && L.has(i) ? max(order_key32(c[i]) >> 16, 1u) << 8 | static_cast<uint32_t>(255 - L.expert(i)) : 0u;
+        for (int i = 0; i < NI; ++i) key[i] = i < n ? (max(order_key32(c[i]) >> 16, 1u) << 8) + (id0 - i) : 0u;
     } else {
         float lo = st.lo, scale = st.scale;
         if (a.by_logit) {
@@ -407,15 +443,13 @@ __device__ __forceinline__ int choose(const RouteScoredArgs& a, const Steps& st,
         } else {
             near = static_cast<uint32_t>(fminf(err * scale, 0x1p24f) + st.near);
         }
-        float all = 0.f;
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
-            // masked experts below all others, among themselves by id
-            const uint32_t q = c[i] == -INFINITY ? 1u : 4u + static_cast<uint32_t>((c[i] - lo) * scale);
-            key[i] = on && L.has(i) ? q << 8 | static_cast<uint32_t>(255 - L.expert(i)) : 0u;
-            all += c[i] == -INFINITY ? 0.f : c[i];
+            close |= !(c[i] < 0x1p127f);   // NaN or (nearly) infinite
+            // -inf becomes 0, as close to the smallest: masked experts are ordered in 64 bits
+            const uint32_t q = 4u + static_cast<uint32_t>((c[i] - lo) * scale);
+            key[i] = i < n ? (q << 8) + (id0 - i) : 0u;
         }
-        close |= !(fabsf(all) < INFINITY);   // NaN or an infinity, or sums past fp32's range
     }
     sort_descending<NI>(key);
     uint32_t got = 0, top = 0;   // lane j: the j-th best
@@ -434,7 +468,7 @@ __device__ __forceinline__ int choose(const RouteScoredArgs& a, const Steps& st,
     if (!exact) {
         if (__any_sync(kFull, close)) return choose64<kBf16>(a, t, lane, on);
         const uint32_t prev = __shfl_up_sync(kFull, got, 1);
-        const bool tie = lane > 0 && got >= 4u << 8 && (prev >> 8) - (got >> 8) <= near;   // got is 0 past the rounds
+        const bool tie = lane > 0 && got != 0u && (prev >> 8) - (got >> 8) <= near;   // got is 0 past the rounds
         const uint32_t ties = __ballot_sync(kFull, tie);
         if (ties) {
             int n = a.top_k;
@@ -442,7 +476,7 @@ __device__ __forceinline__ int choose(const RouteScoredArgs& a, const Steps& st,
                 uint32_t last = top;
                 for (++n; n < 32; ++n) {
                     next();
-                    if (top < 4u << 8 || (last >> 8) - (top >> 8) > near) break;
+                    if (top == 0u || (last >> 8) - (top >> 8) > near) break;
                     if (lane == n) got = top;
                     last = top;
                 }
@@ -457,33 +491,29 @@ __device__ __forceinline__ int choose(const RouteScoredArgs& a, const Steps& st,
 // log of the smallest 64-bit number, 2^-1074, less half a step: scores below it are 0
 constexpr float kLogTiny = -745.13f;
 
-// Slot j's weight on lane j < top_k, from its logit l.  Renormalised weights are taken
-// relative to the largest chosen logit, so that rows of very small scores keep their
-// precision.  A score that is 0 in 64 bits weighs 0 (l = -inf, or a mask of the type's
-// lowest value), and so does every slot of a token whose chosen scores are all 0.
+// Slot j's weight on lane j < top_k, from its logit l.  A score that is 0 in 64 bits weighs 0 (l = -inf, or
+// a mask of the type's lowest value), and so does every slot of a token whose chosen scores are all 0.
 __device__ __forceinline__ float slot_weight(const RouteScoredArgs& a, float l, bool on, float m, float sum) {
     const bool soft = a.score == MXFP4_SCORE_SOFTMAX;
-    if (!a.renorm) {
-        const float w = soft ? (l == m ? 1.f : expf(l - m)) / sum : 1.f / (1.f + expf(-l));
-        return on && l != -INFINITY ? w * a.scale : 0.f;
-    }
-    float top = on && l == l ? l : -INFINITY;
-#pragma unroll
-    for (int o = 4; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
-    top = __shfl_sync(kFull, top, 0);
-    // e^(l - top), of which a sigmoid is e^top / (1 + e^l) times; above 0 the sigmoid itself
-    const float d = !soft && top >= 0.f ? -l : l == top ? 0.f : l - top;
-    float w = expf(d);
-    if (!soft) {
-        if (top >= 0.f) w = __fdividef(1.f, 1.f + w);
-        else w = __fdividef(w, 1.f + expf(l));
-    }
-    // (where the logits order the choice, the row's largest is among the chosen)
-    const float ref = !soft ? 0.f : a.by_logit ? top : m;
-    if (!on || l == -INFINITY || l - ref < kLogTiny) w = 0.f;
+    // (where the logits order the choice, the first chosen is the row's largest)
+    if (soft && a.by_logit && a.renorm) m = __shfl_sync(kFull, l, 0);
+    float w = soft ? (l == m ? 1.f : expf(l - m)) : __fdividef(1.f, 1.f + expf(-l));
+    if (!on || l == -INFINITY) w = 0.f;
+    if (!a.renorm) return w == 0.f ? 0.f : w * (soft ? a.scale / sum : a.scale);   // (sum is 0 where all are masked)
     float s = w;
 #pragma unroll
     for (int o = 4; o > 0; o >>= 1) s += __shfl_xor_sync(kFull, s, o);
+    s = __shfl_sync(kFull, s, 0);
+    if (s < 0x1p-60f) {   // scores so small that they lose bits (or are all 0): relative to the largest chosen
+        float top = on && l == l ? l : -INFINITY;
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
+        w = l == top ? 1.f : expf(l - top);       // a sigmoid far below 0 is e^l
+        if (!on || l == -INFINITY || l - (soft ? m : 0.f) < kLogTiny) w = 0.f;
+        s = w;
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1) s += __shfl_xor_sync(kFull, s, o);
+    }
     return s == 0.f ? 0.f : w / s * a.scale;
 }
 
@@ -773,13 +803,18 @@ cudaError_t launch_route_scored(RouteScoredArgs a, bool bf16, cudaStream_t strea
     a.group_size = a.E / a.n_groups;
     a.seg_log2 = 5;
     while ((32 >> a.seg_log2) < a.n_groups) --a.seg_log2;
+    a.per = (a.group_size + (1 << a.seg_log2) - 1) >> a.seg_log2;
     // items per lane: at most 8 where n_groups is a power of two, else at most 16
-    const int seg = 1 << a.seg_log2, items = (a.group_size + seg - 1) / seg;
-    if (items <= 1) return bf16 ? launch<true, 1>(a, stream) : launch<false, 1>(a, stream);
-    if (items <= 2) return bf16 ? launch<true, 2>(a, stream) : launch<false, 2>(a, stream);
-    if (items <= 4) return bf16 ? launch<true, 4>(a, stream) : launch<false, 4>(a, stream);
-    if (items <= 8) return bf16 ? launch<true, 8>(a, stream) : launch<false, 8>(a, stream);
-    return bf16 ? launch<true, 16>(a, stream) : launch<false, 16>(a, stream);
+    const int ni = a.per <= 1 ? 1 : a.per <= 2 ? 2 : a.per <= 4 ? 4 : a.per <= 8 ? 8 : 16;
+    const int wide = bf16 ? (ni < 8 ? ni : 8) : (ni < 4 ? ni : 4);   // elements of a lane's vector loads
+    a.vec = a.per == ni && a.group_size % ni == 0 && a.E % wide == 0;
+    switch (ni) {
+        case 1: return bf16 ? launch<true, 1>(a, stream) : launch<false, 1>(a, stream);
+        case 2: return bf16 ? launch<true, 2>(a, stream) : launch<false, 2>(a, stream);
+        case 4: return bf16 ? launch<true, 4>(a, stream) : launch<false, 4>(a, stream);
+        case 8: return bf16 ? launch<true, 8>(a, stream) : launch<false, 8>(a, stream);
+        default: return bf16 ? launch<true, 16>(a, stream) : launch<false, 16>(a, stream);
+    }
 }
 
 }  // namespace mx
