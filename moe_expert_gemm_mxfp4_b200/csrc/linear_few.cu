@@ -697,8 +697,10 @@ template <bool kGated, int SPLIT, bool kOwn>
 cudaError_t product(const CUtensorMap& tmap_codes, const LinearArgs& a, const Plan& p, const uint8_t* ws_b,
                     const uint8_t* ws_sfa, cudaStream_t stream, bool launch, int* clusters) {
     auto kern = linear_few_kernel<kGated, SPLIT, kOwn>;
-    const int part = (p.mp + 15) / 16 * 16 * kBM * 4, ring = p.stages * p.stage_bytes + p.slots * kCodeBytes;
-    const int smem = (ring > part ? ring : part) + 1024;
+    static_assert(kMaxMp * kBM * 4 + 1024 <= kSmemLimit - 512, "the partial sums fit");
+    // All of the SM's shared memory, whatever the rings take: a CTA waits for its cluster while it holds
+    // TMEM, so it must not share the SM with a CTA of another cluster that may wait for TMEM.
+    const int smem = kSmemLimit - 512;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};

@@ -58,7 +58,9 @@ __host__ __device__ inline Layout make_layout(int nt) {
     L.out_off = L.bias_off + kEpiWarps * 128 * 4;          // per epilogue warp: its columns' bias,
     L.bar_off = L.out_off + kEpiWarps * kStaged * kPitch * 4;   // and half a chunk's rows
     L.misc_off = L.bar_off + kBars * 8;
-    L.total = L.misc_off + 16 + 1024;          // + slack for the 1024-B alignment of the base
+    // All of the SM's shared memory, whatever the ring takes: a CTA waits for its pair while it holds
+    // TMEM, so it must not share the SM with a CTA of another cluster that may wait for TMEM.
+    L.total = kSmemLimit;
     return L;
 }
 

@@ -115,19 +115,31 @@ __device__ __forceinline__ void load_items(const void* row, int64_t at, int n, b
 __device__ __constant__ double kInvFact[14] = {1.0, 1.0, 1.0 / 2, 1.0 / 6, 1.0 / 24, 1.0 / 120, 1.0 / 720, 1.0 / 5040,
                                                1.0 / 40320, 1.0 / 362880, 1.0 / 3628800, 1.0 / 39916800,
                                                1.0 / 479001600, 1.0 / 6227020800.0};
-// e^x for x <= 0: x = n ln 2 + r, |r| <= 0.35, Taylor's series of e^r (the term after the last is
-// below 2^-57), ln 2 in two parts of which n times the first is exact (Cody and Waite).
-__device__ __forceinline__ double exp_neg(double x) {
-    if (x < -745.2) return 0.0;
-    const double n = rint(x * 1.4426950408889634);
-    double r = fma(n, -0x1.62e42fefp-1, x);
-    r = fma(n, -0x1.473de6af278edp-34, r);
-    double p = kInvFact[13];
+// y <- e^x for V values x <= 0 at a time (they hide each other's latency): x = n ln 2 + r, |r| <= 0.35,
+// Taylor's series of e^r (the term after the last is below 2^-57), ln 2 in two parts of which n
+// times the first is exact (Cody and Waite).
+template <int V>
+__device__ __forceinline__ void exp_neg(double* x) {
+    double n[V], p[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        x[v] = fmax(x[v], -800.0);       // 0 from -745.2 on
+        n[v] = rint(x[v] * 1.4426950408889634);
+        x[v] = fma(n[v], -0x1.62e42fefp-1, x[v]);
+        x[v] = fma(n[v], -0x1.473de6af278edp-34, x[v]);
+        p[v] = kInvFact[13];
+    }
 #pragma unroll 1
-    for (int k = 12; k >= 0; --k) p = fma(p, r, kInvFact[k]);
-    const int e = static_cast<int>(n), h = e / 2;      // 2^e in two factors: e reaches -1075
-    return p * __longlong_as_double(static_cast<int64_t>(1023 + h) << 52) *
-           __longlong_as_double(static_cast<int64_t>(1023 + e - h) << 52);
+    for (int k = 12; k >= 0; --k) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) p[v] = fma(p[v], x[v], kInvFact[k]);
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const int e = static_cast<int>(n[v]), h = e / 2;      // 2^e in two factors: e reaches -1155
+        x[v] = p[v] * __longlong_as_double(static_cast<int64_t>(1023 + h) << 52) *
+               __longlong_as_double(static_cast<int64_t>(1023 + e - h) << 52);
+    }
 }
 // 1 / x for x >= 1 in fp32's range: Newton's steps double the digits of the hardware's reciprocal.
 __device__ __forceinline__ double inv64(double x) {
@@ -136,14 +148,9 @@ __device__ __forceinline__ double inv64(double x) {
     for (int i = 0; i < 2; ++i) y = fma(y, fma(-x, y, 1.0), y);
     return y;
 }
-__device__ __forceinline__ double sigmoid64(float l) {
-    const double t = exp_neg(-fabs(static_cast<double>(l))), y = inv64(1.0 + t);
-    return l < 0.f ? t * y : y;
-}
-// e^(l - m) for the row's largest logit m, which may be infinite (then 1 at each that is m).
-__device__ __forceinline__ double exp_below(float l, float m) {
-    return l == -INFINITY ? 0.0 : l == m ? 1.0 : l != l ? static_cast<double>(l) : exp_neg(static_cast<double>(l) - m);
-}
+// What is raised to the power e for e^(l - m), m the row's largest logit, which may be infinite (then 0 at
+// each that is m); NaN stays.
+__device__ __forceinline__ double below(float l, float m) { return l == m ? 0.0 : static_cast<double>(l) - m; }
 
 // What a softmax score needs of its row, in 64 bits.
 struct Row64 {
@@ -158,9 +165,18 @@ __device__ __forceinline__ Row64 row64(const RouteScoredArgs& a, int64_t row, in
     r.m = order_value32(__reduce_max_sync(kFull, order_key32(r.m)));
     double sum = 0.0;
 #pragma unroll 1
-    for (int e = lane; e < a.E; e += 32) {
-        const double z = exp_below(load_logit<kBf16>(a.logits, row + e), r.m);
-        sum += z == z ? z : 0.0;
+    for (int e = lane; e < a.E; e += 2 * 32) {
+        double z[2];
+        bool in[2];
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+            const float l = e + 32 * v < a.E ? load_logit<kBf16>(a.logits, row + e + 32 * v) : -INFINITY;
+            in[v] = l > -INFINITY;       // neither masked nor NaN
+            z[v] = in[v] ? below(l, r.m) : 0.0;
+        }
+        exp_neg<2>(z);
+#pragma unroll
+        for (int v = 0; v < 2; ++v) sum += in[v] ? z[v] : 0.0;
     }
     __syncwarp();
 #pragma unroll 1
@@ -168,12 +184,29 @@ __device__ __forceinline__ Row64 row64(const RouteScoredArgs& a, int64_t row, in
     if (sum > 0.0) r.scale = inv64(sum);   // at least 1 then
     return r;
 }
-// c of expert e, whose logit is l.
-__device__ __forceinline__ double choice64(const RouteScoredArgs& a, const Row64& r, float l, int e) {
-    if (a.by_logit) return l;
-    if (l == -INFINITY) return l;
-    const double s = a.score == MXFP4_SCORE_SOFTMAX ? exp_below(l, r.m) * r.scale : sigmoid64(l);
-    return s + (a.bias ? a.bias[e] : 0.f);
+// c of V experts e with logits l.
+template <int V>
+__device__ __forceinline__ void choice64(const RouteScoredArgs& a, const Row64& r, const float* l, const int* e, double* c) {
+    if (a.by_logit) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) c[v] = l[v];
+        return;
+    }
+    const bool soft = a.score == MXFP4_SCORE_SOFTMAX;
+#pragma unroll
+    for (int v = 0; v < V; ++v) c[v] = soft ? below(l[v], r.m) : -fabs(static_cast<double>(l[v]));
+    exp_neg<V>(c);
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        if (soft) {
+            c[v] *= r.scale;
+        } else {   // t = e^-|l|: 1 / (1 + t), or t / (1 + t) below 0
+            const double y = inv64(1.0 + c[v]);
+            c[v] = l[v] < 0.f ? c[v] * y : y;
+        }
+        if (a.bias) c[v] += a.bias[e[v]];
+        if (l[v] == -INFINITY || l[v] != l[v]) c[v] = l[v];
+    }
 }
 
 // The place of this lane's group among the groups, in 64 bits.
@@ -185,11 +218,21 @@ __device__ __noinline__ int group_rank64(const RouteScoredArgs& a, int64_t t, in
     const double ninf = -static_cast<double>(INFINITY);
     double t1 = ninf, t2 = ninf;
 #pragma unroll 1
-    for (int i = 0; L.has(i); ++i) {
-        const int e = L.expert(i);
-        const double c = choice64(a, r64, load_logit<kBf16>(a.logits, row + e), e);   // NaN takes no part
-        t2 = c > t1 ? t1 : c > t2 ? c : t2;
-        t1 = c > t1 ? c : t1;
+    for (int i = 0; L.has(i); i += 2) {
+        float l[2];
+        int e[2];
+        double c[2];
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+            e[v] = L.expert(L.has(i + v) ? i + v : i);
+            l[v] = L.has(i + v) ? load_logit<kBf16>(a.logits, row + e[v]) : -INFINITY;
+        }
+        choice64<2>(a, r64, l, e, c);
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {   // NaN takes no part
+            t2 = c[v] > t1 ? t1 : c[v] > t2 ? c[v] : t2;
+            t1 = c[v] > t1 ? c[v] : t1;
+        }
     }
     __syncwarp();
 #pragma unroll 1
@@ -228,7 +271,10 @@ __device__ __noinline__ int choose64(const RouteScoredArgs& a, int64_t t, int la
         for (int i = 0; (live >> i) != 0; ++i) {
             if ((live >> i) & 1u) {
                 const int e = L.expert(i);
-                const uint64_t k = order_key(choice64(a, r64, load_logit<kBf16>(a.logits, row + e), e));
+                const float l = load_logit<kBf16>(a.logits, row + e);
+                double c;
+                choice64<1>(a, r64, &l, &e, &c);
+                const uint64_t k = order_key(c);
                 if (id == 0x7FFFFFFF || k > best) {   // items ascend in e: the first of equals stays
                     best = k;
                     id = e;
@@ -260,7 +306,10 @@ __device__ __noinline__ int resolve64(const RouteScoredArgs& a, int64_t t, int l
     const int id = 255 - static_cast<int>(packed & 255u);
     const int64_t row = t * a.E;
     const Row64 r64 = row64<kBf16>(a, row, lane);
-    const double c = choice64(a, r64, lane < n ? load_logit<kBf16>(a.logits, row + id) : -INFINITY, lane < n ? id : 0);
+    const int e = lane < n ? id : 0;
+    const float l = lane < n ? load_logit<kBf16>(a.logits, row + e) : -INFINITY;
+    double c;
+    choice64<1>(a, r64, &l, &e, &c);
     __syncwarp();
     int rank = 0;
     for (int i = 0; i < n; ++i) {

@@ -87,12 +87,18 @@ def _a2a_rows(t: torch.Tensor, out_rows: list[int], in_rows: list[int], group) -
 
 
 class LibraryOps:
-    """The compute steps on the CUDA library (the product path)."""
+    """The compute steps on the CUDA library (the product path).  `router`: keyword arguments of
+    ``moe_mxfp4_route_scored`` (score, bias, n_groups, ...) for layers whose router scores
+    experts that way; without it the layer routes by ``moe_mxfp4_route``."""
 
-    def __init__(self, mode: int = 0):
+    def __init__(self, mode: int = 0, router: dict | None = None):
         self.mode = mode
+        self.router = router
 
     def route(self, logits, top_k):
+        if self.router is not None:
+            from . import moe_mxfp4_route_scored
+            return moe_mxfp4_route_scored(logits, top_k, **self.router)
         from . import moe_mxfp4_route
         return moe_mxfp4_route(logits, top_k)
 

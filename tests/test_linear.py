@@ -172,6 +172,12 @@ SHAPES = [(1, 32, 1), (1, 64, 2), (2, 32, 130), (3, 96, 64), (7, 160, 258), (8, 
           (512, 544, 600), (513, 192, 256), (600, 2080, 1026), (1030, 704, 770)]
 
 
+# many tokens with little K (the tile's epilogue is all there is), one output column, columns past the
+# last full tile of every width, and few tokens with more K than the few-token engine takes
+SHAPES += [(1100, 32, 1), (900, 64, 40), (2049, 96, 130), (600, 160, 1950), (1025, 32, 2880), (1537, 128, 514),
+           (777, 256, 1300), (3, 8224, 70), (40, 9216, 131)]
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("M,K,N", SHAPES)
 def test_against_oracle(M, K, N):
@@ -332,3 +338,40 @@ def test_own_stream_and_graph(M):
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(cap, mx.mxfp4_linear(buf, c, s, bias=b, act=ACTS[act], residual=r))
+
+
+@pytest.mark.gpu
+def test_calls_on_two_streams_at_once():
+    """Calls of both engines that overlap on the GPU, each with its own workspace."""
+    cases = [_case(M, 320, 520, "swiglu", torch.bfloat16, True, seed=M) for M in (4, 70, 640, 1400)]
+    dev = []
+    for x, codes, scales, act, b, r in cases:
+        dev.append((x.to(DEV), torch.from_numpy(codes).to(DEV), torch.from_numpy(scales).to(DEV), b.to(DEV), r.to(DEV)))
+
+    def call(i, stream=None):
+        x, c, s, b, r = dev[i]
+        return mx.mxfp4_linear(x, c, s, bias=b, act=mx.ACT_SWIGLU, residual=r, stream=stream)
+
+    want = [call(i) for i in range(4)]
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    torch.cuda.synchronize()
+    got = [[call((i + k) % 4, streams[i]) for i in range(4)] for k in range(8)]
+    torch.cuda.synchronize()
+    assert mx.mxfp4_get_device_status() == 0
+    for k in range(8):
+        for i in range(4):
+            assert torch.equal(got[k][i], want[(i + k) % 4])
+
+
+def test_workspace_sizes():
+    """Nothing up to 16 tokens of a short contraction; then the prepared activations and scales, which
+    grow with the tokens; then the weights in bf16, whatever the tokens."""
+    from moe_expert_gemm_mxfp4_b200 import build as mxbuild
+    mxbuild.build()
+    size = mx.mxfp4_linear_workspace_size
+    assert size(1, 2880, 2880) == size(16, 2880, 2880) == 0
+    few = [size(M, 2880, 2880) for M in (17, 64, 112, 256, 384)]
+    assert all(a < b for a, b in zip(few, few[1:])) and few[-1] < 2 * 2880 * 2880
+    assert size(1024, 2880, 2880) == size(8192, 2880, 2880) == 2 * 2880 * 2880
+    assert size(8192, 2880, 5760, mx.ACT_SWIGLU) == 2 * 2880 * 5760
+    assert size(2, 8224, 64) == 2 * 8224 * 64
