@@ -30,6 +30,12 @@ struct GemmArgs {
     int act_stages;
 };
 
+// How a token's experts lie in the lanes that work on it: lanes per group (2^seg_log2), experts per
+// lane, whether those are aligned vectors.
+struct RouteLanes {
+    int seg_log2, per, vec;
+};
+
 // Arguments of the routing with scores (see route_scored.cu).
 struct RouteScoredArgs {
     const void* logits;        // [T, E] fp32 or bf16
@@ -45,9 +51,10 @@ struct RouteScoredArgs {
     int E, top_k, score, n_groups, top_groups, group_top, renorm;
     int by_logit;              // the choice goes by the logits (no bias, no sums of scores)
     float scale;
-    // set by the launch: experts per group, lanes per group (2^seg_log2), experts per lane, whether those
-    // are aligned vectors; tokens per CTA
-    int group_size, seg_log2, per, vec;
+    // set by the launch: experts per group; the lanes of a token, and those of a token that takes a whole
+    // warp; tokens per CTA
+    int group_size;
+    RouteLanes lanes, warp;
     int64_t chunk;
 };
 

@@ -60,19 +60,28 @@ __device__ __forceinline__ float load_logit(const void* p, int64_t i) {
     return kBf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]) : static_cast<const float*>(p)[i];
 }
 
-// Where expert items live in a warp: 2^seg_log2 lanes per group, `per` consecutive experts of it
-// per lane (fewer, or none, at the group's end).
+// Where a token's experts live in the LT lanes that work on it: 2^seg_log2 lanes per group, `per`
+// consecutive experts of it per lane (fewer, or none, at the group's end).
 struct Lanes {
     int g, base, n;   // the lane's group, first expert and number of experts
-    __device__ __forceinline__ Lanes(const RouteScoredArgs& a, int lane) {
-        g = lane >> a.seg_log2;
-        const int first = (lane & ((1 << a.seg_log2) - 1)) * a.per;
+    __device__ __forceinline__ Lanes(const RouteScoredArgs& a, const RouteLanes& l, int lane) {
+        g = lane >> l.seg_log2;
+        const int first = (lane & ((1 << l.seg_log2) - 1)) * l.per;
         base = g * a.group_size + first;
-        n = g < a.n_groups ? max(0, min(a.per, a.group_size - first)) : 0;
+        n = g < a.n_groups ? max(0, min(l.per, a.group_size - first)) : 0;
     }
     __device__ __forceinline__ bool has(int i) const { return i < n; }
     __device__ __forceinline__ int expert(int i) const { return base + i; }
 };
+
+// Largest over the LT lanes of a token.
+template <int LT>
+__device__ __forceinline__ uint32_t lanes_max(uint32_t v) {
+    if (LT == 32) return __reduce_max_sync(kFull, v);
+#pragma unroll
+    for (int o = LT / 2; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(kFull, v, o));
+    return v;
+}
 
 // The lane's values of a row of logits (or of the bias); -inf past its experts.  vec: every lane has NI or
 // none, and they are aligned vectors.
@@ -209,10 +218,10 @@ __device__ __forceinline__ void choice64(const RouteScoredArgs& a, const Row64& 
     }
 }
 
-// The place of this lane's group among the groups, in 64 bits.
+// The groups that one token keeps, a bit each, by the whole warp in 64 bits.
 template <bool kBf16>
-__device__ __noinline__ int group_rank64(const RouteScoredArgs& a, int64_t t, int lane) {
-    const Lanes L(a, lane);
+__device__ __noinline__ uint32_t group_kept64(const RouteScoredArgs& a, int64_t t, int lane) {
+    const Lanes L(a, a.warp, lane);
     const int64_t row = t * a.E;
     const Row64 r64 = row64<kBf16>(a, row, lane);
     const double ninf = -static_cast<double>(INFINITY);
@@ -236,7 +245,7 @@ __device__ __noinline__ int group_rank64(const RouteScoredArgs& a, int64_t t, in
     }
     __syncwarp();
 #pragma unroll 1
-    for (int o = (1 << a.seg_log2) >> 1; o > 0; o >>= 1) {
+    for (int o = (1 << a.warp.seg_log2) >> 1; o > 0; o >>= 1) {
         const double u1 = __shfl_xor_sync(kFull, t1, o), u2 = __shfl_xor_sync(kFull, t2, o);
         t2 = fmax(fmin(t1, u1), fmax(t2, u2));
         t1 = fmax(t1, u1);
@@ -245,18 +254,19 @@ __device__ __noinline__ int group_rank64(const RouteScoredArgs& a, int64_t t, in
     int rank = 0;
 #pragma unroll 1
     for (int g = 0; g < a.n_groups; ++g) {
-        const double u = __shfl_sync(kFull, v, g << a.seg_log2);
+        const double u = __shfl_sync(kFull, v, g << a.warp.seg_log2);
         rank += u > v || (u == v && g < L.g);
     }
-    return rank;
+    return __reduce_or_sync(kFull, L.g < a.n_groups && rank < a.top_groups ? 1u << L.g : 0u);
 }
 
-// The chosen experts of one token whose kept groups are known (on: this lane's is one), all in 64 bits:
-// for rows with NaN or infinities and for runs of close values longer than a warp.  Lane
-// j < top_k returns the id of slot j.
+// The chosen experts of one token whose kept groups are known, by the whole warp in 64 bits: for
+// rows with NaN or infinities and for long runs of close values.  Lane j < top_k returns the
+// id of slot j.
 template <bool kBf16>
-__device__ __noinline__ int choose64(const RouteScoredArgs& a, int64_t t, int lane, bool on) {
-    const Lanes L(a, lane);
+__device__ __noinline__ int choose64(const RouteScoredArgs& a, int64_t t, int lane, uint32_t kept) {
+    const Lanes L(a, a.warp, lane);
+    const bool on = L.g < 32 && ((kept >> L.g) & 1u);
     const int64_t row = t * a.E;
     const Row64 r64 = row64<kBf16>(a, row, lane);
     uint32_t live = 0;   // items that may still be chosen
@@ -299,7 +309,7 @@ __device__ __noinline__ int choose64(const RouteScoredArgs& a, int64_t t, int la
     return mine;
 }
 
-// The first n lanes' experts (packed keys in fp32's order, at least the top_k best of the token and
+// The first n lanes' experts (by the whole warp; packed keys in fp32's order, at least the top_k best of the token and
 // nothing nearer than fp32 tells behind them) in the exact order: lane j < top_k returns slot j.
 template <bool kBf16>
 __device__ __noinline__ int resolve64(const RouteScoredArgs& a, int64_t t, int lane, uint32_t packed, int n) {
@@ -380,21 +390,25 @@ struct Steps {
     }
 };
 
-// The chosen experts of one token (lane j < top_k returns the id of slot j), and for
-// softmax scores that need them the row's maximum and sum of exp(l - m) (NaN left out, an
-// infinite maximum counts 1 for each of its experts).
+// The chosen experts of token t0 + lane / LT (its lane j < top_k returns the id of slot j; past t1 there is no
+// token), and for softmax scores that need them the row's maximum and sum of exp(l - m) (NaN left
+// out, an infinite maximum counts 1 for each of its experts).
 //
 // One key per item: 24 bits that order c, then the complement of the expert's id.  Every lane sorts
-// its items' keys; each round takes the largest head of the lanes' lists with one warp
-// reduction.  bf16 logits that order the choice themselves are exact in 16 of the 24 bits;
-// fp32 ones are taken in steps of 2^-24 of the row's range, scores in the call's Steps.
-template <bool kBf16, int NI>
-__device__ __forceinline__ int choose(const RouteScoredArgs& a, const Steps& st, int64_t t, int lane, float* m_out,
-                                      float* sum_out) {
-    const Lanes L(a, lane);
+// its items' keys; each round takes the largest head of the lanes' lists.  bf16 logits that order
+// the choice themselves are exact in 16 of the 24 bits; fp32 ones are taken in steps of 2^-24 of
+// the row's range, scores in the call's Steps.
+template <bool kBf16, int NI, int LT>
+__device__ __forceinline__ int choose(const RouteScoredArgs& a, const Steps& st, int64_t t0, int64_t t1, int lane,
+                                      float* m_out, float* sum_out) {
+    constexpr uint32_t kMine = LT == 32 ? kFull : (1u << (LT & 31)) - 1u;   // a token's lanes, from the first
+    const int sub = lane / LT, at = lane % LT;
+    const int64_t t = t0 + sub;
+    const Lanes L(a, a.lanes, at);
+    const int items = t < t1 ? L.n : 0;
     float c[NI], b[NI];
-    load_items<kBf16, NI>(a.logits, t * a.E + L.base, L.n, a.vec, c);
-    if (a.bias) load_items<false, NI>(a.bias, L.base, L.n, a.vec, b);
+    load_items<kBf16, NI>(a.logits, t * a.E + L.base, items, a.lanes.vec, c);
+    if (a.bias) load_items<false, NI>(a.bias, L.base, L.n, a.lanes.vec, b);
     else {
 #pragma unroll
         for (int i = 0; i < NI; ++i) b[i] = 0.f;
@@ -410,7 +424,7 @@ __device__ __forceinline__ int choose(const RouteScoredArgs& a, const Steps& st,
             float m = -INFINITY;
 #pragma unroll
             for (int i = 0; i < NI; ++i) m = fmaxf(m, c[i]);
-            m = order_value32(__reduce_max_sync(kFull, order_key32(m)));
+            m = order_value32(lanes_max<LT>(order_key32(m)));
             float sum = 0.f, e[NI];
 #pragma unroll
             for (int i = 0; i < NI; ++i) {
@@ -418,7 +432,7 @@ __device__ __forceinline__ int choose(const RouteScoredArgs& a, const Steps& st,
                 sum += e[i] == e[i] ? e[i] : 0.f;
             }
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
+            for (int o = LT / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
             *m_out = m;
             *sum_out = sum;
             if (!a.by_logit) {
@@ -444,7 +458,7 @@ __device__ __forceinline__ int choose(const RouteScoredArgs& a, const Steps& st,
             t2 = fmaxf(t2, fminf(t1, c[i]));
             t1 = fmaxf(t1, c[i]);
         }
-        for (int o = (1 << a.seg_log2) >> 1; o > 0; o >>= 1) {
+        for (int o = (1 << a.lanes.seg_log2) >> 1; o > 0; o >>= 1) {
             const float u1 = __shfl_xor_sync(kFull, t1, o), u2 = __shfl_xor_sync(kFull, t2, o);
             t2 = fmaxf(fminf(t1, u1), fmaxf(t2, u2));
             t1 = fmaxf(t1, u1);
@@ -456,22 +470,28 @@ __device__ __forceinline__ int choose(const RouteScoredArgs& a, const Steps& st,
         bool won = false;
 #pragma unroll 1
         for (int j = 0; j < a.top_groups; ++j) {   // the best of those left, the first of equals
-            last = __reduce_max_sync(kFull, left);
-            const int first = __ffs(static_cast<int>(__ballot_sync(kFull, left == last))) - 1;
-            won = L.g == first >> a.seg_log2;
+            last = lanes_max<LT>(left);
+            const uint32_t best = (__ballot_sync(kFull, left == last) >> (sub * LT)) & kMine;
+            won = L.g == (__ffs(static_cast<int>(best)) - 1) >> a.lanes.seg_log2;
             if (won) left = 0u;
         }
         on = left == 0u;
         if (!exact) {   // the last group kept and the first left out
-            const uint32_t out = __reduce_max_sync(kFull, left);
+            const uint32_t out = lanes_max<LT>(left);
             const float x = order_value32(last), y = order_value32(out);
             const float big = real && (won || left == out) ? fmaxf(fabsf(t1), fabsf(second)) : 0.f;
             const bool near = y > -INFINITY && !(x - y > 2.f * err + 0x1p-21f * big);
-            if (__any_sync(kFull, near)) on = group_rank64<kBf16>(a, t, lane) < a.top_groups;
+            const uint32_t who = __ballot_sync(kFull, near);
+            for (int s = 0; who != 0u && s < 32 / LT; ++s) {
+                if ((who >> (s * LT)) & kMine) {
+                    const uint32_t kept = group_kept64<kBf16>(a, t0 + s, lane);
+                    if (sub == s) on = L.g < 32 && ((kept >> L.g) & 1u);
+                }
+            }
         }
     }
     uint32_t key[NI], near = 0;   // near: keys of neighbours no further apart are close
-    const int n = on ? L.n : 0;
+    const int n = on ? items : 0;
     const uint32_t id0 = static_cast<uint32_t>(255 - L.base);
     if (exact) {
 #pragma unroll
@@ -485,8 +505,8 @@ __device__ __forceinline__ int choose(const RouteScoredArgs& a, const Steps& st,
                 y = fmaxf(y, c[i]);
                 x = c[i] == -INFINITY ? x : fminf(x, c[i]);
             }
-            y = order_value32(__reduce_max_sync(kFull, order_key32(y)));
-            lo = -order_value32(__reduce_max_sync(kFull, order_key32(-x)));
+            y = order_value32(lanes_max<LT>(order_key32(y)));
+            lo = -order_value32(lanes_max<LT>(order_key32(-x)));
             scale = y > lo ? fminf((0x1p24f - 16.f) / (y - lo), 0x1p100f) : 0.f;
             near = 3u;    // the roundings of the difference and of the product
         } else {
@@ -501,9 +521,9 @@ __device__ __forceinline__ int choose(const RouteScoredArgs& a, const Steps& st,
         }
     }
     sort_descending<NI>(key);
-    uint32_t got = 0, top = 0;   // lane j: the j-th best
+    uint32_t got = 0, top = 0;   // lane j of the token: the j-th best
     auto next = [&] {
-        top = __reduce_max_sync(kFull, key[0]);
+        top = lanes_max<LT>(key[0]);
         const bool pop = key[0] == top;   // keys are distinct, but for the 0 of empty lists
 #pragma unroll
         for (int i = 0; i < NI; ++i) key[i] = pop ? (i + 1 < NI ? key[i + 1] : 0u) : key[i];
@@ -512,29 +532,45 @@ __device__ __forceinline__ int choose(const RouteScoredArgs& a, const Steps& st,
 #pragma unroll 1
     for (int j = 0; j < rounds; ++j) {
         next();
-        if (lane == j) got = top;
+        if (at == j) got = top;
     }
-    if (!exact) {
-        if (__any_sync(kFull, close)) return choose64<kBf16>(a, t, lane, on);
-        const uint32_t prev = __shfl_up_sync(kFull, got, 1);
-        const bool tie = lane > 0 && got != 0u && (prev >> 8) - (got >> 8) <= near;   // got is 0 past the rounds
-        const uint32_t ties = __ballot_sync(kFull, tie);
-        if (ties) {
-            int n = a.top_k;
-            if ((ties >> n) & 1u) {   // the first left out is close: so may be those behind it
-                uint32_t last = top;
-                for (++n; n < 32; ++n) {
-                    next();
-                    if (top == 0u || (last >> 8) - (top >> 8) > near) break;
-                    if (lane == n) got = top;
-                    last = top;
-                }
-                if (n == 32) return choose64<kBf16>(a, t, lane, on);
-            }
-            return resolve64<kBf16>(a, t, lane, got, n);
+    int mine = 255 - static_cast<int>(got & 255u);
+    if (exact) return mine;
+    const uint32_t prev = __shfl_up_sync(kFull, got, 1, LT);
+    const bool tie = at > 0 && got != 0u && (prev >> 8) - (got >> 8) <= near;   // got is 0 past the rounds
+    const uint32_t ties = __ballot_sync(kFull, tie), odd = __ballot_sync(kFull, close);
+    if ((ties | odd) == 0u) return mine;
+    // if the first left out is close, so may be those behind it: as long as one token's list goes on,
+    // up to its LT-th (then the length is LT)
+    int length = a.top_k;
+    bool more = ((ties >> (sub * LT)) & kMine) >> length & 1u;
+    uint32_t last = top;
+    if (more) ++length;
+    while (__any_sync(kFull, more)) {
+        next();
+        more = more && length < LT && top != 0u && (last >> 8) - (top >> 8) <= near;
+        if (more) {
+            if (at == length) got = top;
+            last = top;
+            ++length;
         }
     }
-    return 255 - static_cast<int>(got & 255u);
+#pragma unroll 1
+    for (int s = 0; s < 32 / LT; ++s) {   // one token after the other, by the whole warp
+        const uint32_t its = kMine << (s * LT);
+        if (((ties | odd) & its) == 0u) continue;
+        const int many = __shfl_sync(kFull, length, s * LT);
+        int ids;
+        if ((odd & its) != 0u || many >= LT) {
+            const uint32_t kept = __reduce_or_sync(kFull, sub == s && on && L.g < a.n_groups ? 1u << L.g : 0u);
+            ids = choose64<kBf16>(a, t0 + s, lane, kept);
+        } else {
+            ids = resolve64<kBf16>(a, t0 + s, lane, __shfl_sync(kFull, got, s * LT + lane % LT), many);
+        }
+        ids = __shfl_sync(kFull, ids, at);
+        if (sub == s) mine = ids;
+    }
+    return mine;
 }
 
 // log of the smallest 64-bit number, 2^-1074, less half a step: scores below it are 0
@@ -542,43 +578,48 @@ constexpr float kLogTiny = -745.13f;
 
 // Slot j's weight on lane j < top_k, from its logit l.  A score that is 0 in 64 bits weighs 0 (l = -inf, or
 // a mask of the type's lowest value), and so does every slot of a token whose chosen scores are all 0.
+template <int LT>
 __device__ __forceinline__ float slot_weight(const RouteScoredArgs& a, float l, bool on, float m, float sum) {
     const bool soft = a.score == MXFP4_SCORE_SOFTMAX;
     // (where the logits order the choice, the first chosen is the row's largest)
-    if (soft && a.by_logit && a.renorm) m = __shfl_sync(kFull, l, 0);
+    if (soft && a.by_logit && a.renorm) m = __shfl_sync(kFull, l, 0, LT);
     float w = soft ? (l == m ? 1.f : expf(l - m)) : __fdividef(1.f, 1.f + expf(-l));
     if (!on || l == -INFINITY) w = 0.f;
     if (!a.renorm) return w == 0.f ? 0.f : w * (soft ? a.scale / sum : a.scale);   // (sum is 0 where all are masked)
     float s = w;
 #pragma unroll
     for (int o = 4; o > 0; o >>= 1) s += __shfl_xor_sync(kFull, s, o);
-    s = __shfl_sync(kFull, s, 0);
-    if (s < 0x1p-60f) {   // scores so small that they lose bits (or are all 0): relative to the largest chosen
+    s = __shfl_sync(kFull, s, 0, LT);
+    const bool tiny = s < 0x1p-60f;
+    if (__any_sync(kFull, tiny)) {   // scores so small that they lose bits (or are all 0): relative to the largest chosen
         float top = on && l == l ? l : -INFINITY;
 #pragma unroll
         for (int o = 4; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
-        w = l == top ? 1.f : expf(l - top);       // a sigmoid far below 0 is e^l
-        if (!on || l == -INFINITY || l - (soft ? m : 0.f) < kLogTiny) w = 0.f;
-        s = w;
+        float v = l == top ? 1.f : expf(l - top);       // a sigmoid far below 0 is e^l
+        if (!on || l == -INFINITY || l - (soft ? m : 0.f) < kLogTiny) v = 0.f;
+        float u = v;
 #pragma unroll
-        for (int o = 4; o > 0; o >>= 1) s += __shfl_xor_sync(kFull, s, o);
+        for (int o = 4; o > 0; o >>= 1) u += __shfl_xor_sync(kFull, u, o);
+        if (tiny) w = v, s = u;
     }
     return s == 0.f ? 0.f : w / s * a.scale;
 }
 
-// Top-k, weights and the pair counts of tokens [t0, t1); s_hist [E] zeroed before.
-template <bool kBf16, int NI>
-__device__ void topk_chunk(const RouteScoredArgs& a, int64_t t0, int64_t t1, int32_t* s_hist) {
+// Top-k, weights and the pair counts of tokens [t0, t1), LT lanes to a token; s_hist [E] zeroed before.
+template <bool kBf16, int NI, int LT>
+__device__ __forceinline__ void topk_chunk(const RouteScoredArgs& a, int64_t t0, int64_t t1, int32_t* s_hist) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    constexpr int kTokens = 32 / LT;   // of a warp at a time
     const Steps st(a, lane);
-    for (int64_t t = t0 + warp; t < t1; t += blockDim.x / 32) {
+    for (int64_t t = t0 + warp * kTokens; t < t1; t += blockDim.x / LT) {
         float m = -INFINITY, sum = 1.f;
-        const int id = choose<kBf16, NI>(a, st, t, lane, &m, &sum);
-        const bool on = lane < a.top_k;
-        const float l = on ? load_logit<kBf16>(a.logits, t * a.E + id) : -INFINITY;
-        const float w = slot_weight(a, l, on, m, sum);
+        const int id = choose<kBf16, NI, LT>(a, st, t, t1, lane, &m, &sum);
+        const int64_t mine = t + lane / LT;
+        const bool on = lane % LT < a.top_k && mine < t1;
+        const float l = on ? load_logit<kBf16>(a.logits, mine * a.E + id) : -INFINITY;
+        const float w = slot_weight<LT>(a, l, on, m, sum);
         if (on) {
-            const int p = static_cast<int>(t) * a.top_k + lane;
+            const int p = static_cast<int>(mine) * a.top_k + lane % LT;
             a.ids[p] = id;
             a.weights[p] = w;
             atomicAdd(&s_hist[id], 1);   // a count: its order does not matter
@@ -704,7 +745,7 @@ route_scored_cluster_kernel(const __grid_constant__ RouteScoredArgs a) {
     __syncthreads();
     const int nb = gridDim.x, me = static_cast<int>(cluster_rank());
     const int64_t t0 = min(a.T, a.chunk * me), t1 = min(a.T, t0 + a.chunk);
-    topk_chunk<kBf16, NI>(a, t0, t1, s_hist);
+    topk_chunk<kBf16, NI, 32>(a, t0, t1, s_hist);
     __syncwarp();
     cluster_barrier();   // every CTA's counts are there, and this one's ids
     for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
@@ -734,7 +775,7 @@ route_scored_cluster_kernel(const __grid_constant__ RouteScoredArgs a) {
     place_chunk(a, t0 * a.top_k, t1 * a.top_k, s_base, s_cnt);
 }
 
-template <bool kBf16, int NI>
+template <bool kBf16, int NI, int LT>
 __global__ void __launch_bounds__(kThreads)
 route_scored_topk_kernel(const __grid_constant__ RouteScoredArgs a) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -742,7 +783,7 @@ route_scored_topk_kernel(const __grid_constant__ RouteScoredArgs a) {
     for (int e = threadIdx.x; e < kMaxE; e += blockDim.x) s_hist[e] = 0;
     __syncthreads();
     const int64_t t0 = a.chunk * blockIdx.x, t1 = min(a.T, t0 + a.chunk);
-    topk_chunk<kBf16, NI>(a, t0, t1, s_hist);
+    topk_chunk<kBf16, NI, LT>(a, t0, t1, s_hist);
     __syncthreads();
     const int row = (a.E + 3) / 4 * 4;   // rows of whole 16-byte vectors
     for (int e = threadIdx.x; e < row; e += blockDim.x) a.chunk_counts[blockIdx.x * row + e] = s_hist[e];
@@ -809,14 +850,14 @@ int64_t chunk_of(int64_t T) {
     return n < kFewWarps ? kFewWarps : n;
 }
 
-template <bool kBf16, int NI>
+template <bool kBf16, int NI, int LT>
 cudaError_t launch(RouteScoredArgs a, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (a.T <= kClusterTokens) {
+    if (LT == 32 && a.T <= kClusterTokens) {
         const int64_t n = (a.T + kFewWarps - 1) / kFewWarps;
         const unsigned nc = static_cast<unsigned>(n < kMaxCluster ? n : kMaxCluster);
         a.chunk = (a.T + nc - 1) / nc;
@@ -830,8 +871,8 @@ cudaError_t launch(RouteScoredArgs a, cudaStream_t stream) {
     }
     a.chunk = chunk_of(a.T);
     const unsigned nb = static_cast<unsigned>((a.T + a.chunk - 1) / a.chunk);
-    const int threads = 32 * static_cast<int>(a.chunk > kWarps ? kWarps : a.chunk);
-    route_scored_topk_kernel<kBf16, NI><<<nb, threads, 0, stream>>>(a);
+    const int64_t warps = (a.chunk * LT + 31) / 32;
+    route_scored_topk_kernel<kBf16, NI, LT><<<nb, 32 * static_cast<int>(warps > kWarps ? kWarps : warps), 0, stream>>>(a);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     cfg.gridDim = dim3(nb, 1, 1);
@@ -839,6 +880,28 @@ cudaError_t launch(RouteScoredArgs a, cudaStream_t stream) {
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     return cudaLaunchKernelEx(&cfg, route_scored_place_kernel, a);
+}
+
+// LT lanes to a token; items per lane rounded up to a power of two, at most 16.
+template <bool kBf16, int LT>
+cudaError_t launch_items(const RouteScoredArgs& a, cudaStream_t stream) {
+    if (a.lanes.per <= 1) return launch<kBf16, 1, LT>(a, stream);
+    if (a.lanes.per <= 2) return launch<kBf16, 2, LT>(a, stream);
+    if (a.lanes.per <= 4) return launch<kBf16, 4, LT>(a, stream);
+    if (a.lanes.per <= 8) return launch<kBf16, 8, LT>(a, stream);
+    return launch<kBf16, 16, LT>(a, stream);
+}
+
+RouteLanes lanes_of(const RouteScoredArgs& a, int lt, bool bf16) {
+    RouteLanes l{};
+    while ((1 << l.seg_log2) < lt) ++l.seg_log2;
+    while ((lt >> l.seg_log2) < a.n_groups && l.seg_log2 > 0) --l.seg_log2;
+    l.per = (a.group_size + (1 << l.seg_log2) - 1) >> l.seg_log2;
+    int ni = 1;
+    while (ni < l.per) ni *= 2;
+    const int wide = bf16 ? (ni < 8 ? ni : 8) : (ni < 4 ? ni : 4);   // elements of a lane's vector loads
+    l.vec = l.per == ni && a.group_size % ni == 0 && a.E % wide == 0;
+    return l;
 }
 
 }  // namespace
@@ -850,20 +913,17 @@ size_t route_scored_ws_bytes(int64_t T, int64_t E) {
 
 cudaError_t launch_route_scored(RouteScoredArgs a, bool bf16, cudaStream_t stream) {
     a.group_size = a.E / a.n_groups;
-    a.seg_log2 = 5;
-    while ((32 >> a.seg_log2) < a.n_groups) --a.seg_log2;
-    a.per = (a.group_size + (1 << a.seg_log2) - 1) >> a.seg_log2;
-    // items per lane: at most 8 where n_groups is a power of two, else at most 16
-    const int ni = a.per <= 1 ? 1 : a.per <= 2 ? 2 : a.per <= 4 ? 4 : a.per <= 8 ? 8 : 16;
-    const int wide = bf16 ? (ni < 8 ? ni : 8) : (ni < 4 ? ni : 4);   // elements of a lane's vector loads
-    a.vec = a.per == ni && a.group_size % ni == 0 && a.E % wide == 0;
-    switch (ni) {
-        case 1: return bf16 ? launch<true, 1>(a, stream) : launch<false, 1>(a, stream);
-        case 2: return bf16 ? launch<true, 2>(a, stream) : launch<false, 2>(a, stream);
-        case 4: return bf16 ? launch<true, 4>(a, stream) : launch<false, 4>(a, stream);
-        case 8: return bf16 ? launch<true, 8>(a, stream) : launch<false, 8>(a, stream);
-        default: return bf16 ? launch<true, 16>(a, stream) : launch<false, 16>(a, stream);
+    a.warp = lanes_of(a, 32, bf16);
+    // Half a warp per token where one round of warps does not hold the batch: what a token takes besides its
+    // items is then shared by two (8192 x 128 11.2 -> 10.4 us, 65536 x 128 35.6 -> 29.1, 65536 x 256 in 8
+    // groups 72.5 -> 68.2).  Within one round latency counts and a token has a warp (1200 x 256 in 8 groups
+    // 10.5 us, in half warps 12.2).
+    if (a.T > kMaxChunks * kWarps && a.n_groups <= 16) {
+        a.lanes = lanes_of(a, 16, bf16);
+        if (a.lanes.per <= 16) return bf16 ? launch_items<true, 16>(a, stream) : launch_items<false, 16>(a, stream);
     }
+    a.lanes = a.warp;
+    return bf16 ? launch_items<true, 32>(a, stream) : launch_items<false, 32>(a, stream);
 }
 
 }  // namespace mx

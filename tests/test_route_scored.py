@@ -248,3 +248,44 @@ def test_workspace_and_outputs_stay_inside():
     ws.check("workspace")
     ref = oracle.route_scored(l.double().cpu().numpy(), k, "sigmoid", None, 6, 2, 2)
     assert np.array_equal(out["inv"].t.cpu().numpy(), ref["inv"])
+
+
+# past one round of warps two tokens share a warp: odd last tokens, every number of lanes per group, groups
+# that half a warp does not hold (3 of 85), more groups than half a warp has lanes
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,E,k,G,tg,gt", [
+    (4736, 32, 4, 1, 1, 1), (4737, 32, 4, 1, 1, 1), (4801, 90, 6, 6, 3, 1), (5003, 256, 8, 8, 4, 2), (4999, 255, 7, 3, 2, 2),
+    (9475, 16, 8, 16, 9, 1), (5001, 64, 8, 32, 8, 2), (6007, 1, 1, 1, 1, 1), (5555, 200, 8, 1, 1, 1)])
+def test_many_tokens_against_oracle(T, E, k, G, tg, gt):
+    for i, (score, bias, renorm, bf16) in enumerate([("softmax", False, True, True), ("sigmoid", True, True, False),
+                                                     ("softmax", True, False, False), ("softmax", False, True, False)]):
+        _check(_logits(T, E, T + E + i), k, bf16=bf16, score=score, bias=_bias(E, T + i) if bias else None,
+               n_groups=G, top_groups=tg, group_top=gt, renorm=renorm)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_tokens_that_share_a_warp_do_not_mix(score):
+    """Rows that take the slow paths (ties, masks, infinities, NaN, long runs of near values) beside
+    ordinary ones and beside each other, in both halves."""
+    T, E, G, k = 4999, 48, 6, 5
+    l = _logits(T, E, 41)
+    inf, nan = float("inf"), float("nan")
+    odd = torch.zeros(10, E)
+    odd[1] = -inf
+    odd[2, ::2] = nan
+    odd[3, 7] = inf
+    odd[4] = -3e38
+    odd[5] = torch.arange(E) % 3
+    odd[6, 8:] = -inf
+    odd[7] = 1.0 + torch.arange(E) * 2.0 ** -23
+    odd[8, :20] = -inf
+    odd[9] = 90.0
+    g = torch.Generator().manual_seed(42)
+    at = torch.randperm(T, generator=g)[:1500]
+    l[at] = odd[torch.randint(10, (1500,), generator=g)]
+    l[T - 1] = odd[5]
+    for bias in (None, _bias(E, 43)):
+        for kw in (dict(), dict(n_groups=G, top_groups=2, group_top=2), dict(n_groups=G, top_groups=3, renorm=False)):
+            _check(l, k, score=score, bias=bias, **kw)
+            _check(l, k, bf16=True, score=score, bias=bias, **kw)
