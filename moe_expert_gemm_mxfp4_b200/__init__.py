@@ -359,24 +359,27 @@ def moe_mxfp4_route_scored(logits: torch.Tensor, top_k: int, score: int = SCORE_
     top_k = int(top_k)
     if top_k < 1:
         raise ValueError(f"top_k: expected at least 1, got {top_k}")
-    # one allocation for the outputs and the workspace, each on a 16-byte boundary: seven took half the call
+    # one allocation for the workspace and the outputs, each on a 16-byte boundary: seven took half the call,
+    # and every piece of it that becomes a tensor takes a microsecond
     P = T * top_k
     need = 0 if ws is not None else moe_mxfp4_route_scored_workspace_size(T, E, top_k)
-    pad_p, pad_e, pad_o = -P % 4, -E % 4, -(E + 1) % 4
-    buf = logits.new_empty((4 * (P + pad_p) + 2 * E + 1 + pad_e + pad_o + need // 4,), dtype=torch.int32)
-    if pad_p or pad_e:
-        ids, _, weights, _, perm, _, inv, _, counts, _, offsets, _, rest = buf.split_with_sizes(
-            (P, pad_p, P, pad_p, P, pad_p, P, pad_p, E, pad_e, E + 1, pad_o, need // 4))
+    pad_p, pad_e, skip = -P % 4, -E % 4, need // 4
+    buf = logits.new_empty((skip + 4 * (P + pad_p) + 2 * E + 1 + pad_e,), dtype=torch.int32)
+    if skip or pad_p or pad_e:
+        _, ids, _, weights, _, perm, _, inv, _, counts, _, offsets = buf.split_with_sizes(
+            (skip, P, pad_p, P, pad_p, P, pad_p, P, pad_p, E, pad_e, E + 1))
     else:
-        ids, weights, perm, inv, counts, offsets, _, rest = buf.split_with_sizes((P, P, P, P, E, E + 1, pad_o, need // 4))
+        ids, weights, perm, inv, counts, offsets = buf.split_with_sizes((P, P, P, P, E, E + 1))
     out = dict(ids=ids.view(T, top_k), weights=weights.view(torch.float32).view(T, top_k), counts=counts,
                offsets=offsets, perm=perm, inv=inv)
-    space = ws if ws is not None else rest
+    if ws is not None:
+        space, nbytes = ws.data_ptr(), ws.numel() * ws.element_size()
+    else:
+        space, nbytes = buf.data_ptr() if need else None, need
     _lib.check("moe_mxfp4_route_scored", lib.moe_mxfp4_route_scored(
         logits.data_ptr(), dt, T, E, top_k, int(score), None if bias is None else bias.data_ptr(), int(n_groups),
         int(top_groups), int(group_top), int(bool(renorm)), float(scale), ids.data_ptr(), weights.data_ptr(),
-        counts.data_ptr(), offsets.data_ptr(), perm.data_ptr(), inv.data_ptr(), space.data_ptr() if need or ws is not None else None,
-        need if ws is None else ws.numel() * ws.element_size(), _stream(stream)))
+        counts.data_ptr(), offsets.data_ptr(), perm.data_ptr(), inv.data_ptr(), space, nbytes, _stream(stream)))
     if stream is not None:
         _used_on(stream, buf)
     return out
