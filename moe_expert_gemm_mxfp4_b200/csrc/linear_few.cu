@@ -674,13 +674,22 @@ Plan make_plan(int64_t M, int64_t K, int64_t n_out, bool gated) {
 
 }  // namespace
 
-// Few tokens as long as one round of CTAs holds them and three token tiles do: beyond, every round
-// streams the weights again, and dequantizing them once is less.  (2880 x 2880: 384 tokens 17 us here, 21 there,
-// 512 23 and 21; 5760 x 2880 gated: 384 24 and 27, 512 44 and 27; 11520 x 2880: 128 23 and 31, 192 38
-// and 32.)  The prepare kernel keeps 32 rows of block scales in shared memory, which bounds K.
+// Which engine is sooner done, by microseconds fitted to measurements.  A round of this engine's CTAs streams
+// its weights again: 6 + 0.0036 K.  The other one dequantizes them once, 2.5 bytes a weight, and its
+// longest pair takes 1 ns per unit of its plan's cost and stage.  One token tile is always sooner here.
+// (Here and there, us: 2880 x 2880, 384 tokens 17 and 21, 512 20 and 21; 5760 x 2880 gated, 336 20 and 24,
+// 384 34 and 25; 11520 x 7680, 112 37 and 82, 256 66 and 83, 384 97 and 106, 512 133 and 107.)  The prepare
+// kernel keeps 32 rows of block scales in shared memory, which bounds K.
 bool linear_is_few(int64_t M, int64_t K, int64_t n_out, bool gated) {
     const int64_t t = (M + kMaxMp - 1) / kMaxMp, f = gated ? 64 : kBM, w = (n_out + f - 1) / f;
-    return K <= 8192 && (t == 1 || (t <= 4 && t * w <= kSms));
+    if (K > 8192) return false;
+    if (t == 1) return true;
+    if (t > kSms || w > (int64_t{1} << 30)) return false;
+    const double here = static_cast<double>((t * w + kSms - 1) / kSms) * (6.0 + 0.0036 * static_cast<double>(K));
+    const double weights = static_cast<double>(n_out) * (gated ? 2 : 1) * static_cast<double>(K);
+    const double there = 8.0 + 5e-7 * weights +
+                         1e-3 * static_cast<double>(linear_many_plan(M, n_out, gated, kSms).cost * ((K + 127) / 128));
+    return here < there;
 }
 
 size_t linear_few_ws_bytes(int64_t M, int64_t K, int64_t n_out, bool gated) {

@@ -176,6 +176,9 @@ SHAPES = [(1, 32, 1), (1, 64, 2), (2, 32, 130), (3, 96, 64), (7, 160, 258), (8, 
 # last full tile of every width, and few tokens with more K than the few-token engine takes
 SHAPES += [(1100, 32, 1), (900, 64, 40), (2049, 96, 130), (600, 160, 1950), (1025, 32, 2880), (1537, 128, 514),
            (777, 256, 1300), (3, 8224, 70), (40, 9216, 131)]
+# two rounds of the few-token engine, ten token tiles of it; the other engine with little to do per tile
+SHAPES += [(300, 2048, 9500), (1100, 672, 1536), (16700, 32, 40), (20000, 64, 1), (2600, 160, 1950), (5000, 64, 514),
+           (2049, 96, 1300), (6000, 96, 258), (4000, 128, 515), (1400, 256, 1550), (9000, 32, 130)]
 
 
 @pytest.mark.gpu
@@ -190,7 +193,7 @@ def test_against_oracle(M, K, N):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("act", list(ACTS))
-@pytest.mark.parametrize("M,K,N", [(5, 96, 70), (70, 160, 300), (700, 256, 302)])
+@pytest.mark.parametrize("M,K,N", [(5, 96, 70), (70, 160, 300), (700, 256, 302), (6000, 96, 302)])
 def test_activations(act, M, K, N):
     for bias in (torch.float32, torch.bfloat16):
         _check(*_case(M, K, N, act, bias, bias == torch.float32, seed=5, std=4.0))
@@ -198,14 +201,14 @@ def test_activations(act, M, K, N):
 
 # every route through the sizes, at odd N (rows that no vector is aligned to)
 @pytest.mark.gpu
-@pytest.mark.parametrize("M", [1, 20, 100, 400, 1500])
+@pytest.mark.parametrize("M", [1, 20, 100, 400, 1500, 2700])
 def test_odd_rows(M):
     _check(*_case(M, 288, 1001, "gelu_tanh", torch.float32, True))
     _check(*_case(M, 288, 1002, "swiglu", torch.float32, True))   # n_out = 501
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("M", [1, 24, 150, 600, 1100])
+@pytest.mark.parametrize("M", [1, 24, 150, 600, 1100, 17000])
 def test_wide_range_of_scales(M):
     """Block scales and activations over many powers of two, zero blocks among them."""
     K, N = 320, 200
@@ -220,7 +223,7 @@ def test_wide_range_of_scales(M):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("M", [1, 24, 150, 600, 1100])
+@pytest.mark.parametrize("M", [1, 24, 150, 600, 1100, 17000])
 def test_outliers_inside_a_block(M):
     """One element of a block 2^12 times the others: the small ones still count in full."""
     K, N = 256, 130
@@ -234,7 +237,7 @@ def test_outliers_inside_a_block(M):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("M", [1, 24, 150, 600, 1100])
+@pytest.mark.parametrize("M", [1, 24, 150, 600, 1100, 17000])
 def test_exact_products(M):
     """Powers of two and small whole numbers add without rounding: the result is the formula's."""
     K, N = 192, 96
@@ -256,7 +259,7 @@ def test_exact_products(M):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("M", [1, 24, 150, 600, 1100])
+@pytest.mark.parametrize("M", [1, 24, 150, 600, 1100, 17000])
 @pytest.mark.parametrize("act", ["none", "relu"])
 def test_infinities_and_nan(M, act):
     K, N = 128, 140
@@ -294,7 +297,7 @@ def test_infinities_and_nan(M, act):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("M", [3, 64, 300, 1200])
+@pytest.mark.parametrize("M", [3, 64, 300, 1200, 6000])
 def test_residual_in_place(M):
     x, codes, scales, act, b, r = _case(M, 320, 260, "silu", torch.bfloat16, True)
     want = _check(x, codes, scales, act, b, r)
@@ -306,7 +309,8 @@ def test_residual_in_place(M):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("M,K,N,act", [(1, 64, 3, "none"), (19, 352, 201, "none"), (77, 160, 130, "swiglu"),
-                                       (300, 288, 257, "none"), (1025, 96, 258, "swiglu"), (1100, 544, 1003, "none")])
+                                       (300, 288, 257, "none"), (1025, 96, 258, "swiglu"), (1100, 544, 1003, "none"),
+                                       (17000, 96, 130, "swiglu"), (6000, 96, 258, "none"), (4000, 128, 515, "none")])
 def test_stays_inside_output_and_workspace(M, K, N, act):
     from test_guard_gpu import Guarded
     x, codes, scales, act, b, r = _case(M, K, N, act, torch.float32, True)
@@ -319,7 +323,7 @@ def test_stays_inside_output_and_workspace(M, K, N, act):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("M", [2, 96, 700, 1300])
+@pytest.mark.parametrize("M", [2, 96, 700, 1300, 5700])
 def test_own_stream_and_graph(M):
     x, codes, scales, act, b, r = _case(M, 480, 330, "swiglu", torch.bfloat16, True)
     c, s, b, r = torch.from_numpy(codes).to(DEV), torch.from_numpy(scales).to(DEV), b.to(DEV), r.to(DEV)
@@ -343,7 +347,7 @@ def test_own_stream_and_graph(M):
 @pytest.mark.gpu
 def test_calls_on_two_streams_at_once():
     """Calls of both engines that overlap on the GPU, each with its own workspace."""
-    cases = [_case(M, 320, 520, "swiglu", torch.bfloat16, True, seed=M) for M in (4, 70, 640, 1400)]
+    cases = [_case(M, 320, 520, "swiglu", torch.bfloat16, True, seed=M) for M in (4, 70, 640, 3600)]
     dev = []
     for x, codes, scales, act, b, r in cases:
         dev.append((x.to(DEV), torch.from_numpy(codes).to(DEV), torch.from_numpy(scales).to(DEV), b.to(DEV), r.to(DEV)))
@@ -361,6 +365,21 @@ def test_calls_on_two_streams_at_once():
     for k in range(8):
         for i in range(4):
             assert torch.equal(got[k][i], want[(i + k) % 4])
+
+
+def test_both_engines_are_in_the_shapes():
+    """The workspace tells which engine a size goes to: the one for many tokens holds the weights in bf16."""
+    from moe_expert_gemm_mxfp4_b200 import build as mxbuild
+    mxbuild.build()
+
+    def many(M, K, N, act="none"):
+        return mx.mxfp4_linear_workspace_size(M, K, N, ACTS[act]) == (N * K * 2 + 255) // 256 * 256
+
+    assert 8 <= sum(many(*s) for s in SHAPES) <= len(SHAPES) - 20
+    assert many(6000, 96, 302) and many(17000, 320, 200) and many(17000, 256, 130) and many(17000, 192, 96)
+    assert many(17000, 128, 140) and many(2700, 288, 1001) and many(2700, 288, 1002, "swiglu") and many(6000, 320, 260)
+    assert many(17000, 96, 130, "swiglu") and many(4000, 128, 515) and many(5700, 480, 330, "swiglu")
+    assert many(3600, 320, 520, "swiglu") and not many(300, 2048, 9500) and not many(1100, 672, 1536)
 
 
 def test_workspace_sizes():
