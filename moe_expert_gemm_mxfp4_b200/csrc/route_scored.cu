@@ -14,7 +14,7 @@
 // than that, the candidates' c are computed again in 64 bits, a lane each, and ranked; where
 // the groups on both sides of the cut do, the whole token is.
 //
-// Up to 256 tokens: one launch, a cluster of up to 8 CTAs with a warp per token; the CTAs exchange
+// Up to 128 tokens: one launch, a cluster of up to 8 CTAs with a warp per token; the CTAs exchange
 // their per-expert pair counts through distributed shared memory.  More tokens: two kernels over
 // at most kMaxChunks contiguous chunks of tokens (one CTA each), the second launched while
 // the first runs (programmatic dependent launch):
@@ -22,6 +22,11 @@
 //   route_scored_place  every CTA sums the chunk counts before its own and over all
 //                       (16-byte loads from L2), scans the experts, and ranks its
 //                       chunk's pairs in ascending order by warp match masks.
+//
+// What bounds it: the bytes are few (8192 x 256 fp32: 1.4 us at the copy bandwidth, 65536 x 128 bf16: 3.2),
+// and a token takes some 870 warp instructions with groups and a bias and 340 without, next to which the
+// latency of the two kernels (8 us) shows.  Times of the whole routing: 1 x 32 4.2 us, 64 x 256 in 8 groups
+// 7.1, 1237 x 90 in 6 groups 12, 8192 x 256 in 8 groups 19, 65536 x 128 30 (700 GB/s).
 #include "common.cuh"
 #include "internal.h"
 
@@ -31,9 +36,12 @@ namespace {
 
 constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
-constexpr int kFewWarps = 8;       // of a CTA at least, while the batch has fewer than 8 tokens per SM
+constexpr int kFewWarps = 8;       // of a CTA at least: tokens that share its set-up (4 and 16 differ by 0.5 us, 32 takes 1 to 2 more)
 constexpr int kMaxCluster = 8;
-constexpr int kClusterTokens = kMaxCluster * kWarps;   // one warp per token, one launch
+// Tokens of one launch, a warp each, 16 to a CTA.  (One launch and two, us, 256 experts in 8 groups: 64 tokens
+// 7.4 and 9.4, 128 8.4 and 9.4, 256 12.8 and 9.9.)
+constexpr int kClusterWarps = 16;
+constexpr int kClusterTokens = kMaxCluster * kClusterWarps;
 constexpr int kMaxE = 256;
 constexpr int kMaxChunks = 148;    // one CTA per SM
 constexpr uint32_t kFull = 0xFFFFFFFFu;
@@ -737,7 +745,7 @@ __device__ __forceinline__ int32_t ld_rank(const int32_t* p, uint32_t rank) {   
 
 // The whole routing of at most kClusterTokens tokens: gridDim.x CTAs, one cluster.
 template <bool kBf16, int NI>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(32 * kClusterWarps)
 route_scored_cluster_kernel(const __grid_constant__ RouteScoredArgs a) {
     __shared__ int32_t s_hist[kMaxE], s_sum[kMaxE], s_base[kMaxE], s_off[kMaxE + 1];
     __shared__ __align__(16) int32_t s_cnt[kWarps * kMaxE];

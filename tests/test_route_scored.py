@@ -141,7 +141,7 @@ def _bias(E, seed, scale=0.05):
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("T,E,k,G,tg,gt", [
     (1, 1, 1, 1, 1, 1), (1, 256, 8, 8, 4, 2), (2, 3, 2, 3, 2, 1), (16, 32, 4, 1, 1, 1), (17, 33, 5, 1, 1, 1),
-    (33, 34, 6, 17, 4, 2), (64, 256, 8, 8, 4, 2), (100, 60, 7, 5, 3, 2), (129, 255, 8, 17, 9, 1),
+    (33, 34, 6, 17, 4, 2), (64, 256, 8, 8, 4, 2), (100, 60, 7, 5, 3, 2), (128, 96, 6, 6, 3, 2), (129, 255, 8, 17, 9, 1),
     (333, 96, 8, 32, 8, 1), (500, 64, 1, 4, 1, 2), (512, 256, 8, 32, 3, 2), (513, 254, 8, 2, 1, 2),
     (2367, 90, 6, 6, 3, 1), (2369, 72, 3, 9, 2, 2), (5000, 256, 8, 16, 5, 2)])
 def test_against_oracle(score, T, E, k, G, tg, gt):
