@@ -329,7 +329,7 @@ linear_few_kernel(const __grid_constant__ CUtensorMap tmap_codes, const __grid_c
     // kOwn: spreading warp 4 h + w splits tokens w, w + 4, ... (at most 16) of half h of each stage and
     // fetches the scales of its rows 32 w .. 32 w + 31; all stages' are on their way from the start
     uint2 xv[kOwn ? kOwnStages : 1][4];
-    uint32_t sv[kOwn ? kOwnStages : 1];
+    uint32_t sv[kOwn ? kOwnStages : 1][4];
     if (kOwn && warp < kSpreadWarps) {
         const int kb = static_cast<int>(a.K / 32), half = warp >> 2;
         const int64_t row = weight_row<kGated>(a, f, 32 * (warp & 3) + lane);
@@ -337,16 +337,14 @@ linear_few_kernel(const __grid_constant__ CUtensorMap tmap_codes, const __grid_c
 #pragma unroll
         for (int i = 0; i < kOwnStages; ++i) {
             const int64_t k = 256LL * (j0 + i) + 128 * half + 4 * lane;
-            uint32_t b[4];
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 const int t = (warp & 3) + 4 * q, x = 8 * (j0 + i) + 4 * half + q;
                 xv[i][q] = make_uint2(0u, 0u);
                 if (i < n && t < mt && k < a.K)
                     xv[i][q] = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.x) + (t0 + t) * a.K + k));
-                b[q] = i < n && x < kb ? __ldg(scales + x) : 0x7Fu;
+                sv[i][q] = i < n && x < kb ? __ldg(scales + x) : 0x7Fu;
             }
-            sv[i] = b[0] | b[1] << 8 | b[2] << 16 | b[3] << 24;
         }
     }
     tc_fence_before();
@@ -361,27 +359,8 @@ linear_few_kernel(const __grid_constant__ CUtensorMap tmap_codes, const __grid_c
         const uint32_t from = smem_u32(codes) + r * 128 + half * 64 + 16 * ch;
         const uint32_t to = smem_u32(smem) + half * kATile + r * kRow + (((2 * ch) ^ (r & 7)) << 4);
         bool ok = true;
-        auto spread = [&](int i, const uint2* x, uint32_t scales) {
+        auto spread = [&](int i) {
             bool got = i < NS || wait_poll(&empty[i % NS], ((i / NS) & 1) ^ 1, &s_abort);
-            if (kOwn && __all_sync(0xFFFFFFFFu, got)) {
-                uint8_t* tile = smem + i % NS * p.stage_bytes + 2 * kATile + half * 2 * p.mp * kRow;
-                uint8_t* atom = smem + i % NS * p.stage_bytes + 2 * kATile + 4 * p.mp * kRow + half * p.sfb_bytes;
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const int t = (warp & 3) + 4 * q;
-                    if (t < mt) {
-                        const Parts z = split4(x[q]);
-                        *reinterpret_cast<uint32_t*>(tile + tile_at(t, lane)) = z.hi;
-                        *reinterpret_cast<uint32_t*>(tile + tile_at(p.mp + t, lane)) = z.lo;
-                        if ((lane & 7) == 0) {
-                            atom[atom_at(t, lane >> 3)] = static_cast<uint8_t>(z.s_hi);
-                            atom[atom_at(p.mp + t, lane >> 3)] = static_cast<uint8_t>(z.s_lo);
-                        }
-                    }
-                }
-                uint8_t* sfa = smem + i % NS * p.stage_bytes + 2 * kATile + p.b_bytes + half * kAtom;
-                *reinterpret_cast<uint32_t*>(sfa + 16 * lane + 4 * (warp & 3)) = scales;
-            }
             if (got) got = wait_poll(&code_full[i % CS], (i / CS) & 1, &s_abort);
             if (!__all_sync(0xFFFFFFFFu, got)) return false;
             const uint32_t src = from + i % CS * kCodeBytes, dst = to + i % NS * p.stage_bytes;
@@ -393,6 +372,34 @@ linear_few_kernel(const __grid_constant__ CUtensorMap tmap_codes, const __grid_c
                 sts64(dst + q * 32 * kRow, v[q].x, v[q].y);
                 sts64((dst ^ 16u) + q * 32 * kRow, v[q].z, v[q].w);
             }
+            if (kOwn) {   // one copy of this code, whatever the stage and token: it is met cold
+                uint8_t* tile = smem + i % NS * p.stage_bytes + 2 * kATile + half * 2 * p.mp * kRow;
+                uint8_t* atom = smem + i % NS * p.stage_bytes + 2 * kATile + 4 * p.mp * kRow + half * p.sfb_bytes;
+                uint2 x[4];
+                uint32_t scales = 0;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    x[q] = xv[0][q];
+                    uint32_t b = sv[0][q];
+#pragma unroll
+                    for (int u = 1; u < (kOwn ? kOwnStages : 1); ++u)
+                        if (i == u) x[q] = xv[u][q], b = sv[u][q];
+                    scales |= b << (8 * q);
+                }
+#pragma unroll 1
+                for (int t = warp & 3; t < mt; t += 4) {
+                    const Parts z = split4(x[0]);
+                    x[0] = x[1], x[1] = x[2], x[2] = x[3];
+                    *reinterpret_cast<uint32_t*>(tile + tile_at(t, lane)) = z.hi;
+                    *reinterpret_cast<uint32_t*>(tile + tile_at(p.mp + t, lane)) = z.lo;
+                    if ((lane & 7) == 0) {
+                        atom[atom_at(t, lane >> 3)] = static_cast<uint8_t>(z.s_hi);
+                        atom[atom_at(p.mp + t, lane >> 3)] = static_cast<uint8_t>(z.s_lo);
+                    }
+                }
+                uint8_t* sfa = smem + i % NS * p.stage_bytes + 2 * kATile + p.b_bytes + half * kAtom;
+                *reinterpret_cast<uint32_t*>(sfa + 16 * lane + 4 * (warp & 3)) = scales;
+            }
             fence_async_proxy();   // generic writes -> the tensor core's reads
             __syncwarp();
             if (lane == 0) {
@@ -401,13 +408,8 @@ linear_few_kernel(const __grid_constant__ CUtensorMap tmap_codes, const __grid_c
             }
             return true;
         };
-        if (kOwn) {
-#pragma unroll
-            for (int i = 0; i < kOwnStages; ++i)
-                if (i < n && ok) ok = spread(i, xv[i], sv[i]);
-        } else {
-            for (int i = 0; i < n && ok; ++i) ok = spread(i, xv[0], 0u);
-        }
+#pragma unroll 1
+        for (int i = 0; i < n && ok; ++i) ok = spread(i);
         if (!ok) {
             s_abort = 1;
             record_status(a.status, MXFP4_ERR_TIMEOUT);
