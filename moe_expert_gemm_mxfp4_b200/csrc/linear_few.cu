@@ -28,9 +28,9 @@
 // run); each finishes a share of the tokens.
 //
 // What bounds it: up to a hundred tokens neither bytes nor MMAs but the chain of a launch (set-up, the first
-// codes, the spreading of a stage, the cluster's sums): 1 x 2880 x 2880 8.6 us (0.7 at the copy bandwidth),
+// codes, the spreading of a stage, the cluster's sums): 1 x 2880 x 2880 7.8 us (0.7 at the copy bandwidth),
 // 64 x 2880 x 5760 gated 13.0 (1.5); with long weights the spreading, 32 x 7680 x 11520 29 us (1.7 TB/s); with
-// several token tiles the MMAs and the waits around them, 512 x 2880 x 2880 19.5 us (435 TFLOP/s).
+// several token tiles the MMAs, twice what bf16's would be, and the finish, 512 x 2880 x 2880 19.0 us (447 TFLOP/s).
 //
 // hi and lo rows lie next to each other in one MMA of N = 2 Mp columns while that fits the 128
 // rows of a scale atom (an MMA of N <= 64 costs the same whatever its N), else they are
@@ -54,8 +54,8 @@ constexpr int kATile = kBM * kRow;
 constexpr int kAtom = 512;           // scale atom: 128 rows x 4 scales
 constexpr int kMaxMp = 112;          // tokens per tile: two stages and two code slots still fit
 constexpr int kOwnMp = 16;           // largest token tile that is prepared where it is used: one launch instead of two
-                                     // (2880 x 2880, us, called by a host 11 instead of 15; replayed from a graph 8.3 and
-                                     // 7.9 for 1 token, 10.4 and 8.2 for 16, where each CTA's own splitting shows),
+                                     // (2880 x 2880, us, called by a host 11 instead of 15; replayed from a graph 7.5 and
+                                     // 7.9 for 1 token, 8.5 and 8.1 for 8, 10.2 and 8.2 for 16, where the splitting shows),
 constexpr int kOwnStages = 3;        // and the stages of a CTA it is loaded ahead for
 constexpr int kMaxStages = 3;
 constexpr int kCodeBytes = kBM * 128;   // a code slot: a stage's 128 bytes of each row
@@ -585,9 +585,15 @@ linear_few_kernel(const __grid_constant__ CUtensorMap tmap_codes, const __grid_c
 #pragma unroll
                         for (int q = 0; q < SPLIT; ++q) {
                             const uint32_t at = mine + cc * (kBM * 4);
-                            const uint32_t from = SPLIT > 1 ? in_rank(at, q) : at;
-                            v[b][q] = ld_cluster_f32x4(from);
-                            if (kGated) w[b][q] = ld_cluster_f32x4(from + 64 * 4);
+                            if (SPLIT > 1) {
+                                const uint32_t from = in_rank(at, q);
+                                v[b][q] = ld_cluster_f32x4(from);
+                                if (kGated) w[b][q] = ld_cluster_f32x4(from + 64 * 4);
+                            } else {
+                                const float* at_own = part + cc * kBM + 4 * qd;
+                                v[b][q] = *reinterpret_cast<const float4*>(at_own);
+                                if (kGated) w[b][q] = *reinterpret_cast<const float4*>(at_own + 64);
+                            }
                         }
                     }
                 }
@@ -687,7 +693,7 @@ Plan make_plan(int64_t M, int64_t K, int64_t n_out, bool gated) {
 // Which engine is sooner done, by microseconds fitted to measurements.  A round of this engine's CTAs streams
 // its weights again: 6 + 0.0036 K.  The other one dequantizes them once, 2.5 bytes a weight, and its
 // longest pair takes 1 ns per unit of its plan's cost and stage.  One token tile is always sooner here.
-// (Here and there, us: 2880 x 2880, 384 tokens 17 and 21, 512 20 and 21; 5760 x 2880 gated, 336 20 and 24,
+// (Here and there, us: 2880 x 2880, 384 tokens 17 and 21, 512 19 and 21; 5760 x 2880 gated, 336 20 and 24,
 // 384 34 and 25; 11520 x 7680, 112 37 and 82, 256 66 and 83, 384 97 and 106, 512 133 and 107.)  The prepare
 // kernel keeps 32 rows of block scales in shared memory, which bounds K.
 bool linear_is_few(int64_t M, int64_t K, int64_t n_out, bool gated) {
