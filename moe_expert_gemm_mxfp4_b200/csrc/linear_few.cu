@@ -30,7 +30,7 @@
 // What bounds it: up to a hundred tokens neither bytes nor MMAs but the chain of a launch (set-up, the first
 // codes, the spreading of a stage, the cluster's sums): 1 x 2880 x 2880 7.8 us (0.7 at the copy bandwidth),
 // 64 x 2880 x 5760 gated 13.0 (1.5); with long weights the spreading, 32 x 7680 x 11520 29 us (1.7 TB/s); with
-// several token tiles the MMAs, twice what bf16's would be, and the finish, 512 x 2880 x 2880 19.0 us (447 TFLOP/s).
+// several token tiles the MMAs (of both parts) and the finish, 512 x 2880 x 2880 19.0 us (447 TFLOP/s).
 //
 // hi and lo rows lie next to each other in one MMA of N = 2 Mp columns while that fits the 128
 // rows of a scale atom (an MMA of N <= 64 costs the same whatever its N), else they are
