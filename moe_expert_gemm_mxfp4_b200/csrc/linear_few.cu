@@ -30,7 +30,7 @@
 // What bounds it: up to a hundred tokens neither bytes nor MMAs but the chain of a launch (set-up, the first
 // codes, the spreading of a stage, the cluster's sums): 1 x 2880 x 2880 7.8 us (0.7 at the copy bandwidth),
 // 64 x 2880 x 5760 gated 13.0 (1.5); with long weights the spreading, 32 x 7680 x 11520 29 us (1.7 TB/s); with
-// several token tiles the MMAs (of both parts) and the finish, 512 x 2880 x 2880 19.0 us (447 TFLOP/s).
+// several token tiles the MMAs (of both parts) and the finish, 512 x 2880 x 2880 18.4 us (462 TFLOP/s).
 //
 // hi and lo rows lie next to each other in one MMA of N = 2 Mp columns while that fits the 128
 // rows of a scale atom (an MMA of N <= 64 costs the same whatever its N), else they are
@@ -231,18 +231,16 @@ linear_few_prepare_kernel(const LinearArgs a, const Plan p, uint8_t* __restrict_
         }
         return;
     }
-    const int64_t items = a.M * halves;
-    const int64_t step = static_cast<int64_t>(gridDim.x - w_ctas) * (kPrepareThreads / 32);
-    for (int64_t it = static_cast<int64_t>(blockIdx.x - w_ctas) * (kPrepareThreads / 32) + warp; it < items; it += step) {
-        const int64_t t = it / halves;
-        const int j = static_cast<int>(it - t * halves);
-        const int64_t tt = t / p.mp;
-        const int r = static_cast<int>(t - tt * p.mp);
-        const int64_t k = static_cast<int64_t>(j) * kRow + 4 * lane;
+    // 32 bits hold the items: this engine takes at most kSms tiles of kMaxMp tokens, and K of 64 half stages
+    const unsigned items = static_cast<unsigned>(a.M) * halves, step = (gridDim.x - w_ctas) * (kPrepareThreads / 32);
+    for (unsigned it = (blockIdx.x - w_ctas) * (kPrepareThreads / 32) + warp; it < items; it += step) {
+        const unsigned t = it / halves, tt = t / static_cast<unsigned>(p.mp);
+        const int j = static_cast<int>(it - t * halves), r = static_cast<int>(t - tt * p.mp);
+        const int k = j * kRow + 4 * lane;
         uint2 v = make_uint2(0u, 0u);
         if (k < a.K) v = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.x) + t * a.K + k));
         const Parts q = split4(v);
-        uint8_t* blk = ws_b + (tt * p.nk + (j >> 1)) * p.b_bytes;
+        uint8_t* blk = ws_b + (static_cast<int64_t>(tt) * p.nk + (j >> 1)) * p.b_bytes;
         uint8_t* tile = blk + (j & 1) * 2 * p.mp * kRow;
         const int r_lo = p.mp + r;
         *reinterpret_cast<uint32_t*>(tile + tile_at(r, lane)) = q.hi;
