@@ -132,7 +132,8 @@ MXFP4_API int32_t mxfp4_token_tile_rows(int64_t rows, int64_t groups, mxfp4_mode
  *           SWIGLU SiLU(z_g) * z_u with W rows [0, N/2) gate and [N/2, N) up (N even);
  *   n_out   N, or N / 2 with SWIGLU;
  *   bias    [N] in bf16 or fp32 per `bias_dt`, or NULL;
- *   residual bf16 [M, n_out], or NULL; it may be y itself (the sum in place).
+ *   residual bf16 [M, n_out], or NULL; it may be y itself (the sum in place).  Else y overlaps
+ *           neither it nor x (MXFP4_ERR_INVALID_ARG).
  * Inf and NaN in x, in a block scale (0xFF), bias or residual spread as in the formula.
  * A weight is its code times 2^(S-127); where that is past bf16's range (S > 252) it may
  * enter the product as Inf or as the exact value.

@@ -89,6 +89,11 @@ EncodeTiledFn encode_fn() {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+bool overlap(const void* p, int64_t p_bytes, const void* q, int64_t q_bytes) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+    return a < b ? b - a < static_cast<uintptr_t>(p_bytes) : a - b < static_cast<uintptr_t>(q_bytes);
+}
+
 // Packed codes of G groups as a 3-D tensor {K/2 bytes, rows, G}; box {128, box_rows, 1}
 // (128 B = 256 K values of each row per copy); 128-byte swizzle (conflict-free 16-B
 // reads of one row per thread).
@@ -542,6 +547,10 @@ mxfp4_status mxfp4_linear(const void* x_bf16, int64_t M, int64_t K, const uint8_
     if (!aligned16(x_bf16) || !aligned16(w_codes) || !aligned16(w_scales) || !aligned16(y_bf16) ||
         (bias && !aligned16(bias)) || (residual_bf16 && !aligned16(residual_bf16)))
         return MXFP4_ERR_MISALIGNED;
+    const int64_t y_bytes = 2 * M * n_out;
+    if (overlap(y_bf16, y_bytes, x_bf16, 2 * M * K)) return MXFP4_ERR_INVALID_ARG;
+    if (residual_bf16 && residual_bf16 != y_bf16 && overlap(y_bf16, y_bytes, residual_bf16, y_bytes))
+        return MXFP4_ERR_INVALID_ARG;
     const size_t need = mxfp4_linear_workspace_size(M, K, N, act);
     if (need > 0 && (!ws || ws_bytes < need)) return MXFP4_ERR_WORKSPACE;
     if (ws && !aligned16(ws)) return MXFP4_ERR_MISALIGNED;

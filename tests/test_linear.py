@@ -54,6 +54,7 @@ def test_oracle_against_fsum(act):
 # ---------------------------------------------------------------- refusals (CPU)
 
 A, U, N0 = ctypes.c_void_p(0x10000), ctypes.c_void_p(0x10001), ctypes.c_void_p(0)
+FAR = ctypes.c_void_p(1 << 50)
 
 
 def test_argument_checks():
@@ -61,7 +62,7 @@ def test_argument_checks():
     mxbuild.build()
     lib = _lib.load()
 
-    def call(x=A, M=8, K=256, c=A, s=A, N=512, bias=N0, bdt=0, act=0, res=N0, y=A, ws=A, nbytes=1 << 40):
+    def call(x=A, M=8, K=256, c=A, s=A, N=512, bias=N0, bdt=0, act=0, res=N0, y=FAR, ws=A, nbytes=1 << 40):
         return lib.mxfp4_linear(x, M, K, c, s, N, bias, bdt, act, res, y, ws, nbytes, N0)
 
     for kw in (dict(x=N0), dict(c=N0), dict(s=N0), dict(y=N0), dict(M=0), dict(K=0), dict(N=0), dict(M=-1), dict(N=-5),
@@ -78,6 +79,23 @@ def test_argument_checks():
             assert call(M=M, K=2880, N=5760, act=5, nbytes=need - 1) == _lib.ERR_WORKSPACE
             assert call(M=M, K=2880, N=5760, act=5, ws=N0, nbytes=0) == _lib.ERR_WORKSPACE
     assert mx.mxfp4_linear_workspace_size(0, 2880, 5760) == 0
+    # y over x, or over a residual that is not y itself: 64 x 256 of x, 64 x 512 of y and residual.  What passes
+    # this check is refused by the next, for a workspace of nothing: no call here may launch on made-up addresses.
+    at = ctypes.c_void_p
+    base, far, x_bytes, y_bytes = 1 << 30, 1 << 40, 64 * 256 * 2, 64 * 512 * 2
+    assert mx.mxfp4_linear_workspace_size(64, 256, 512) > 0
+
+    def placed(**kw):
+        return call(M=64, nbytes=0, **kw)
+
+    for y in (base, base + 16, base + x_bytes - 16, base - y_bytes + 16):
+        assert placed(x=at(base), y=at(y)) == _lib.ERR_INVALID_ARG
+    for y in (base + 16, base + y_bytes - 16, base - y_bytes + 16):
+        assert placed(x=at(far), res=at(base), y=at(y)) == _lib.ERR_INVALID_ARG
+    for y in (base + x_bytes, base - y_bytes):
+        assert placed(x=at(base), y=at(y)) == _lib.ERR_WORKSPACE
+    for y in (base, base + y_bytes, base - y_bytes):
+        assert placed(x=at(far), res=at(base), y=at(y)) == _lib.ERR_WORKSPACE
 
 
 def test_binding_refusals():
@@ -305,6 +323,18 @@ def test_residual_in_place(M):
     args = (x.to(DEV), torch.from_numpy(codes).to(DEV), torch.from_numpy(scales).to(DEV))
     out = mx.mxfp4_linear(*args, bias=b.to(DEV), act=ACTS[act], residual=buf, out=buf)
     assert out is buf and torch.equal(buf, want)
+
+
+@pytest.mark.gpu
+def test_output_over_the_input_is_refused():
+    x, codes, scales, _, _, r = _case(5, 128, 128, "none", None, True)
+    c, s = torch.from_numpy(codes).to(DEV), torch.from_numpy(scales).to(DEV)
+    both = torch.cat([x, r]).to(DEV)
+    for kw in (dict(out=both[:5]), dict(out=both[1:6]), dict(out=both[4:9], residual=both[5:])):
+        with pytest.raises(mx.Mxfp4Error):
+            mx.mxfp4_linear(both[:5] if "residual" not in kw else x.to(DEV), c, s, **kw)
+    y = mx.mxfp4_linear(both[:5], c, s, residual=both[5:], out=both[5:])   # the rows behind x, in place
+    assert torch.equal(y, mx.mxfp4_linear(x.to(DEV), c, s, residual=r.to(DEV)))
 
 
 @pytest.mark.gpu
