@@ -289,3 +289,28 @@ def test_tokens_that_share_a_warp_do_not_mix(score):
         for kw in (dict(), dict(n_groups=G, top_groups=2, group_top=2), dict(n_groups=G, top_groups=3, renorm=False)):
             _check(l, k, score=score, bias=bias, **kw)
             _check(l, k, bf16=True, score=score, bias=bias, **kw)
+
+
+@pytest.mark.gpu
+def test_calls_on_several_streams_at_once():
+    """Calls that need the whole GPU at once, small ones and a linear layer, on four streams that do not wait for
+    each other."""
+    E, k = 64, 4
+    logits = [_logits(T, E, 50 + T).to(DEV) for T in (40, 700, 6000, 20000)]
+    x = torch.randn(300, 512, generator=torch.Generator().manual_seed(5)).to(torch.bfloat16).to(DEV)
+    codes, scales = mx.mxfp4_quantize(torch.randn(640, 512, generator=torch.Generator().manual_seed(6)).to(DEV))
+    want = [mx.moe_mxfp4_route_scored(l, k, n_groups=8, top_groups=4) for l in logits]
+    y = mx.mxfp4_linear(x, codes, scales)
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    torch.cuda.synchronize()
+    got = []
+    for r in range(6):
+        for i, s in enumerate(streams):
+            n = (i + r) % 4
+            got.append((n, mx.moe_mxfp4_route_scored(logits[n], k, n_groups=8, top_groups=4, stream=s),
+                        mx.mxfp4_linear(x, codes, scales, stream=s)))
+    torch.cuda.synchronize()
+    assert mx.mxfp4_get_device_status() == 0
+    for n, r, z in got:
+        assert all(torch.equal(r[key], want[n][key]) for key in want[n])
+        assert torch.equal(z, y)
