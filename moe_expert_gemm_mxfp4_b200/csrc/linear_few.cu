@@ -760,8 +760,10 @@ cudaError_t product_of(int split, const CUtensorMap& tmap_codes, const LinearArg
         case 1: return product<kGated, 1, kOwn>(tmap_codes, a, p, ws_b, ws_sfa, stream, launch, clusters);
         case 2: return product<kGated, 2, kOwn>(tmap_codes, a, p, ws_b, ws_sfa, stream, launch, clusters);
         case 4: return product<kGated, 4, kOwn>(tmap_codes, a, p, ws_b, ws_sfa, stream, launch, clusters);
-        default: return product<kGated, 8, kOwn>(tmap_codes, a, p, ws_b, ws_sfa, stream, launch, clusters);
+        default: break;
     }
+    if constexpr (kOwn) return cudaErrorInvalidValue;   // own_split gives at most 4
+    else return product<kGated, kMaxCluster, kOwn>(tmap_codes, a, p, ws_b, ws_sfa, stream, launch, clusters);
 }
 
 // K split over the largest cluster of which the GPU holds all at once (a second round costs more than
