@@ -465,9 +465,10 @@ __device__ __forceinline__ int choose(const RouteScoredArgs& a, const Steps& st,
     if (a.top_groups < a.n_groups) {
         float t1 = -INFINITY, t2 = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < NI; ++i) {   // NaN takes no part
-            t2 = fmaxf(t2, fminf(t1, c[i]));
-            t1 = fmaxf(t1, c[i]);
+        for (int i = 0; i < NI; ++i) {
+            const float v = c[i] == c[i] ? c[i] : -INFINITY;   // NaN takes no part
+            t2 = fmaxf(t2, fminf(t1, v));
+            t1 = fmaxf(t1, v);
         }
         for (int o = (1 << a.lanes.seg_log2) >> 1; o > 0; o >>= 1) {
             const float u1 = __shfl_xor_sync(kFull, t1, o), u2 = __shfl_xor_sync(kFull, t2, o);

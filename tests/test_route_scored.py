@@ -314,3 +314,18 @@ def test_calls_on_several_streams_at_once():
     for n, r, z in got:
         assert all(torch.equal(r[key], want[n][key]) for key in want[n])
         assert torch.equal(z, y)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("T", [100, 700, 5000])
+def test_nan_logits_do_not_count_for_their_group(score, T):
+    """A few NaN among ordinary logits: a group's two largest values are those of its numbers."""
+    E, G = 48, 4
+    g = torch.Generator().manual_seed(T)
+    l = torch.randn(T, E, generator=g) * 2
+    l[torch.rand(T, E, generator=g) < 0.04] = float("nan")
+    for bias in (None, _bias(E, 61)):
+        for tg in (1, 2):
+            _check(l, 5, score=score, bias=bias, n_groups=G, top_groups=tg, group_top=2)
+            _check(l, 5, bf16=True, score=score, bias=bias, n_groups=G, top_groups=tg, group_top=2, renorm=False)
