@@ -9,9 +9,10 @@
 // bf16 has 8 significant bits, hi takes 4, and what is left of an element fits the 4 of lo: the
 // sum is exact for every element within 2^14 of its block's largest, and off by at most
 // 2^-22 of that largest for the others, about what one addition in fp32 rounds.  Products with
-// E2M1 are exact, sums are fp32.  A block that holds Inf or NaN gets the scale NaN; an output
-// that comes out NaN is computed again from x and W in fp32, so that infinities act as in
-// the formula.
+// E2M1 are exact, sums are fp32.  A block that holds Inf or NaN gets the scale NaN, and
+// hi alone passes fp32's range where x is in the last 3% of it (significands from 0xF8 on round up to
+// 2^128); so a sum that is not finite is computed again from x and W themselves, and infinities
+// act as in the formula.
 //
 // Two launches, the second overlapping the first (programmatic dependent launch):
 //   linear_few_prepare  x -> hi and lo tiles in the tensor core's shared-memory image, their
@@ -253,18 +254,18 @@ linear_few_prepare_kernel(const LinearArgs a, const Plan p, uint8_t* __restrict_
     }
 }
 
-// One output's sum in fp32 from x and W themselves.
+// One output's sum from x and W themselves: in 64 bits, whose range no product and no partial sum leaves.
 __device__ __noinline__ float dot_direct(const LinearArgs& a, int64_t m, int64_t row) {
     const uint16_t* x = static_cast<const uint16_t*>(a.x) + m * a.K;
     const uint8_t* c = a.codes + row * (a.K / 2);
-    float acc = 0.f;
+    double acc = 0.0;
     for (int64_t k = 0; k < a.K; k += 2) {
-        const float s = e8m0_f32(a.scales[row * (a.K / 32) + k / 32]);
+        const double s = e8m0_f32(a.scales[row * (a.K / 32) + k / 32]);
         const uint32_t byte = c[k / 2];
-        acc += __uint_as_float(static_cast<uint32_t>(x[k]) << 16) * (e2m1_f32(byte & 15u) * s);
-        acc += __uint_as_float(static_cast<uint32_t>(x[k + 1]) << 16) * (e2m1_f32(byte >> 4) * s);
+        acc = fma(static_cast<double>(__uint_as_float(static_cast<uint32_t>(x[k]) << 16)), e2m1_f32(byte & 15u) * s, acc);
+        acc = fma(static_cast<double>(__uint_as_float(static_cast<uint32_t>(x[k + 1]) << 16)), e2m1_f32(byte >> 4) * s, acc);
     }
-    return acc;
+    return static_cast<float>(acc);
 }
 
 // ---------------------------------------------------------------- product
@@ -608,10 +609,10 @@ linear_few_kernel(const __grid_constant__ CUtensorMap tmap_codes, const __grid_c
                         z[0] += v[b][q].x, z[1] += v[b][q].y, z[2] += v[b][q].z, z[3] += v[b][q].w;
                         if (kGated) u[0] += w[b][q].x, u[1] += w[b][q].y, u[2] += w[b][q].z, u[3] += w[b][q].w;
                     }
-                    bool nan = false;
+                    bool finite = true;
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) nan |= z[j] != z[j] || u[j] != u[j];
-                    if (nan) {
+                    for (int j = 0; j < 4; ++j) finite = finite && fabsf(z[j]) < INFINITY && fabsf(u[j]) < INFINITY;
+                    if (!finite) {
                         for (int j = 0; j < 4; ++j) {
                             if (n0 + j < a.n_out) {
                                 z[j] = dot_direct(a, m, n0 + j);

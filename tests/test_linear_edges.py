@@ -1,0 +1,77 @@
+"""The linear layer (mxfp4_linear) at the edges of its range."""
+import numpy as np
+import pytest
+import torch
+
+import moe_expert_gemm_mxfp4_b200 as mx
+from test_linear import ACTS, DEV
+
+# token counts that reach the few-token engine with one launch, with hi and lo in one MMA, with two MMAs, with several
+# token tiles; and the many-token engine
+TOKENS = [1, 5, 24, 100, 150, 600, 17000]
+
+
+def _one_hot(N, K, at, code=0x2, scale=127):
+    """MXFP4 weights of zeros but for `code` (0x2: 1.0) at (n, at[n]), every block scale `scale`."""
+    codes = np.zeros((N, K // 2), dtype=np.uint8)
+    for n, k in enumerate(at):
+        if k is not None:
+            codes[n, k // 2] = code << (4 * (k % 2))
+    return torch.from_numpy(codes).to(DEV), torch.full((N, K // 32), scale, dtype=torch.uint8, device=DEV)
+
+
+def _linear(x, codes, scales, act="none", **kw):
+    y = mx.mxfp4_linear(x.to(DEV), codes, scales, act=ACTS[act], **kw)
+    torch.cuda.synchronize()
+    assert mx.mxfp4_get_device_status() == 0
+    return y.cpu()
+
+
+# the patterns of bf16's largest values, 248 2^120 to 255 2^120
+LARGEST = torch.arange(0x7F78, 0x7F80, dtype=torch.int16).view(torch.bfloat16)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M", TOKENS)
+def test_largest_values_stay_finite(M):
+    """One element at the top of bf16's range times a power of two: the result is the element's product, exactly
+    (a sum of one nonzero term has no rounding), and finite where it fits bf16."""
+    K, N = 96, 5
+    vals = LARGEST[torch.arange(M) % 8] * torch.where(torch.arange(M) % 3 == 1, -1.0, 1.0).to(torch.bfloat16)
+    x = torch.zeros(M, K, dtype=torch.bfloat16)
+    x[:, 41] = vals
+    codes, scales = _one_hot(N, K, [41, None, 41, 7, 41])
+    got = _linear(x, codes, scales)
+    zero = torch.zeros(M, dtype=torch.bfloat16)
+    assert torch.equal(got, torch.stack([vals, zero, vals, zero, vals], 1))
+    # the same products from smaller factors: half of the element against a weight of 2, an eighth against 4 x 2
+    for part, code, scale in ((0.5, 0x4, 127), (0.125, 0x6, 128)):
+        x[:, 41] = (vals.float() * part).to(torch.bfloat16)
+        codes, scales = _one_hot(N, K, [41, None, 41, 7, 41], code, scale)
+        got = _linear(x, codes, scales)
+        assert torch.equal(got, torch.stack([vals, zero, vals, zero, vals], 1))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M", TOKENS)
+def test_largest_values_through_the_gate(M):
+    """gate 2 against the largest up, and the largest gate against up 0.5.  SiLU(2) is within 2^-16 of its value in
+    fp32, the product and bf16 round once each: 2^-8 + 2^-15 of the result."""
+    K, F = 64, 3
+    big = LARGEST[torch.arange(M) % 8]
+    x = torch.zeros(M, K, dtype=torch.bfloat16)
+    x[:, 3], x[:, 40] = 2.0, big
+    # features: gate and up rows (3, 40); (40, 3) with half of x[3]'s weight; (None, 40)
+    codes, scales = _one_hot(2 * F, K, [3, 40, None, 40, 3, 40])
+    scales[F + 1] = 125                                              # up: 0.25 x 2
+    got = _linear(x, codes, scales, "swiglu").double()
+    b = big.double()
+    want = torch.stack([2 / (1 + np.exp(-2.0)) * b, b * 0.5, torch.zeros(M, dtype=torch.float64)], 1)
+    limit = torch.finfo(torch.bfloat16).max
+    over = want > limit * (1 + 2.0 ** -9)                            # the first overflows: SiLU(2) is 1.76
+    assert torch.isinf(got[over]).all()
+    assert (torch.abs(got - want)[~over] <= (2.0 ** -8 + 2.0 ** -15) * want[~over]).all()
+    x[:, 3] = 1.0                                                    # SiLU(1) = 0.73: all finite
+    got = _linear(x, codes, scales, "swiglu").double()
+    want = torch.stack([1 / (1 + np.exp(-1.0)) * b, b * 0.25, torch.zeros(M, dtype=torch.float64)], 1)
+    assert (torch.abs(got - want) <= (2.0 ** -8 + 2.0 ** -15) * want).all()
