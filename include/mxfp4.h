@@ -138,7 +138,8 @@ MXFP4_API int32_t mxfp4_token_tile_rows(int64_t rows, int64_t groups, mxfp4_mode
  * A weight is its code times 2^(S-127); where that is past bf16's range (S > 252) it may
  * enter the product as Inf or as the exact value.
  * Requires K % 32 == 0, K <= 2^20, M and N <= 2^30, N * K <= 2^40 and M * n_out <= 2^46; any M >= 1, N >= 1.  ws:
- * mxfp4_linear_workspace_size() bytes (0 for up to 16 tokens where K is short).
+ * mxfp4_linear_workspace_size() bytes (0 for up to 16 tokens where K is short, and for
+ * sizes or an activation that the call refuses).
  * Source: agentlenshq.com, "Transformers 4.40 performance upgrades for OpenAI GPT-OSS ...",
  * section "MXFP4 4-Bit Quantization" (MXFP4 weights multiplied without a bf16 copy of the
  * model); the epilogue is this library's. */

@@ -523,8 +523,21 @@ mxfp4_status mxfp4_gemm(const void* x_bf16, int64_t M, int64_t K, const uint8_t*
     return e == cudaSuccess ? MXFP4_OK : cuda_fail(e);
 }
 
+// The sizes and the activation that the linear layer takes; for its workspace query as well, whose arithmetic
+// the limits keep in range.
+static mxfp4_status check_linear_sizes(int64_t M, int64_t K, int64_t N, mxfp4_act act) {
+    if (M <= 0 || K <= 0 || N <= 0) return MXFP4_ERR_INVALID_ARG;
+    if (act < MXFP4_ACT_NONE || act > MXFP4_ACT_SWIGLU) return MXFP4_ERR_INVALID_ARG;
+    const int64_t lim = int64_t{1} << 30;
+    if (K % 32 != 0 || K > (1 << 20) || M > lim || N > lim) return MXFP4_ERR_UNSUPPORTED_SHAPE;
+    if (act == MXFP4_ACT_SWIGLU && N % 2 != 0) return MXFP4_ERR_UNSUPPORTED_SHAPE;
+    const int64_t n_out = act == MXFP4_ACT_SWIGLU ? N / 2 : N;
+    if (M > (int64_t{1} << 46) / n_out || N > (int64_t{1} << 40) / K) return MXFP4_ERR_UNSUPPORTED_SHAPE;
+    return MXFP4_OK;
+}
+
 size_t mxfp4_linear_workspace_size(int64_t M, int64_t K, int64_t N, mxfp4_act act) {
-    if (M <= 0 || K <= 0 || N <= 0) return 0;
+    if (check_linear_sizes(M, K, N, act) != MXFP4_OK) return 0;
     const bool gated = act == MXFP4_ACT_SWIGLU;
     const int64_t n_out = gated ? N / 2 : N;
     if (mx::linear_is_few(M, K, n_out, gated)) return align_up(mx::linear_few_ws_bytes(M, K, n_out, gated), 256);
@@ -536,14 +549,10 @@ mxfp4_status mxfp4_linear(const void* x_bf16, int64_t M, int64_t K, const uint8_
                           mxfp4_act act, const void* residual_bf16, void* y_bf16, void* ws, size_t ws_bytes,
                           void* stream) {
     if (!x_bf16 || !w_codes || !w_scales || !y_bf16) return MXFP4_ERR_INVALID_ARG;
-    if (M <= 0 || K <= 0 || N <= 0) return MXFP4_ERR_INVALID_ARG;
     if (bias && bias_dt != MXFP4_IN_BF16 && bias_dt != MXFP4_IN_F32) return MXFP4_ERR_INVALID_ARG;
-    if (act < MXFP4_ACT_NONE || act > MXFP4_ACT_SWIGLU) return MXFP4_ERR_INVALID_ARG;
-    const int64_t lim = int64_t{1} << 30;
-    if (K % 32 != 0 || K > (1 << 20) || M > lim || N > lim) return MXFP4_ERR_UNSUPPORTED_SHAPE;
-    if (act == MXFP4_ACT_SWIGLU && N % 2 != 0) return MXFP4_ERR_UNSUPPORTED_SHAPE;
+    mxfp4_status st = check_linear_sizes(M, K, N, act);
+    if (st != MXFP4_OK) return st;
     const int64_t n_out = act == MXFP4_ACT_SWIGLU ? N / 2 : N;
-    if (M > (int64_t{1} << 46) / n_out || N > (int64_t{1} << 40) / K) return MXFP4_ERR_UNSUPPORTED_SHAPE;
     if (!aligned16(x_bf16) || !aligned16(w_codes) || !aligned16(w_scales) || !aligned16(y_bf16) ||
         (bias && !aligned16(bias)) || (residual_bf16 && !aligned16(residual_bf16)))
         return MXFP4_ERR_MISALIGNED;
@@ -555,7 +564,7 @@ mxfp4_status mxfp4_linear(const void* x_bf16, int64_t M, int64_t K, const uint8_
     if (need > 0 && (!ws || ws_bytes < need)) return MXFP4_ERR_WORKSPACE;
     if (ws && !aligned16(ws)) return MXFP4_ERR_MISALIGNED;
     DeviceInfo* d = nullptr;
-    mxfp4_status st = device_info(&d);
+    st = device_info(&d);
     if (st != MXFP4_OK) return st;
     mx::LinearArgs a{};
     a.x = x_bf16;
