@@ -8,9 +8,16 @@
 namespace mx {
 namespace linear {
 
-// z / (1 + e^-v): the hardware's exponential and quotient are off by less than 2^-17 of the
-// result here, far below bf16's half step.
-__device__ __forceinline__ float over_one_plus_exp(float z, float v) { return __fdividef(z, 1.f + __expf(-v)); }
+// z / (1 + e^-v) by h = e^(-|v| / 2), which stays a normal number wherever the result is one in fp32: z h^2 / (1 + h^2)
+// for negative v (e^-v itself passes a reciprocal's range at 2^126, and the result would be 0 from
+// v = -87.3 on, where SiLU is -5e-37).  The rounded argument and the hardware's 2^x leave h off by less than
+// (|v| + 5) 2^-24 of itself, so the result by twice that and some 2^-21: below 2^-15 where it is not 0.
+__device__ __forceinline__ float over_one_plus_exp(float z, float v) {
+    float h, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(h) : "f"(-0.72134752044448170f * fabsf(v)));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + h * h));
+    return (v < 0.f ? z * h * h : z) * r;
+}
 
 // z -> act(z) for four outputs in fp32 (u: the gated activation's second factors).  One copy of
 // this code per kernel and one switch per four outputs: inlined at every element, the

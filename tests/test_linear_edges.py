@@ -75,3 +75,38 @@ def test_largest_values_through_the_gate(M):
     got = _linear(x, codes, scales, "swiglu").double()
     want = torch.stack([1 / (1 + np.exp(-1.0)) * b, b * 0.25, torch.zeros(M, dtype=torch.float64)], 1)
     assert (torch.abs(got - want) <= (2.0 ** -8 + 2.0 ** -15) * want).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M", TOKENS)
+@pytest.mark.parametrize("act", ["silu", "gelu_tanh", "gelu", "swiglu"])
+def test_tails_of_the_activations(M, act):
+    """z from -110 to 110: the activations keep their relative accuracy down to bf16's smallest numbers.  The
+    exponential's argument v carries at most 6 roundings (|v| <= 104 where the result is not 0: 104 * 6 * 2^-24, below
+    2^-14 of the result), the hardware's exponential is off by (4 + 1.2 |v|) 2^-23, below 2^-15, the quotient and
+    the products by less than 2^-20: 2^-13 together.  bf16 rounds once (2^-8, at the bottom half of 2^-133), and
+    fp32 before the gate's product by 2^-150 at the bottom."""
+    K = 96
+    z = torch.linspace(-110, 110, 881).to(torch.bfloat16)
+    x = torch.zeros(M, K, dtype=torch.bfloat16)
+    at = (88 + torch.arange(M)[:, None] * 97 + torch.arange(3) * 861) % 881   # the first row: z = -88, -93, -98
+    x[:, [1, 34, 63]] = z[at]
+    up = 1.0
+    if act == "swiglu":   # the up rows read 2^40, in a block of its own
+        x[:, 70] = up = 2.0 ** 40
+        codes, scales = _one_hot(6, K, [1, 34, 63, 70, 70, 70])
+    else:
+        codes, scales = _one_hot(3, K, [1, 34, 63])
+    got = _linear(x, codes, scales, act).double()
+    v = z[at].double()
+    if act == "gelu":
+        want = 0.5 * v * torch.special.erfc(-v / 2 ** 0.5)
+    elif act == "gelu_tanh":
+        want = v * torch.sigmoid(2 * (2 / np.pi) ** 0.5 * (v + 0.044715 * v ** 3))
+    else:
+        want = v * torch.sigmoid(v) * up
+    tol = (2.0 ** -8 + 2.0 ** -13) * want.abs() + 2.0 ** -134 + 2.0 ** -150 * up
+    bad = (got - want).abs() > tol
+    assert not bad.any(), (v[bad][:5], got[bad][:5], want[bad][:5])
+    if act == "swiglu":
+        assert want.abs()[0, 0] > 1e-25              # far above the smallest numbers
