@@ -3,8 +3,10 @@ import numpy as np
 import pytest
 import torch
 
+import oracle
 import moe_expert_gemm_mxfp4_b200 as mx
-from test_linear import ACTS, DEV
+from helpers import f64_of
+from test_linear import ACTS, DEV, _weights, tolerance
 
 # token counts that reach the few-token engine with one launch, with hi and lo in one MMA, with two MMAs, with several
 # token tiles; and the many-token engine
@@ -110,3 +112,52 @@ def test_tails_of_the_activations(M, act):
     assert not bad.any(), (v[bad][:5], got[bad][:5], want[bad][:5])
     if act == "swiglu":
         assert want.abs()[0, 0] > 1e-25              # far above the smallest numbers
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M", TOKENS)
+@pytest.mark.parametrize("act,N", [("none", 141), ("relu", 143), ("silu", 142), ("gelu", 141), ("gelu_tanh", 131),
+                                   ("swiglu", 280), ("swiglu", 282), ("swiglu", 142)])
+def test_infinities_and_nan_through_every_epilogue(M, act, N):
+    """Inf and NaN in x, in block scales (gate and up rows), bias and residual come out where the formula has them, and
+    nowhere else; beside them the results are the ordinary ones, within the bound of the parity tests."""
+    K, inf, nan = 128, float("inf"), float("nan")
+    n_out = N // 2 if act == "swiglu" else N
+    g = torch.Generator().manual_seed(M + N)
+    x = torch.randn(M, K, generator=g).to(torch.bfloat16)
+    x[0, 3] = inf
+    if M > 4:
+        x[1, 70] = -inf
+        x[2, 5], x[2, 9] = inf, -inf
+        x[3, 64] = nan
+    codes, scales = _weights(N, K, 4)
+    scales = scales.copy()
+    scales[7, 1] = scales[n_out - 1, 3] = scales[N - 1, 0] = scales[N - 12, 2] = 255
+    bias = (torch.randn(N, generator=g) * 0.3).to(torch.bfloat16 if N % 2 else torch.float32)
+    bias[2], bias[14], bias[N - 3], bias[N - 20], bias[n_out - 5] = inf, -inf, nan, inf, -inf
+    res = torch.randn(M, n_out, generator=g).to(torch.bfloat16)
+    res[0, 11], res[0, 12], res[M - 1, n_out - 7], res[M - 1, 20] = inf, nan, -inf, inf
+    got = _linear(x, torch.from_numpy(codes).to(DEV), torch.from_numpy(scales).to(DEV), act, bias=bias.to(DEV),
+                  residual=res.to(DEV)).double().numpy()
+    xf, b, r = f64_of(x), f64_of(bias), f64_of(res)
+    W = oracle.dequantize_f64(codes, scales)
+    assert np.isnan(W).any()
+    with np.errstate(all="ignore"):
+        z = torch.from_numpy(xf) @ torch.from_numpy(W).T + torch.from_numpy(b)
+        if act == "swiglu":
+            a = z[:, :n_out] / (1 + torch.exp(-z[:, :n_out])) * z[:, n_out:]
+        else:
+            a = dict(none=lambda v: v, relu=lambda v: torch.where(v < 0, 0.0, v), silu=lambda v: v / (1 + torch.exp(-v)),
+                     gelu=lambda v: v * (1 + torch.erf(v / 2 ** 0.5)) / 2,
+                     gelu_tanh=lambda v: v * (1 + torch.tanh((2 / np.pi) ** 0.5 * (v + 0.044715 * v ** 3))) / 2)[act](z)
+        ref = a.numpy() + r
+    assert np.array_equal(np.isnan(got), np.isnan(ref))
+    isinf = np.isinf(ref)
+    assert isinf.any() and np.array_equal(got[isinf], ref[isinf])
+    fin = np.isfinite(ref)
+    assert np.isfinite(got[fin]).all()
+    # the bound from finite stand-ins: an output is finite only where what is not finite did not reach it (or relu cut it off)
+    xs, bs, rs = (np.where(np.isfinite(v), v, 0.0) for v in (xf, b, r))
+    tol = tolerance(torch.from_numpy(xs), codes, np.where(scales == 255, 0, scales).astype(np.uint8), bs, act,
+                    np.where(fin, ref, 0.0), rs)
+    assert (np.abs(got[fin] - ref[fin]) <= tol[fin]).all()
