@@ -174,13 +174,24 @@ def _plain(t, dev, dtype, shape) -> bool:
     return t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous()
 
 
-def _used_on(stream, *tensors):
-    """Tell the allocator that `stream`, if the caller gave one, uses these tensors: those
-    allocated here belong to the current stream's pool and must not be reused before."""
-    if stream is not None and stream != torch.cuda.current_stream():
-        for t in tensors:
-            if t is not None:
-                t.record_stream(stream)
+def _elsewhere(stream) -> bool:
+    return stream is not None and stream != torch.cuda.current_stream()
+
+
+def _called_on(stream, call, *operands):
+    """``call()`` with `stream` current, for a caller whose current stream is another one.  What the call allocates
+    then comes from `stream`'s own pool: a free block of the caller's pool may still wait for the caller's kernels,
+    which `stream` does not.  The operands' memory is not reused before `stream` is done with them, the results' not
+    before the caller's stream is."""
+    here = torch.cuda.current_stream()
+    with torch.cuda.stream(stream):
+        result = call()
+    for t in operands:
+        if t is not None:
+            t.record_stream(stream)
+    for t in result.values() if isinstance(result, dict) else (result,):
+        t.record_stream(here)
+    return result
 
 
 @lru_cache(maxsize=1024)
@@ -218,7 +229,11 @@ def mxfp4_linear(x: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Tensor,
                  residual=None, out=None, ws=None, stream=None):
     """y bf16 [M, n_out] = act(x bf16 [M, K] . dequant(W)^T + bias) + residual (W4A16), W codes
     [N, K/2] + scales [N, K/32]; bias bf16 or fp32 [N]; n_out = N, or N / 2 with ACT_SWIGLU
-    (W rows [0, N/2) gate, [N/2, N) up); residual bf16 [M, n_out], which may be `out`."""
+    (W rows [0, N/2) gate, [N/2, N) up); residual bf16 [M, n_out], which may be `out`.  On another `stream` than the
+    current one the caller orders the two: operands written before, results read after."""
+    if _elsewhere(stream):
+        return _called_on(stream, lambda: mxfp4_linear(x, w_codes, w_scales, bias, act, residual, out, ws),
+                          x, w_codes, w_scales, bias, residual, out, ws)
     act = int(act)
     try:
         (M, K), (N, _), dev = x.shape, w_codes.shape, x.get_device()
@@ -234,21 +249,18 @@ def mxfp4_linear(x: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Tensor,
     if not ready:
         M, K, N, n_out = _check_linear_operands(x, w_codes, w_scales, bias, act, residual, out, ws)
     lib = _lib.load()
-    new_out = new_ws = None
     nbytes = 0 if ws is None else ws.numel() * ws.element_size()
     if out is None:
-        out = new_out = x.new_empty((M, n_out))
+        out = x.new_empty((M, n_out))
     if ws is None:
         nbytes = mxfp4_linear_workspace_size(M, K, N, act)
         if nbytes:
-            ws = new_ws = w_codes.new_empty((nbytes,))
+            ws = w_codes.new_empty((nbytes,))
     bias_dt = _lib.IN_F32 if bias is not None and bias.dtype is torch.float32 else _lib.IN_BF16
     _lib.check("mxfp4_linear", lib.mxfp4_linear(
         x.data_ptr(), M, K, w_codes.data_ptr(), w_scales.data_ptr(), N, None if bias is None else bias.data_ptr(),
         bias_dt, act, None if residual is None else residual.data_ptr(), out.data_ptr(),
         None if ws is None else ws.data_ptr(), nbytes, _stream(stream)))
-    if stream is not None:
-        _used_on(stream, new_out, new_ws)
     return out
 
 
@@ -344,7 +356,11 @@ def moe_mxfp4_route_scored(logits: torch.Tensor, top_k: int, score: int = SCORE_
     bf16 [T, E]; bias fp32 [E] is added to the scores for the choice only; of n_groups groups
     the top_groups by their group_top largest choice values are kept; weights are the chosen
     experts' scores, renormalised to their sum if `renorm`, times `scale`.  Returns the dict
-    of ``moe_mxfp4_route``."""
+    of ``moe_mxfp4_route``.  On another `stream` than the current one the caller orders the two, as for
+    ``mxfp4_linear``."""
+    if _elsewhere(stream):
+        return _called_on(stream, lambda: moe_mxfp4_route_scored(logits, top_k, score, bias, n_groups, top_groups,
+                                                                 group_top, renorm, scale, ws), logits, bias, ws)
     try:
         (T, E), dev, dtype = logits.shape, logits.get_device(), logits.dtype
         ready = (dev >= 0 and dev == torch.cuda.current_device() and ws is None
@@ -380,8 +396,6 @@ def moe_mxfp4_route_scored(logits: torch.Tensor, top_k: int, score: int = SCORE_
         logits.data_ptr(), dt, T, E, top_k, int(score), None if bias is None else bias.data_ptr(), int(n_groups),
         int(top_groups), int(group_top), int(bool(renorm)), float(scale), ids.data_ptr(), weights.data_ptr(),
         counts.data_ptr(), offsets.data_ptr(), perm.data_ptr(), inv.data_ptr(), space, nbytes, _stream(stream)))
-    if stream is not None:
-        _used_on(stream, buf)
     return out
 
 
