@@ -718,7 +718,7 @@ mxfp4_status moe_mxfp4_route_scored(const void* router_logits, mxfp4_in_dtype dt
     a.renorm = renorm != 0;
     a.by_logit = !bias && (n_groups == 1 || group_top == 1);
     a.scale = scale;
-    cudaError_t e = mx::launch_route_scored(a, dt == MXFP4_IN_BF16, static_cast<cudaStream_t>(stream));
+    cudaError_t e = mx::launch_route_scored(a, dt == MXFP4_IN_BF16, d->sm_count, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? MXFP4_OK : cuda_fail(e);
 }
 

@@ -115,7 +115,7 @@ cudaError_t launch_gather_rows(const void* src, int64_t n_src, int64_t row_bytes
 cudaError_t launch_combine(const void* y_sorted, const int32_t* inv, int64_t T, int top_k,
                            int64_t H, void* out, int sm_count, cudaStream_t stream);
 size_t route_scored_ws_bytes(int64_t T, int64_t E);
-cudaError_t launch_route_scored(RouteScoredArgs a, bool bf16, cudaStream_t stream);
+cudaError_t launch_route_scored(RouteScoredArgs a, bool bf16, int sm_count, cudaStream_t stream);
 bool linear_is_few(int64_t M, int64_t K, int64_t n_out, bool gated);   // the engine: few or many tokens
 size_t linear_few_ws_bytes(int64_t M, int64_t K, int64_t n_out, bool gated);
 cudaError_t launch_linear_few(const LinearArgs& a, const CUtensorMap& tmap_codes, void* ws, int sm_count,

@@ -15,8 +15,8 @@
 // the groups on both sides of the cut do, the whole token is.
 //
 // Up to 128 tokens: a cluster of up to 8 CTAs with a warp per token; the CTAs exchange their per-expert
-// pair counts through distributed shared memory.  More tokens: at most kMaxChunks contiguous chunks of
-// them, one CTA each, all on the GPU at once (a cooperative launch; as two kernels, the second overlapping
+// pair counts through distributed shared memory.  More tokens: contiguous chunks of them, at most
+// one per SM (route_chunks.h), one CTA each, all on the GPU at once (a cooperative launch; as two kernels, the second overlapping
 // the first, a host needs 23 us for a call instead of 21; replayed, 300 x 32 takes 8.7 us here and 7.8 so, 65536 x
 // 128 28.3 and 29.1).  A CTA writes its chunk's counts, ranks its
 // pairs by warp match masks, and after a barrier of the grid sums the counts of the chunks before its
@@ -32,6 +32,7 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "route_chunks.h"
 
 namespace mx {
 
@@ -39,14 +40,13 @@ namespace {
 
 constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
-constexpr int kFewWarps = 8;       // of a CTA at least: tokens that share its set-up (4 and 16 differ by 0.5 us, 32 takes 1 to 2 more)
 constexpr int kMaxCluster = 8;
 // Tokens of a cluster, a warp each, 16 to a CTA.  (256 experts in 8 groups, us: 128 tokens 8.4 and, by a grid, 129
 // 10.5; with 32 to a CTA 256 tokens 12.8, by a grid 10.9.)
 constexpr int kClusterWarps = 16;
 constexpr int kClusterTokens = kMaxCluster * kClusterWarps;
 constexpr int kMaxE = 256;
-constexpr int kMaxChunks = 148;    // one CTA per SM
+constexpr int kMaxChunks = kRouteMaxChunks;
 constexpr uint32_t kFull = 0xFFFFFFFFu;
 
 // A double's place in the order of the choice, larger is better: the bits folded so
@@ -850,21 +850,15 @@ route_scored_grid_kernel(const __grid_constant__ RouteScoredArgs a) {
     });
 }
 
-// Tokens of a chunk: 8, a warp per token, while the SMs last, then what fills one CTA per SM.
-int64_t chunk_of(int64_t T) {
-    const int64_t n = (T + kMaxChunks - 1) / kMaxChunks;
-    return n < kFewWarps ? kFewWarps : n;
-}
-
 template <bool kBf16, int NI, int LT>
-cudaError_t launch(RouteScoredArgs a, cudaStream_t stream) {
+cudaError_t launch(RouteScoredArgs a, int sm_count, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     if (LT == 32 && a.T <= kClusterTokens) {
-        const int64_t n = (a.T + kFewWarps - 1) / kFewWarps;
+        const int64_t n = (a.T + kRouteMinChunk - 1) / kRouteMinChunk;
         const unsigned nc = static_cast<unsigned>(n < kMaxCluster ? n : kMaxCluster);
         a.chunk = (a.T + nc - 1) / nc;
         cfg.gridDim = dim3(nc, 1, 1);
@@ -875,8 +869,8 @@ cudaError_t launch(RouteScoredArgs a, cudaStream_t stream) {
         attr[0].val.clusterDim.z = 1;
         return cudaLaunchKernelEx(&cfg, route_scored_cluster_kernel<kBf16, NI>, a);
     }
-    a.chunk = chunk_of(a.T);
-    const unsigned nb = static_cast<unsigned>((a.T + a.chunk - 1) / a.chunk);
+    a.chunk = route_chunk(a.T, sm_count);
+    const unsigned nb = static_cast<unsigned>(route_chunks(a.T, sm_count));
     cfg.gridDim = dim3(nb, 1, 1);
     cfg.blockDim = dim3(kThreads, 1, 1);
     attr[0].id = cudaLaunchAttributeCooperative;
@@ -886,12 +880,12 @@ cudaError_t launch(RouteScoredArgs a, cudaStream_t stream) {
 
 // LT lanes to a token; items per lane rounded up to a power of two, at most 16.
 template <bool kBf16, int LT>
-cudaError_t launch_items(const RouteScoredArgs& a, cudaStream_t stream) {
-    if (a.lanes.per <= 1) return launch<kBf16, 1, LT>(a, stream);
-    if (a.lanes.per <= 2) return launch<kBf16, 2, LT>(a, stream);
-    if (a.lanes.per <= 4) return launch<kBf16, 4, LT>(a, stream);
-    if (a.lanes.per <= 8) return launch<kBf16, 8, LT>(a, stream);
-    return launch<kBf16, 16, LT>(a, stream);
+cudaError_t launch_items(const RouteScoredArgs& a, int sm_count, cudaStream_t stream) {
+    if (a.lanes.per <= 1) return launch<kBf16, 1, LT>(a, sm_count, stream);
+    if (a.lanes.per <= 2) return launch<kBf16, 2, LT>(a, sm_count, stream);
+    if (a.lanes.per <= 4) return launch<kBf16, 4, LT>(a, sm_count, stream);
+    if (a.lanes.per <= 8) return launch<kBf16, 8, LT>(a, sm_count, stream);
+    return launch<kBf16, 16, LT>(a, sm_count, stream);
 }
 
 RouteLanes lanes_of(const RouteScoredArgs& a, int lt, bool bf16) {
@@ -909,23 +903,24 @@ RouteLanes lanes_of(const RouteScoredArgs& a, int lt, bool bf16) {
 }  // namespace
 
 size_t route_scored_ws_bytes(int64_t T, int64_t E) {
-    const int64_t n = (T + chunk_of(T) - 1) / chunk_of(T);
+    // (a device with fewer SMs has no more chunks)
+    const int64_t n = route_chunks(T, kMaxChunks);
     return T <= kClusterTokens ? 0 : static_cast<size_t>(n * ((E + 3) / 4 * 4)) * sizeof(int32_t);
 }
 
-cudaError_t launch_route_scored(RouteScoredArgs a, bool bf16, cudaStream_t stream) {
+cudaError_t launch_route_scored(RouteScoredArgs a, bool bf16, int sm_count, cudaStream_t stream) {
     a.group_size = a.E / a.n_groups;
     a.warp = lanes_of(a, 32, bf16);
     // Half a warp per token where one round of warps does not hold the batch: what a token takes besides its
     // items is then shared by two (8192 x 128 11.2 -> 10.4 us, 65536 x 128 35.6 -> 29.1, 65536 x 256 in 8
     // groups 72.5 -> 68.2).  Within one round latency counts and a token has a warp (1200 x 256 in 8 groups
     // 10.5 us, in half warps 12.2).
-    if (a.T > kMaxChunks * kWarps && a.n_groups <= 16) {
+    if (a.T > route_max_chunks(sm_count) * kWarps && a.n_groups <= 16) {
         a.lanes = lanes_of(a, 16, bf16);
-        if (a.lanes.per <= 16) return bf16 ? launch_items<true, 16>(a, stream) : launch_items<false, 16>(a, stream);
+        if (a.lanes.per <= 16) return bf16 ? launch_items<true, 16>(a, sm_count, stream) : launch_items<false, 16>(a, sm_count, stream);
     }
     a.lanes = a.warp;
-    return bf16 ? launch_items<true, 32>(a, stream) : launch_items<false, 32>(a, stream);
+    return bf16 ? launch_items<true, 32>(a, sm_count, stream) : launch_items<false, 32>(a, sm_count, stream);
 }
 
 }  // namespace mx
