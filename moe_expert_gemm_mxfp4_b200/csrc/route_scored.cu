@@ -88,10 +88,13 @@ struct Lanes {
 // Largest over the LT lanes of a token.
 template <int LT>
 __device__ __forceinline__ uint32_t lanes_max(uint32_t v) {
-    if (LT == 32) return __reduce_max_sync(kFull, v);
+    if constexpr (LT == 32) {
+        return __reduce_max_sync(kFull, v);
+    } else {
 #pragma unroll
-    for (int o = LT / 2; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(kFull, v, o));
-    return v;
+        for (int o = LT / 2; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(kFull, v, o));
+        return v;
+    }
 }
 
 // The lane's values of a row of logits (or of the bias); -inf past its experts.  vec: every lane has NI or
