@@ -1,5 +1,5 @@
-// How the scored routing of many tokens is dealt to CTAs: contiguous chunks of tokens, one CTA each, all
-// on the GPU at once (so never more than it has SMs: a CTA takes one whole).
+// How the scored routing of many tokens is dealt to CTAs: contiguous chunks of tokens, one CTA each, in one
+// round (so never more than the device has SMs: a CTA takes one whole).
 #pragma once
 
 #include <cstdint>

@@ -14,22 +14,23 @@
 // than that, the candidates' c are computed again in 64 bits, a lane each, and ranked; where
 // the groups on both sides of the cut do, the whole token is.
 //
-// Up to 128 tokens: a cluster of up to 8 CTAs with a warp per token; the CTAs exchange their per-expert
-// pair counts through distributed shared memory.  More tokens: contiguous chunks of them, at most
-// one per SM (route_chunks.h), one CTA each, all on the GPU at once (a cooperative launch; as two kernels, the second overlapping
-// the first, a host needs 23 us for a call instead of 21; replayed, 300 x 32 takes 8.7 us here and 7.8 so, 65536 x
-// 128 28.3 and 29.1).  A CTA writes its chunk's counts, ranks its
-// pairs by warp match masks, and after a barrier of the grid sums the counts of the chunks before its
-// own and of all (16-byte loads from L2), scans the experts and places the pairs.
+// Up to 128 tokens: one launch, a cluster of up to 8 CTAs with a warp per token; the CTAs exchange their
+// per-expert pair counts through distributed shared memory.  More tokens: two kernels over contiguous
+// chunks of them (route_chunks.h), one CTA each, the second launched while the first runs
+// (programmatic dependent launch):
+//   route_scored_topk   ids and weights, and the chunk's per-expert pair counts;
+//   route_scored_place  every CTA sums the counts of the chunks before its own and of all (16-byte
+//                       loads from L2), scans the experts, and ranks its chunk's pairs in ascending
+//                       order by warp match masks.
+// (One kernel with a barrier of the grid in between needs all its CTAs on the GPU at once and waits without a
+// limit for those that are not; it was no faster on the device: 300 x 32 8.6 us against 7.8 so, 1237 x 90 12.3
+// against 12.0, 65536 x 128 29.8 and 29.8.)
 //
-// What bounds it: the bytes are few (8192 x 256 fp32: 1.4 us at the copy bandwidth, 65536 x 128 bf16: 3.2),
-// and a token takes some 870 warp instructions with groups and a bias and 340 without, next to which the
-// launch, the barrier and the placing (8 us) show.  Times of the whole routing: 1 x 32 4.2 us, 64 x 256 in 8 groups
-// 7.1, 1237 x 90 in 6 groups 12, 8192 x 256 in 8 groups 19, 65536 x 128 29 (720 GB/s).
-#include <cooperative_groups.h>
-
-#include <utility>
-
+// What bounds it: the bytes are few (8192 x 256 fp32: 1.4 us at the copy bandwidth, 65536 x 128 bf16: 3.2).  A
+// token takes some 1100 warp instructions with groups and a bias and 300 without, placing included; long rows
+// of tokens come near the issue limit, a prompt waits for its slowest warps at the end of a chunk, and next
+// to both the latency of two kernels (8 us) shows.  Times of the whole routing: 1 x 32 4.2 us, 64 x 256 in 8 groups
+// 7.1, 1237 x 90 in 6 groups 12, 8192 x 256 in 8 groups 19, 65536 x 128 30 (700 GB/s).
 #include "common.cuh"
 #include "internal.h"
 #include "route_chunks.h"
@@ -41,8 +42,8 @@ namespace {
 constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
-// Tokens of a cluster, a warp each, 16 to a CTA.  (256 experts in 8 groups, us: 128 tokens 8.4 and, by a grid, 129
-// 10.5; with 32 to a CTA 256 tokens 12.8, by a grid 10.9.)
+// Tokens of a cluster, a warp each, 16 to a CTA.  (256 experts in 8 groups, us: 128 tokens 8.4 and, by two kernels,
+// 129 9.5; with 32 to a CTA 256 tokens 12.8, by two kernels 9.9.)
 constexpr int kClusterWarps = 16;
 constexpr int kClusterTokens = kMaxCluster * kClusterWarps;
 constexpr int kMaxE = 256;
@@ -669,15 +670,12 @@ __device__ void scan_experts(const int32_t* s_tot, int32_t* s_off, int E) {
     }
 }
 
-// perm and inv of pairs [p0, p1).  Each warp takes a run of up to kHold 32-pair strips at a time; the
-// lanes of a strip that hold the same expert are one match mask.  `ready` is called once, when the first
-// strips are counted and before the first position is written: it sets s_first[e], the sorted position of
-// the range's first pair of expert e, by then.  s_run [kMaxE] zeroed before; s_cnt: [warps][kMaxE].
+// perm and inv of pairs [p0, p1): s_base[e] is the sorted position of the range's first pair of
+// expert e.  Each warp takes a run of up to kHold 32-pair strips at a time; the lanes of a strip that
+// hold the same expert are one match mask.  s_cnt: [warps][kMaxE].
 constexpr int kHold = 4;
-template <class Ready>
-__device__ __forceinline__ void place_chunk(const RouteScoredArgs& a, int64_t p0, int64_t p1, const int32_t* s_first,
-                                            int32_t* s_run, int32_t* s_cnt, Ready ready) {
-    bool known = false;
+__device__ __forceinline__ void place_chunk(const RouteScoredArgs& a, int64_t p0, int64_t p1, int32_t* s_base,
+                                            int32_t* s_cnt) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x / 32;
     const uint32_t lt = (1u << lane) - 1u;
     int32_t* cnt = s_cnt + warp * kMaxE;
@@ -704,7 +702,7 @@ __device__ __forceinline__ void place_chunk(const RouteScoredArgs& a, int64_t p0
         }
         __syncthreads();
         for (int x = threadIdx.x; x < a.E; x += blockDim.x) {
-            int run = s_run[x];
+            int run = s_base[x];
             for (int w = 0; w < used; w += 8) {
                 int v[8];
 #pragma unroll
@@ -715,10 +713,8 @@ __device__ __forceinline__ void place_chunk(const RouteScoredArgs& a, int64_t p0
                     run += v[i];
                 }
             }
-            s_run[x] = run;
+            s_base[x] = run;
         }
-        if (!known) ready();
-        known = true;
         __syncthreads();
 #pragma unroll
         for (int s = 0; s < kHold; ++s) {
@@ -727,7 +723,7 @@ __device__ __forceinline__ void place_chunk(const RouteScoredArgs& a, int64_t p0
                 const int first = e[s] < kMaxE ? cnt[e[s]] : 0;
                 __syncwarp();
                 if (e[s] < kMaxE) {
-                    const int pos = s_first[e[s]] + first + __popc(mask[s] & lt);
+                    const int pos = first + __popc(mask[s] & lt);
                     a.perm[pos] = static_cast<int32_t>(p);
                     a.inv[p] = pos;
                     if ((mask[s] & lt) == 0) cnt[e[s]] = first + __popc(mask[s]);
@@ -737,7 +733,6 @@ __device__ __forceinline__ void place_chunk(const RouteScoredArgs& a, int64_t p0
         }
         __syncthreads();   // the counts are used up
     }
-    if (!known) ready();
 }
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -760,9 +755,9 @@ __device__ __forceinline__ int32_t ld_rank(const int32_t* p, uint32_t rank) {   
 template <bool kBf16, int NI>
 __global__ void __launch_bounds__(32 * kClusterWarps)
 route_scored_cluster_kernel(const __grid_constant__ RouteScoredArgs a) {
-    __shared__ int32_t s_hist[kMaxE], s_sum[kMaxE], s_first[kMaxE], s_run[kMaxE], s_off[kMaxE + 1];
+    __shared__ int32_t s_hist[kMaxE], s_sum[kMaxE], s_base[kMaxE], s_off[kMaxE + 1];
     __shared__ __align__(16) int32_t s_cnt[kClusterWarps * kMaxE];
-    for (int e = threadIdx.x; e < kMaxE; e += blockDim.x) s_hist[e] = s_run[e] = 0;
+    for (int e = threadIdx.x; e < kMaxE; e += blockDim.x) s_hist[e] = 0;
     __syncthreads();
     const int nb = gridDim.x, me = static_cast<int>(cluster_rank());
     const int64_t t0 = min(a.T, a.chunk * me), t1 = min(a.T, t0 + a.chunk);
@@ -779,7 +774,7 @@ route_scored_cluster_kernel(const __grid_constant__ RouteScoredArgs a) {
             before += q < me ? v[q] : 0;
         }
         s_sum[e] = tot;
-        s_first[e] = before;
+        s_base[e] = before;
     }
     __syncwarp();
     cluster_barrier();   // no CTA reads another's counts any more (and this one's sums are there)
@@ -789,68 +784,81 @@ route_scored_cluster_kernel(const __grid_constant__ RouteScoredArgs a) {
         if (me == 0) a.offsets[e] = s_off[e];
         if (e < a.E) {
             if (me == 0) a.counts[e] = s_sum[e];
-            s_first[e] += s_off[e];
+            s_base[e] += s_off[e];
         }
     }
     __syncthreads();
-    place_chunk(a, t0 * a.top_k, t1 * a.top_k, s_first, s_run, s_cnt, [] {});
+    place_chunk(a, t0 * a.top_k, t1 * a.top_k, s_base, s_cnt);
 }
 
-// The whole routing of more tokens: a chunk of them per CTA, all CTAs on the GPU at once (cooperative launch).
+// More tokens: a chunk of them per CTA, its ids and weights and a row of its pair counts.
 template <bool kBf16, int NI, int LT>
 __global__ void __launch_bounds__(kThreads)
-route_scored_grid_kernel(const __grid_constant__ RouteScoredArgs a) {
-    __shared__ int32_t s_sum[kMaxE], s_first[kMaxE], s_run[kMaxE], s_off[kMaxE + 1];
-    __shared__ __align__(16) int32_t s_cnt[kWarps * kMaxE];
+route_scored_topk_kernel(const __grid_constant__ RouteScoredArgs a) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    __shared__ int32_t s_hist[kMaxE];
+    for (int e = threadIdx.x; e < kMaxE; e += blockDim.x) s_hist[e] = 0;
+    __syncthreads();
+    const int64_t t0 = a.chunk * blockIdx.x, t1 = min(a.T, t0 + a.chunk);
+    topk_chunk<kBf16, NI, LT>(a, t0, t1, s_hist);
+    __syncthreads();
+    const int row = (a.E + 3) / 4 * 4;   // whole 16-byte vectors
+    for (int e = threadIdx.x; e < row; e += blockDim.x) a.chunk_counts[blockIdx.x * row + e] = s_hist[e];
+}
+
+// A chunk's pairs to their places, from all chunks' counts.
+__global__ void __launch_bounds__(kThreads)
+route_scored_place_kernel(const __grid_constant__ RouteScoredArgs a) {
+    // the threads in parts of kMaxE / 4, four experts per thread: part q sums chunks q, q + kParts, ...
+    __shared__ int32_t s_off[kMaxE + 1], s_base[kMaxE], s_sum[kMaxE];
+    __shared__ __align__(16) int32_t s_cnt[kWarps * kMaxE];   // first the parts' sums, then the warps' counts
+    constexpr int kParts = kThreads / (kMaxE / 4), kEach = (kMaxChunks + kParts - 1) / kParts;
+    static_assert(2 * kParts * kMaxE <= kWarps * kMaxE, "the parts' sums fit");
+    int4(*s_tot)[kMaxE / 4] = reinterpret_cast<int4(*)[kMaxE / 4]>(s_cnt);
+    int4(*s_before)[kMaxE / 4] = s_tot + kParts;
     const int nb = gridDim.x, me = blockIdx.x;
-    for (int e = threadIdx.x; e < kMaxE; e += blockDim.x) s_sum[e] = s_first[e] = s_run[e] = 0;
+    const int e4 = threadIdx.x % (kMaxE / 4), part = threadIdx.x / (kMaxE / 4), row4 = (a.E + 3) / 4;
+    asm volatile("griddepcontrol.wait;" ::: "memory");   // the chunks' counts and ids are complete
+    if (e4 < row4) {
+        int4 tot = make_int4(0, 0, 0, 0), before = tot;
+        int4 v[kEach];   // all in flight
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+            const int c = part + kParts * i;
+            v[i] = c < nb ? __ldcg(reinterpret_cast<const int4*>(a.chunk_counts) + c * row4 + e4) : make_int4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+            tot.x += v[i].x, tot.y += v[i].y, tot.z += v[i].z, tot.w += v[i].w;
+            if (part + kParts * i < me) before.x += v[i].x, before.y += v[i].y, before.z += v[i].z, before.w += v[i].w;
+        }
+        s_tot[part][e4] = tot;
+        s_before[part][e4] = before;
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
+        int tot = 0, before = 0;
+#pragma unroll
+        for (int q = 0; q < kParts; ++q) {
+            tot += reinterpret_cast<const int32_t*>(s_tot[q])[e];
+            before += reinterpret_cast<const int32_t*>(s_before[q])[e];
+        }
+        s_sum[e] = tot;
+        s_base[e] = before;
+    }
+    __syncthreads();
+    scan_experts(s_sum, s_off, a.E);
+    __syncthreads();
+    for (int e = threadIdx.x; e <= a.E; e += blockDim.x) {
+        if (me == 0) a.offsets[e] = s_off[e];
+        if (e < a.E) {
+            if (me == 0) a.counts[e] = s_sum[e];
+            s_base[e] += s_off[e];
+        }
+    }
     __syncthreads();
     const int64_t t0 = a.chunk * me, t1 = min(a.T, t0 + a.chunk);
-    topk_chunk<kBf16, NI, LT>(a, t0, t1, s_sum);
-    __syncthreads();
-    const int row4 = (a.E + 3) / 4;   // rows of whole 16-byte vectors
-    for (int e = threadIdx.x; e < 4 * row4; e += blockDim.x) {
-        a.chunk_counts[me * 4 * row4 + e] = s_sum[e];
-        s_sum[e] = 0;
-    }
-    cooperative_groups::grid_group grid = cooperative_groups::this_grid();
-    auto arrived = grid.barrier_arrive();
-    place_chunk(a, t0 * a.top_k, t1 * a.top_k, s_first, s_run, s_cnt, [&] {
-        grid.barrier_wait(std::move(arrived));   // the chunks' counts are there
-        // the threads in parts of kMaxE / 4, four experts per thread: part q sums chunks q, q + kParts, ...
-        constexpr int kParts = kThreads / (kMaxE / 4), kEach = (kMaxChunks + kParts - 1) / kParts;
-        const int e4 = threadIdx.x % (kMaxE / 4), part = threadIdx.x / (kMaxE / 4);
-        if (e4 < row4) {
-            int4 tot = make_int4(0, 0, 0, 0), before = tot;
-            int4 v[kEach];   // all in flight
-#pragma unroll
-            for (int i = 0; i < kEach; ++i) {
-                const int c = part + kParts * i;
-                v[i] = c < nb ? __ldcg(reinterpret_cast<const int4*>(a.chunk_counts) + c * row4 + e4) : make_int4(0, 0, 0, 0);
-            }
-#pragma unroll
-            for (int i = 0; i < kEach; ++i) {
-                tot.x += v[i].x, tot.y += v[i].y, tot.z += v[i].z, tot.w += v[i].w;
-                if (part + kParts * i < me) before.x += v[i].x, before.y += v[i].y, before.z += v[i].z, before.w += v[i].w;
-            }
-            const int t[4] = {tot.x, tot.y, tot.z, tot.w}, b[4] = {before.x, before.y, before.z, before.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {   // whole numbers: their order does not matter
-                if (t[i] != 0) atomicAdd(&s_sum[4 * e4 + i], t[i]);
-                if (b[i] != 0) atomicAdd(&s_first[4 * e4 + i], b[i]);
-            }
-        }
-        __syncthreads();
-        scan_experts(s_sum, s_off, a.E);
-        __syncthreads();
-        for (int e = threadIdx.x; e <= a.E; e += blockDim.x) {
-            if (me == 0) a.offsets[e] = s_off[e];
-            if (e < a.E) {
-                if (me == 0) a.counts[e] = s_sum[e];
-                s_first[e] += s_off[e];
-            }
-        }
-    });
+    place_chunk(a, t0 * a.top_k, t1 * a.top_k, s_base, s_cnt);
 }
 
 template <bool kBf16, int NI, int LT>
@@ -874,11 +882,15 @@ cudaError_t launch(RouteScoredArgs a, int sm_count, cudaStream_t stream) {
     }
     a.chunk = route_chunk(a.T, sm_count);
     const unsigned nb = static_cast<unsigned>(route_chunks(a.T, sm_count));
+    const int64_t warps = (a.chunk * LT + 31) / 32;
+    route_scored_topk_kernel<kBf16, NI, LT><<<nb, 32 * static_cast<int>(warps > kWarps ? kWarps : warps), 0, stream>>>(a);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
     cfg.gridDim = dim3(nb, 1, 1);
     cfg.blockDim = dim3(kThreads, 1, 1);
-    attr[0].id = cudaLaunchAttributeCooperative;
-    attr[0].val.cooperative = 1;
-    return cudaLaunchKernelEx(&cfg, route_scored_grid_kernel<kBf16, NI, LT>, a);
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    return cudaLaunchKernelEx(&cfg, route_scored_place_kernel, a);
 }
 
 // LT lanes to a token; items per lane rounded up to a power of two, at most 16.

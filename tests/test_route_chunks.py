@@ -1,6 +1,6 @@
-"""The CTAs that a scored routing of many tokens takes have to be on the GPU at once: on a device with fewer SMs (a
-part of one, say) there are fewer of them, with more tokens each, and the workspace of the public query still
-holds their counts."""
+"""The CTAs that a scored routing of many tokens takes run in one round: on a device with fewer SMs (a part of one,
+say) there are fewer of them, with more tokens each, and the workspace of the public query still holds their
+counts."""
 import ctypes
 import os
 import subprocess

@@ -111,3 +111,38 @@ def test_the_current_stream_itself(op):
     with torch.cuda.stream(side):
         got = call(a, side)
     assert _equal(got, want)
+
+
+def test_routing_beside_itself_on_streams_of_two_priorities():
+    """Large calls on a stream of high and one of low priority, beside linear layers that take whole SMs: no CTA of
+    a call waits for one that another call keeps off the GPU."""
+    logits, route = _route()
+    x, linear = _linear()
+    want, y = route(logits), linear(x)["y"]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(priority=0), torch.cuda.Stream(priority=-1), torch.cuda.Stream(priority=0)]
+    got = []
+    for _ in range(12):
+        got.append((route(logits, streams[0]), linear(x, streams[2])["y"], route(logits, streams[1])))
+    torch.cuda.synchronize()
+    assert mx.mxfp4_get_device_status() == 0
+    for a, z, b in got:
+        assert all(torch.equal(a[k], want[k]) and torch.equal(b[k], want[k]) for k in want)
+        assert torch.equal(z, y)
+
+
+def test_routing_beside_itself_in_one_graph():
+    logits, route = _route()
+    want = {k: v.clone() for k, v in route(logits).items()}
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        here = torch.cuda.current_stream()
+        side.wait_stream(here)
+        a = route(logits, side)
+        b = route(logits)
+        here.wait_stream(side)
+    for _ in range(4):
+        graph.replay()
+    assert _equal(a, want) and _equal(b, want)
