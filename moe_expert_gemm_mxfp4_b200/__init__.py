@@ -16,6 +16,7 @@ from __future__ import annotations
 
 import ctypes
 from functools import lru_cache
+from operator import itemgetter
 
 import torch
 
@@ -174,10 +175,6 @@ def _plain(t, dev, dtype, shape) -> bool:
     return t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous()
 
 
-def _elsewhere(stream) -> bool:
-    return stream is not None and stream != torch.cuda.current_stream()
-
-
 def _called_on(stream, call, *operands):
     """``call()`` with `stream` current, for a caller whose current stream is another one.  What the call allocates
     then comes from `stream`'s own pool: a free block of the caller's pool may still wait for the caller's kernels,
@@ -231,7 +228,7 @@ def mxfp4_linear(x: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Tensor,
     [N, K/2] + scales [N, K/32]; bias bf16 or fp32 [N]; n_out = N, or N / 2 with ACT_SWIGLU
     (W rows [0, N/2) gate, [N/2, N) up); residual bf16 [M, n_out], which may be `out`.  On another `stream` than the
     current one the caller orders the two: operands written before, results read after."""
-    if _elsewhere(stream):
+    if stream is not None and stream != torch.cuda.current_stream():
         return _called_on(stream, lambda: mxfp4_linear(x, w_codes, w_scales, bias, act, residual, out, ws),
                           x, w_codes, w_scales, bias, residual, out, ws)
     act = int(act)
@@ -334,6 +331,22 @@ def moe_mxfp4_route_scored_workspace_size(T, E, top_k) -> int:
     return int(_lib.load().moe_mxfp4_route_scored_workspace_size(T, E, top_k))
 
 
+@lru_cache(maxsize=1024)
+def _scored_layout(T, E, top_k, with_ws):
+    """The scored routing's workspace and outputs in one buffer of 4-byte elements, each on a 16-byte boundary: the
+    buffer's size, the sizes of its pieces (there are none for no padding: each costs the call half a
+    microsecond), what picks ids, weights, perm, inv, counts and offsets from them, and those six's byte offsets."""
+    P = T * top_k
+    ws = moe_mxfp4_route_scored_workspace_size(T, E, top_k) // 4 if with_ws else 0
+    pieces, places, at = [ws] if ws else [], [], []
+    for n in (P, P, P, P, E, E + 1):
+        places.append(len(pieces))
+        at.append(4 * sum(pieces))
+        pieces += [n, -n % 4] if n % 4 else [n]
+    del pieces[places[-1] + 1:]
+    return sum(pieces), pieces, itemgetter(*places), at
+
+
 def _check_scored_operands(logits, bias, ws):
     """Raise unless the scored routing's operands fit together; returns (T, E)."""
     _need_dims(logits, "logits", 2)
@@ -358,7 +371,7 @@ def moe_mxfp4_route_scored(logits: torch.Tensor, top_k: int, score: int = SCORE_
     experts' scores, renormalised to their sum if `renorm`, times `scale`.  Returns the dict
     of ``moe_mxfp4_route``.  On another `stream` than the current one the caller orders the two, as for
     ``mxfp4_linear``."""
-    if _elsewhere(stream):
+    if stream is not None and stream != torch.cuda.current_stream():
         return _called_on(stream, lambda: moe_mxfp4_route_scored(logits, top_k, score, bias, n_groups, top_groups,
                                                                  group_top, renorm, scale, ws), logits, bias, ws)
     try:
@@ -375,28 +388,22 @@ def moe_mxfp4_route_scored(logits: torch.Tensor, top_k: int, score: int = SCORE_
     top_k = int(top_k)
     if top_k < 1:
         raise ValueError(f"top_k: expected at least 1, got {top_k}")
-    # one allocation for the workspace and the outputs, each on a 16-byte boundary: seven took half the call,
-    # and every piece of it that becomes a tensor takes a microsecond
-    P = T * top_k
-    need = 0 if ws is not None else moe_mxfp4_route_scored_workspace_size(T, E, top_k)
-    pad_p, pad_e, skip = -P % 4, -E % 4, need // 4
-    buf = logits.new_empty((skip + 4 * (P + pad_p) + 2 * E + 1 + pad_e,), dtype=torch.int32)
-    if skip or pad_p or pad_e:
-        _, ids, _, weights, _, perm, _, inv, _, counts, _, offsets = buf.split_with_sizes(
-            (skip, P, pad_p, P, pad_p, P, pad_p, P, pad_p, E, pad_e, E + 1))
-    else:
-        ids, weights, perm, inv, counts, offsets = buf.split_with_sizes((P, P, P, P, E, E + 1))
-    out = dict(ids=ids.view(T, top_k), weights=weights.view(torch.float32).view(T, top_k), counts=counts,
-               offsets=offsets, perm=perm, inv=inv)
+    # one allocation for the workspace and the outputs, each on a 16-byte boundary: seven took half the call
+    size, pieces, six, (at_ids, at_weights, at_perm, at_inv, at_counts, at_offsets) = _scored_layout(T, E, top_k, ws is None)
+    buf = logits.new_empty((size,), dtype=torch.int32)
+    base = buf.data_ptr()
     if ws is not None:
         space, nbytes = ws.data_ptr(), ws.numel() * ws.element_size()
-    else:
-        space, nbytes = buf.data_ptr() if need else None, need
+    else:   # in front of the outputs
+        nbytes = at_ids
+        space = base if nbytes else None
     _lib.check("moe_mxfp4_route_scored", lib.moe_mxfp4_route_scored(
         logits.data_ptr(), dt, T, E, top_k, int(score), None if bias is None else bias.data_ptr(), int(n_groups),
-        int(top_groups), int(group_top), int(bool(renorm)), float(scale), ids.data_ptr(), weights.data_ptr(),
-        counts.data_ptr(), offsets.data_ptr(), perm.data_ptr(), inv.data_ptr(), space, nbytes, _stream(stream)))
-    return out
+        int(top_groups), int(group_top), int(bool(renorm)), float(scale), base + at_ids, base + at_weights,
+        base + at_counts, base + at_offsets, base + at_perm, base + at_inv, space, nbytes, _stream(stream)))
+    ids, weights, perm, inv, counts, offsets = six(buf.unsafe_split_with_sizes(pieces))
+    return dict(ids=ids.view(T, top_k), weights=weights.view(torch.float32).view(T, top_k), counts=counts,
+                offsets=offsets, perm=perm, inv=inv)
 
 
 def mxfp4_gather_rows(src: torch.Tensor, idx: torch.Tensor, div: int = 1, out=None, stream=None):
