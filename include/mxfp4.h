@@ -134,7 +134,8 @@ MXFP4_API int32_t mxfp4_token_tile_rows(int64_t rows, int64_t groups, mxfp4_mode
  *   bias    [N] in bf16 or fp32 per `bias_dt`, or NULL;
  *   residual bf16 [M, n_out], or NULL; it may be y itself (the sum in place).  Else y overlaps
  *           neither it nor x (MXFP4_ERR_INVALID_ARG).
- * Inf and NaN in x, in a block scale (0xFF), bias or residual spread as in the formula.
+ * Inf and NaN in x, in a block scale (0xFF), bias or residual spread as in the formula.  Up to some hundreds
+ * of tokens an output whose sum is not finite costs a serial sum over K: milliseconds, if a call holds many.
  * A weight is its code times 2^(S-127); where that is past bf16's range (S > 252) it may
  * enter the product as Inf or as the exact value.
  * Requires K % 32 == 0, K <= 2^20, M and N <= 2^30, N * K <= 2^40 and M * n_out <= 2^46; any M >= 1, N >= 1.  ws:
@@ -213,7 +214,8 @@ MXFP4_API size_t moe_mxfp4_route_workspace_size(int64_t T, int64_t E, int32_t to
  * groups have nothing better; a score below the smallest 64-bit number is 0, and a token
  * whose chosen scores are all 0 gets weights 0.  A NaN
  * logit takes no part in the softmax of the others, and its c (like a NaN bias's) ranks below -inf;
- * a token that has to choose a NaN logit gets NaN there (with renorm in all its slots).
+ * a token that has to choose a NaN logit gets NaN there (with renorm in all its slots).  Without
+ * renorm, a score below 2^-126 may weigh 0.
  * ids, counts, offsets, perm, inv as moe_mxfp4_route (pairs p = t * top_k + j).
  * Requires 1 <= top_k <= 8, E <= 256, n_groups <= 32, E % n_groups == 0, group_top 1 or 2
  * and at most E / n_groups, 1 <= top_groups <= n_groups, top_k <= top_groups * E /

@@ -46,7 +46,7 @@ struct RouteScoredArgs {
     int32_t* offsets;          // [E + 1]
     int32_t* perm;             // [T * top_k]
     int32_t* inv;              // [T * top_k]
-    int32_t* chunk_counts;     // scratch [chunks, E]
+    int32_t* chunk_counts;     // scratch [chunks, E rounded up to a multiple of 4]
     int64_t T;
     int E, top_k, score, n_groups, top_groups, group_top, renorm;
     int by_logit;              // the choice goes by the logits (no bias, no sums of scores)

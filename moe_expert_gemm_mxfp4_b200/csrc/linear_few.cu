@@ -29,9 +29,10 @@
 // run); each finishes a share of the tokens.
 //
 // What bounds it: up to a hundred tokens neither bytes nor MMAs but the chain of a launch (set-up, the first
-// codes, the spreading of a stage, the cluster's sums): 1 x 2880 x 2880 7.8 us (0.7 at the copy bandwidth),
-// 64 x 2880 x 5760 gated 13.0 (1.5); with long weights the spreading, 32 x 7680 x 11520 29 us (1.7 TB/s); with
-// several token tiles the MMAs (of both parts) and the finish, 512 x 2880 x 2880 18.4 us (462 TFLOP/s).
+// codes, the spreading of a stage, the cluster's sums): 1 x 2880 x 2880 7.5 to 7.9 us (0.7 at the copy bandwidth),
+// 64 x 2880 x 5760 gated 12.8 (1.5); with long weights the spreading, 32 x 7680 x 11520 28 us (1.7 TB/s); with
+// several token tiles the MMAs (of both parts) and the finish, 512 x 2880 x 2880 18.3 us (464 TFLOP/s; with
+// SiLU 20).
 //
 // hi and lo rows lie next to each other in one MMA of N = 2 Mp columns while that fits the 128
 // rows of a scale atom (an MMA of N <= 64 costs the same whatever its N), else they are
@@ -703,8 +704,10 @@ Plan make_plan(int64_t M, int64_t K, int64_t n_out, bool gated) {
 // its weights again: 6 + 0.0036 K.  The other one dequantizes them once, 2.5 bytes a weight, and its
 // longest pair takes 1 ns per unit of its plan's cost and stage.  One token tile is always sooner here.
 // (Here and there, us: 2880 x 2880, 384 tokens 17 and 21, 512 19 and 21; 5760 x 2880 gated, 336 20 and 24,
-// 384 34 and 25; 11520 x 7680, 112 37 and 82, 256 66 and 83, 384 97 and 106, 512 133 and 107.)  The prepare
-// kernel keeps 32 rows of block scales in shared memory, which bounds K.
+// 384 34 and 25; 11520 x 7680, 112 37 and 82, 256 66 and 83, 384 97 and 106, 512 133 and 107.)
+// K ends at 8192 because the fit does: longer ones were not measured here.  Nothing else asks for that bound (the
+// prepare kernel's 32 rows of block scales fill its shared memory at K = 49000), and the other engine
+// dequantizes all of W for the few tokens of such a call.
 bool linear_is_few(int64_t M, int64_t K, int64_t n_out, bool gated) {
     const int64_t t = (M + kMaxMp - 1) / kMaxMp, f = gated ? 64 : kBM, w = (n_out + f - 1) / f;
     if (K > 8192) return false;

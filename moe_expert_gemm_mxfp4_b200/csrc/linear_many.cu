@@ -17,8 +17,8 @@
 // What bounds it: the MMAs of a stage (4 nt cycles) where nt = 256 and the power limit; below that
 // the copies, about 47 bytes per cycle and SM from L2, so that a tile costs as 256 + nt.
 //
-// Measured with the weights' pass: 8192 x 2880 x 5760 gated 169 us (1609 TFLOP/s), 8192 x 2880 x 2880 100 to 114
-// (1340 to 1190, residual and all), 2048 x 7680 x 2880 76 (1195; the pass takes 12 of them).  Eight more warps that
+// Measured with the weights' pass: 8192 x 2880 x 5760 gated 169 us (1609 TFLOP/s), 8192 x 2880 x 2880 100 to 121
+// (1350 to 1120, residual and all), 2048 x 7680 x 2880 77 with residual (1175) and 75 without; the pass takes 12 of them.  Eight more warps that
 // dequantize into shared memory inside the product, so that the pass goes, took 274, 172 and 141.
 //
 // Roles in each CTA (12 warps): warp 0 producer (its own half of both tiles; completion is

@@ -27,9 +27,9 @@
 // against 12.0, 65536 x 128 29.8 and 29.8.)
 //
 // What bounds it: the bytes are few (8192 x 256 fp32: 1.4 us at the copy bandwidth, 65536 x 128 bf16: 3.2).  A
-// token takes some 1100 warp instructions with groups and a bias and 300 without, placing included; long rows
-// of tokens come near the issue limit, a prompt waits for its slowest warps at the end of a chunk, and next
-// to both the latency of two kernels (8 us) shows.  Times of the whole routing: 1 x 32 4.2 us, 64 x 256 in 8 groups
+// token takes some 720 warp instructions with groups and a bias and 260 without, and 30 to 290 more to place its
+// pairs.  65536 tokens issue in 70% of the first kernel's cycles; 8192 in 51%, and the SMs are at work in 64% of the
+// time only: what two launches and the last warps of each chunk leave open (counters of both kernels).  Times of the whole routing: 1 x 32 4.2 us, 64 x 256 in 8 groups
 // 7.1, 1237 x 90 in 6 groups 12, 8192 x 256 in 8 groups 19, 65536 x 128 30 (700 GB/s).
 #include "common.cuh"
 #include "internal.h"
